@@ -6,9 +6,11 @@ loudly; there is no other implementation behind these names.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdm05_suffix_attn.so")
@@ -33,7 +35,9 @@ EXPORTS = ("dm05_suffix_attn", "dm05_suffix_attn_ex", "dm05_suffix_attn_workspac
            "dm05_suffix_attn_host_copy_bytes", "dm05_selftest_wait_timeout", "dm05_prefix_prefill_attn",
            "dm05_prefix_prefill_reserve", "dm05_prefix_prefill_plan", "dm05_suffix_qkv_prologue",
            "dm05_suffix_attn_steps_create", "dm05_suffix_attn_steps_launch", "dm05_suffix_attn_steps_destroy",
-           "dm05_post_attention", "dm05_post_attention_reserve")
+           "dm05_post_attention", "dm05_post_attention_reserve", "dm05_kv8_quantize", "dm05_suffix_attn_kv8",
+           "dm05_suffix_attn_kv8_plan", "dm05_prefix_attn_mass", "dm05_prefix_attn_mass_kv8", "dm05_prefix_evict",
+           "dm05_prefix_evict_kv8")
 
 _lock = threading.Lock()
 _lib = None
@@ -109,6 +113,20 @@ def lib() -> ctypes.CDLL:
             L.dm05_post_attention.restype = i
             L.dm05_post_attention_reserve.argtypes = [i] * 6 + [p]
             L.dm05_post_attention_reserve.restype = i
+            L.dm05_kv8_quantize.argtypes = [p] * 7 + [i] * 6 + [p]
+            L.dm05_kv8_quantize.restype = i
+            L.dm05_suffix_attn_kv8.argtypes = [p] * 5 + [i] + [p] * 7 + [sz] + [i] * 6 + [p]
+            L.dm05_suffix_attn_kv8.restype = i
+            L.dm05_suffix_attn_kv8_plan.argtypes = [i] * 6 + [ctypes.POINTER(i)] * 3 + [ctypes.POINTER(sz)]
+            L.dm05_suffix_attn_kv8_plan.restype = i
+            L.dm05_prefix_attn_mass.argtypes = [p] * 7 + [i] * 6 + [p]
+            L.dm05_prefix_attn_mass.restype = i
+            L.dm05_prefix_attn_mass_kv8.argtypes = [p] * 3 + [i] + [p] * 5 + [i] * 6 + [p]
+            L.dm05_prefix_attn_mass_kv8.restype = i
+            L.dm05_prefix_evict.argtypes = [p] * 10 + [i] * 8 + [p]
+            L.dm05_prefix_evict.restype = i
+            L.dm05_prefix_evict_kv8.argtypes = [p] * 4 + [i] + [p] * 10 + [i] * 8 + [p]
+            L.dm05_prefix_evict_kv8.restype = i
             _lib = L
     return _lib
 
@@ -202,6 +220,56 @@ def dm05_post_attention(attn, h, scale, shift, gate, wo, wgu, wd, out, B, S, Hq,
 
 def dm05_post_attention_reserve(B, S, Hq, D, Hd, F, stream) -> int:
     return lib().dm05_post_attention_reserve(B, S, Hq, D, Hd, F, stream)
+
+
+def dm05_kv8_quantize(k, v, valid_len, k8, v8, k_scale, v_scale, B, Hkv, P, D, block, first, stream) -> int:
+    """The 8-bit form (e4m3 codes, a scale per block of tokens and KV head) of a prefix cache."""
+    return lib().dm05_kv8_quantize(k, v, valid_len, k8, v8, k_scale, v_scale, B, Hkv, P, D, block, first, stream)
+
+
+def dm05_suffix_attn_kv8(q, k8, v8, k_scale, v_scale, block, prefix_valid_len, prefix_mask, k_suffix, v_suffix, out,
+                         lse, workspace, workspace_bytes, B, Hq, Hkv, P, S, D, stream) -> int:
+    """The suffix attention over an 8-bit prefix cache."""
+    return lib().dm05_suffix_attn_kv8(q, k8, v8, k_scale, v_scale, block, prefix_valid_len, prefix_mask, k_suffix,
+                                      v_suffix, out, lse, workspace, workspace_bytes, B, Hq, Hkv, P, S, D, stream)
+
+
+def dm05_suffix_attn_kv8_plan(B, Hq, Hkv, P, S, D):
+    """Returns (status, splits_per_head, tile_rows, row_blocks, workspace_bytes)."""
+    sp, tr, rb, ws = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
+    rc = lib().dm05_suffix_attn_kv8_plan(B, Hq, Hkv, P, S, D, ctypes.byref(sp), ctypes.byref(tr), ctypes.byref(rb),
+                                         ctypes.byref(ws))
+    return rc, sp.value, tr.value, rb.value, ws.value
+
+
+def dm05_prefix_attn_mass(q, k_prefix, prefix_valid_len, prefix_mask, lse, mass_in, mass, B, Hq, Hkv, P, S, D,
+                          stream) -> int:
+    """The attention weight each prefix position received, from a bf16 cache."""
+    return lib().dm05_prefix_attn_mass(q, k_prefix, prefix_valid_len, prefix_mask, lse, mass_in, mass, B, Hq, Hkv, P,
+                                       S, D, stream)
+
+
+def dm05_prefix_attn_mass_kv8(q, k8, k_scale, block, prefix_valid_len, prefix_mask, lse, mass_in, mass, B, Hq, Hkv,
+                              P, S, D, stream) -> int:
+    """The same from an 8-bit cache."""
+    return lib().dm05_prefix_attn_mass_kv8(q, k8, k_scale, block, prefix_valid_len, prefix_mask, lse, mass_in, mass,
+                                           B, Hq, Hkv, P, S, D, stream)
+
+
+def dm05_prefix_evict(k, v, mass, valid_len, mask, k_out, v_out, mass_out, positions, valid_out, B, Hkv, P, P_out, D,
+                      n_keep, n_first, n_last, stream) -> int:
+    """Keeps the positions of largest mass in a smaller bf16 cache."""
+    return lib().dm05_prefix_evict(k, v, mass, valid_len, mask, k_out, v_out, mass_out, positions, valid_out, B, Hkv,
+                                   P, P_out, D, n_keep, n_first, n_last, stream)
+
+
+def dm05_prefix_evict_kv8(k8, v8, k_scale, v_scale, block, mass, valid_len, mask, k8_out, v8_out, k_scale_out,
+                          v_scale_out, mass_out, positions, valid_out, B, Hkv, P, P_out, D, n_keep, n_first, n_last,
+                          stream) -> int:
+    """The same on an 8-bit cache."""
+    return lib().dm05_prefix_evict_kv8(k8, v8, k_scale, v_scale, block, mass, valid_len, mask, k8_out, v8_out,
+                                       k_scale_out, v_scale_out, mass_out, positions, valid_out, B, Hkv, P, P_out, D,
+                                       n_keep, n_first, n_last, stream)
 
 
 def post_attention(attn, h, scale, shift, gate, wo, wgu, wd, eps=1e-6, out=None, stream=None):
@@ -443,3 +511,321 @@ def reserve_for(q, k_prefix, stream=None) -> None:
     rc = dm05_suffix_attn_reserve(B, Hq, k_prefix.shape[1], k_prefix.shape[2], S, D, _stream_handle(stream))
     if rc != DM05_OK:
         raise Dm05Error(rc, "dm05_suffix_attn_reserve")
+
+
+# ---- prefix-cache compression -----------------------------------------------
+
+class Kv8Cache(NamedTuple):
+    """A prefix cache held in 8 bits: row j of k stands for
+    k_scale[..., j // block] * k[..., j, :], and the same for v.
+
+    k, v: float8_e4m3fn [B, Hkv, P, D]; k_scale, v_scale: fp32
+    [B, Hkv, ceil(P / block)]; block: 16, 32, 64 or 128 positions."""
+    k: "torch.Tensor"
+    v: "torch.Tensor"
+    k_scale: "torch.Tensor"
+    v_scale: "torch.Tensor"
+    block: int
+
+
+class EvictedPrefix(NamedTuple):
+    """What prefix_evict keeps: the smaller cache, the kept positions' mass
+    (fp32 [B, Hkv, P_out], 0 behind the kept rows), where each row came from
+    (int32 [B, Hkv, P_out], -1 behind them) and its valid lengths (int32 [B])."""
+    k: "torch.Tensor"
+    v: "torch.Tensor"
+    mass: "torch.Tensor"
+    positions: "torch.Tensor"
+    valid_len: "torch.Tensor"
+
+
+class EvictedPrefixKv8(NamedTuple):
+    """The same for an 8-bit cache."""
+    cache: Kv8Cache
+    mass: "torch.Tensor"
+    positions: "torch.Tensor"
+    valid_len: "torch.Tensor"
+
+
+def _need(name, t, dtype, shape, device):
+    """A dense CUDA tensor of this type and shape on `device`, or ValueError."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {list(shape)} on {device}")
+
+
+def _need_prefix(valid_len, mask, B, P, device):
+    import torch
+    if valid_len is not None:
+        _need("prefix_valid_len", valid_len, torch.int32, (B,), device)
+    if mask is not None:
+        _need("prefix_mask", mask, torch.uint8, (B, P), device)
+
+
+def _need_cache(name, cache, device=None):
+    """Checks an 8-bit cache; returns its (B, Hkv, P, D)."""
+    import torch
+    if cache.k.dim() != 4:
+        raise ValueError(f"{name}.k must be [B,Hkv,P,D]")
+    B, Hkv, P, D = cache.k.shape
+    if cache.block not in (16, 32, 64, 128):
+        raise ValueError(f"{name}.block must be 16, 32, 64 or 128")
+    device = cache.k.device if device is None else device
+    scales = (B, Hkv, -(-P // cache.block))
+    _need(f"{name}.k", cache.k, torch.float8_e4m3fn, (B, Hkv, P, D), device)
+    _need(f"{name}.v", cache.v, torch.float8_e4m3fn, (B, Hkv, P, D), device)
+    _need(f"{name}.k_scale", cache.k_scale, torch.float32, scales, device)
+    _need(f"{name}.v_scale", cache.v_scale, torch.float32, scales, device)
+    return B, Hkv, P, D
+
+
+@contextlib.contextmanager
+def _other_device_or_stream(device, stream):
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            h = int(stream)
+            stream = torch.cuda.ExternalStream(h, device=device) if h else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device} like the tensors")
+        with torch.cuda.stream(stream):  # what is allocated here belongs to that stream
+            yield stream.cuda_stream
+
+
+def _on(device, stream):
+    """Context in which the library is called: the tensors' device current,
+    new tensors allocated for `stream`; yields the stream's handle."""
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext(torch.cuda.current_stream().cuda_stream)
+    return _other_device_or_stream(device, stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kv8_quantize(k, v, block: int = 64, valid_len=None, first: int = 0, out: Optional[Kv8Cache] = None, stream=None):
+    """The 8-bit form of a bf16 prefix cache [B,Hkv,P,D]; returns the Kv8Cache.
+
+    Rows [first, valid_len) are written (first a multiple of the block, for a
+    prefix that is quantised in pieces); a fresh cache has zero codes and unit
+    scales elsewhere.  With `out` given, its block is used and everything else
+    in it is left as it was."""
+    import torch
+    if k.dim() != 4:
+        raise ValueError("k must be [B,Hkv,P,D]")
+    B, Hkv, P, D = k.shape
+    dev = k.device
+    _need("k", k, torch.bfloat16, (B, Hkv, P, D), dev)
+    _need("v", v, torch.bfloat16, (B, Hkv, P, D), dev)
+    if valid_len is not None:
+        _need("valid_len", valid_len, torch.int32, (B,), dev)
+    if out is not None and _need_cache("out", out, dev) != (B, Hkv, P, D):
+        raise ValueError("out must be a cache of k's sizes")
+    if out is None and block not in (16, 32, 64, 128):
+        raise ValueError("block must be 16, 32, 64 or 128")
+    with _on(dev, stream) as s:
+        if out is None:
+            codes = lambda: torch.zeros((B, Hkv, P, D), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)  # noqa: E731
+            ones = lambda: torch.ones((B, Hkv, -(-P // block)), dtype=torch.float32, device=dev)  # noqa: E731
+            out = Kv8Cache(codes(), codes(), ones(), ones(), block)
+        rc = dm05_kv8_quantize(k.data_ptr(), v.data_ptr(), _ptr(valid_len), out.k.data_ptr(), out.v.data_ptr(),
+                               out.k_scale.data_ptr(), out.v_scale.data_ptr(), B, Hkv, P, D, out.block, first, s)
+    if rc != DM05_OK:
+        raise Dm05Error(rc, "dm05_kv8_quantize")
+    return out
+
+
+def suffix_attn_kv8(q, cache: Kv8Cache, k_suffix, v_suffix, prefix_valid_len=None, prefix_mask=None, out=None,
+                    lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Suffix attention over an 8-bit prefix cache; returns (out, lse or None).
+
+    As suffix_attn, with the prefix in a Kv8Cache.  workspace: a contiguous
+    uint8 CUDA tensor of at least dm05_suffix_attn_kv8_plan's bytes that no
+    call running at the same time uses; allocated for the call when not given."""
+    import torch
+    if q.dim() != 4:
+        raise ValueError("q must be [B,Hq,S,D]")
+    B, Hq, S, D = q.shape
+    dev = q.device
+    bf = torch.bfloat16
+    _need("q", q, bf, (B, Hq, S, D), dev)
+    Bc, Hkv, P, Dc = _need_cache("cache", cache, dev)
+    if Bc != B or Dc != D:
+        raise ValueError("cache must have q's batch and head size")
+    _need("k_suffix", k_suffix, bf, (B, Hkv, S, D), dev)
+    _need("v_suffix", v_suffix, bf, (B, Hkv, S, D), dev)
+    _need_prefix(prefix_valid_len, prefix_mask, B, P, dev)
+    if out is not None:
+        _need("out", out, bf, (B, Hq, S, D), dev)
+    if lse is not None:
+        _need("lse", lse, torch.float32, (B, Hq, S), dev)
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous CUDA uint8 tensor on {dev}")
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((B, Hq, S, D), dtype=bf, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq, S), dtype=torch.float32, device=dev)
+        if workspace is None:
+            rc, _, _, _, need = dm05_suffix_attn_kv8_plan(B, Hq, Hkv, P, S, D)
+            if rc != DM05_OK:
+                raise Dm05Error(rc, "dm05_suffix_attn_kv8")
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = dm05_suffix_attn_kv8(q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+                                  cache.v_scale.data_ptr(), cache.block, _ptr(prefix_valid_len), _ptr(prefix_mask),
+                                  k_suffix.data_ptr(), v_suffix.data_ptr(), out.data_ptr(), _ptr(lse),
+                                  _ptr(workspace), 0 if workspace is None else workspace.numel(), B, Hq, Hkv, P, S, D,
+                                  s)
+    if rc != DM05_OK:
+        raise Dm05Error(rc, "dm05_suffix_attn_kv8")
+    return out, lse
+
+
+def _mass(q, k, k_scale, block, lse, valid_len, mask, mass_in, mass, stream):
+    import torch
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,Hq,S,D] and the keys [B,Hkv,P,D]")
+    B, Hq, S, D = q.shape
+    Hkv, P = k.shape[1], k.shape[2]
+    dev = q.device
+    _need("q", q, torch.bfloat16, (B, Hq, S, D), dev)
+    if k_scale is None:
+        _need("k_prefix", k, torch.bfloat16, (B, Hkv, P, D), dev)
+    else:
+        if block not in (16, 32, 64, 128):
+            raise ValueError("block must be 16, 32, 64 or 128")
+        _need("k8", k, torch.float8_e4m3fn, (B, Hkv, P, D), dev)
+        _need("k_scale", k_scale, torch.float32, (B, Hkv, -(-P // block)), dev)
+    _need("lse", lse, torch.float32, (B, Hq, S), dev)
+    _need_prefix(valid_len, mask, B, P, dev)
+    if mass_in is not None:
+        _need("mass_in", mass_in, torch.float32, (B, Hkv, P), dev)
+    if mass is not None:
+        _need("mass", mass, torch.float32, (B, Hkv, P), dev)
+    with _on(dev, stream) as s:
+        if mass is None:
+            mass = torch.empty((B, Hkv, P), dtype=torch.float32, device=dev)
+        if k_scale is None:
+            rc = dm05_prefix_attn_mass(q.data_ptr(), k.data_ptr(), _ptr(valid_len), _ptr(mask), lse.data_ptr(),
+                                       _ptr(mass_in), mass.data_ptr(), B, Hq, Hkv, P, S, D, s)
+        else:
+            rc = dm05_prefix_attn_mass_kv8(q.data_ptr(), k.data_ptr(), k_scale.data_ptr(), block, _ptr(valid_len),
+                                           _ptr(mask), lse.data_ptr(), _ptr(mass_in), mass.data_ptr(), B, Hq, Hkv, P,
+                                           S, D, s)
+    if rc != DM05_OK:
+        raise Dm05Error(rc, "dm05_prefix_attn_mass")
+    return mass
+
+
+def prefix_attn_mass(q, k_prefix, lse, prefix_valid_len=None, prefix_mask=None, mass_in=None, mass=None, stream=None):
+    """The attention weight that each prefix position received in a
+    suffix_attn call with this q, lse and masks, summed over the queries of
+    each KV head and added to mass_in; returns fp32 [B,Hkv,P] (`mass`, which
+    may be mass_in itself, when given)."""
+    return _mass(q, k_prefix, None, 0, lse, prefix_valid_len, prefix_mask, mass_in, mass, stream)
+
+
+def prefix_attn_mass_kv8(q, k8, k_scale, block, lse, prefix_valid_len=None, prefix_mask=None, mass_in=None, mass=None,
+                         stream=None):
+    """prefix_attn_mass over the keys of an 8-bit cache (its k, k_scale and block)."""
+    if k_scale is None:
+        raise ValueError("k_scale must be given")
+    return _mass(q, k8, k_scale, block, lse, prefix_valid_len, prefix_mask, mass_in, mass, stream)
+
+
+def _need_evicted(mass, B, Hkv, P, P_out, valid_len_in, mask, mass_out, positions, valid_len, dev):
+    import torch
+    _need("mass", mass, torch.float32, (B, Hkv, P), dev)
+    _need_prefix(valid_len_in, mask, B, P, dev)
+    if mass_out is not None:
+        _need("mass_out", mass_out, torch.float32, (B, Hkv, P_out), dev)
+    if positions is not None:
+        _need("positions", positions, torch.int32, (B, Hkv, P_out), dev)
+    if valid_len is not None:
+        _need("valid_len", valid_len, torch.int32, (B,), dev)
+
+
+def _evict_outputs(B, Hkv, P_out, mass_out, positions, valid_len, dev):
+    import torch
+    if mass_out is None:
+        mass_out = torch.empty((B, Hkv, P_out), dtype=torch.float32, device=dev)
+    if positions is None:
+        positions = torch.empty((B, Hkv, P_out), dtype=torch.int32, device=dev)
+    if valid_len is None:
+        valid_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    return mass_out, positions, valid_len
+
+
+def prefix_evict(k, v, mass, n_keep: int, n_first: int = 0, n_last: int = 0, prefix_valid_len=None, prefix_mask=None,
+                 bucket: Optional[int] = None, k_out=None, v_out=None, mass_out=None, positions=None, valid_len=None,
+                 stream=None) -> EvictedPrefix:
+    """Keeps the n_keep visible positions of largest mass per (sample, KV
+    head), the first n_first and the last n_last in range before all others,
+    in a cache of `bucket` rows (n_keep, or k_out's, when not given).  Fresh
+    outputs hold zeros behind the kept rows; given ones keep what they held
+    there."""
+    import torch
+    if k.dim() != 4:
+        raise ValueError("k must be [B,Hkv,P,D]")
+    B, Hkv, P, D = k.shape
+    dev = k.device
+    bf = torch.bfloat16
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out must be given together")
+    if k_out is not None and k_out.dim() == 4 and bucket is None:
+        bucket = k_out.shape[2]
+    bucket = n_keep if bucket is None else bucket
+    _need("k", k, bf, (B, Hkv, P, D), dev)
+    _need("v", v, bf, (B, Hkv, P, D), dev)
+    if k_out is not None:
+        _need("k_out", k_out, bf, (B, Hkv, bucket, D), dev)
+        _need("v_out", v_out, bf, (B, Hkv, bucket, D), dev)
+    _need_evicted(mass, B, Hkv, P, bucket, prefix_valid_len, prefix_mask, mass_out, positions, valid_len, dev)
+    with _on(dev, stream) as s:
+        if k_out is None:
+            k_out = torch.zeros((B, Hkv, bucket, D), dtype=bf, device=dev)
+            v_out = torch.zeros((B, Hkv, bucket, D), dtype=bf, device=dev)
+        mass_out, positions, valid_len = _evict_outputs(B, Hkv, bucket, mass_out, positions, valid_len, dev)
+        rc = dm05_prefix_evict(k.data_ptr(), v.data_ptr(), mass.data_ptr(), _ptr(prefix_valid_len), _ptr(prefix_mask),
+                               k_out.data_ptr(), v_out.data_ptr(), mass_out.data_ptr(), positions.data_ptr(),
+                               valid_len.data_ptr(), B, Hkv, P, bucket, D, n_keep, n_first, n_last, s)
+    if rc != DM05_OK:
+        raise Dm05Error(rc, "dm05_prefix_evict")
+    return EvictedPrefix(k_out, v_out, mass_out, positions, valid_len)
+
+
+def prefix_evict_kv8(cache: Kv8Cache, mass, n_keep: int, n_first: int = 0, n_last: int = 0, prefix_valid_len=None,
+                     prefix_mask=None, bucket: Optional[int] = None, out: Optional[Kv8Cache] = None, mass_out=None,
+                     positions=None, valid_len=None, stream=None) -> EvictedPrefixKv8:
+    """prefix_evict on an 8-bit cache: the kept rows form blocks of the same
+    size with scales of their own (a fresh `out` has zero codes and unit
+    scales behind them)."""
+    import torch
+    B, Hkv, P, D = _need_cache("cache", cache)
+    dev = cache.k.device
+    if out is not None and bucket is None and out.k.dim() == 4:
+        bucket = out.k.shape[2]
+    bucket = n_keep if bucket is None else bucket
+    if out is not None and (_need_cache("out", out, dev) != (B, Hkv, bucket, D) or out.block != cache.block):
+        raise ValueError(f"out must be a cache of {bucket} rows with cache's other sizes and block")
+    _need_evicted(mass, B, Hkv, P, bucket, prefix_valid_len, prefix_mask, mass_out, positions, valid_len, dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            codes = lambda: torch.zeros((B, Hkv, bucket, D), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)  # noqa: E731
+            ones = lambda: torch.ones((B, Hkv, -(-bucket // cache.block)), dtype=torch.float32, device=dev)  # noqa: E731
+            out = Kv8Cache(codes(), codes(), ones(), ones(), cache.block)
+        mass_out, positions, valid_len = _evict_outputs(B, Hkv, bucket, mass_out, positions, valid_len, dev)
+        rc = dm05_prefix_evict_kv8(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+                                   cache.v_scale.data_ptr(), cache.block, mass.data_ptr(), _ptr(prefix_valid_len),
+                                   _ptr(prefix_mask), out.k.data_ptr(), out.v.data_ptr(), out.k_scale.data_ptr(),
+                                   out.v_scale.data_ptr(), mass_out.data_ptr(), positions.data_ptr(),
+                                   valid_len.data_ptr(), B, Hkv, P, bucket, D, n_keep, n_first, n_last, s)
+    if rc != DM05_OK:
+        raise Dm05Error(rc, "dm05_prefix_evict_kv8")
+    return EvictedPrefixKv8(out, mass_out, positions, valid_len)

@@ -7,7 +7,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libdm05_suffix_attn.so")
-SOURCES = [os.path.join(HERE, "csrc", "dm05_suffix_attn.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("dm05_suffix_attn.cu", "prefix_cache.cu")]
 
 
 def deps() -> list:

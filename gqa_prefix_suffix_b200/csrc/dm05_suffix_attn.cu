@@ -17,6 +17,7 @@
 #include <thread>
 #include <vector>
 
+#include "dm05_internal.h"
 #include "post_attn_kernels.cuh"
 #include "qkv_prologue_kernel.cuh"
 #include "suffix_attn_kernel.cuh"
@@ -1642,3 +1643,47 @@ void release_post_buffers()
     }
     g_post_ws.clear();
 }
+
+// ---------------------------------------------------------------------------
+// What the library's other translation units use (dm05_internal.h).
+namespace dm05 {
+namespace internal {
+
+int device(cudaStream_t stream, bool need_err, Device *out) noexcept
+{
+    try {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (get_encoder() != DM05_OK) return DM05_ERR_CUDA;
+        DeviceState *ds = nullptr;
+        int rc = device_state(false, &ds);
+        if (rc != DM05_OK) return rc;
+        if (need_err && ds->err == nullptr) {
+            cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+            if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) return DM05_ERR_CUDA;
+            if (cs != cudaStreamCaptureStatusNone) return DM05_ERR_WORKSPACE;
+            rc = device_state(true, &ds, stream);
+            if (rc != DM05_OK) return rc;
+        }
+        out->err = ds->err;
+        out->num_sms = ds->num_sms;
+        out->split_override = g_split_override;
+        out->row_block_override = g_row_block_override;
+        out->ordinal = static_cast<int>(ds - g_dev.data());
+        return DM05_OK;
+    } catch (...) {
+        return DM05_ERR_CUDA;  // no exception crosses the C boundary
+    }
+}
+
+int encode_tiled(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
+                 const cuuint64_t *strides, const cuuint32_t *box) noexcept
+{
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const CUresult r = g_encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DM05_OK : DM05_ERR_CUDA;
+}
+
+}  // namespace internal
+}  // namespace dm05

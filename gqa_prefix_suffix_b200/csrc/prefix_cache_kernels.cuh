@@ -1,0 +1,411 @@
+// prefix_cache_kernels.cuh -- sm_100a kernels that fill and shrink the prefix
+// KV cache: the 8-bit quantiser and the eviction (selection, then a gather
+// of the kept rows).
+//
+// The 8-bit cache holds e4m3 codes [B, Hkv, P, 256] and, for K and for V, one
+// fp32 scale for each block of `block` consecutive rows of a KV head:
+// row j stands for scale[j / block] * code[j].  The quantiser writes powers
+// of two: e4m3 is a floating format, so a finer scale would not make the
+// codes more exact (the relative step is 2^-4 at any scale), and with a power
+// of two the division and the product back are exact, the value fits bf16
+// unrounded, and codes move between blocks (eviction) without a second
+// rounding unless they fall below the new block's smallest step.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "suffix_attn_kernel.cuh"
+
+namespace dm05 {
+namespace cache {
+
+constexpr int kRowBytes8 = kHeadDim;         // one 8-bit row
+constexpr int kMinScaleExp = -64;            // smallest scale 2^-64
+constexpr float kCodeMax = 448.0f;           // largest e4m3 value
+constexpr uint32_t kCodeNan = 0x7fu;
+
+// valid_len of a sample, clamped to [0, P]; the clamp is recorded once.
+__device__ __forceinline__ int clamped_len(const int32_t *valid_len, int b, int P, uint32_t *err, bool report)
+{
+    if (valid_len == nullptr) return P;
+    const int raw = __ldg(valid_len + b);
+    const int vl = min(max(raw, 0), P);
+    if (raw != vl && report) atomicOr(err, kEwClamped);
+    return vl;
+}
+
+// The smallest power of two s >= 2^-64 with amax <= 448 s (amax finite and
+// >= 0; s = 1 for amax = 0).  448 = 1.75 * 2^8, so with amax = f * 2^e,
+// 1 <= f < 2, the exponent is e - 8, one more when f > 1.75.  A subnormal
+// amax has a biased exponent field of 0 and gets the smallest scale.
+__device__ __forceinline__ float pow2_scale(float amax)
+{
+    if (amax == 0.0f) return 1.0f;
+    const uint32_t u = __float_as_uint(amax);
+    int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = max(e, kMinScaleExp);
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// 1 / s of a power of two s in [2^-64, 2^120]
+__device__ __forceinline__ float pow2_inverse(float s)
+{
+    return __uint_as_float((254u << 23) - __float_as_uint(s));
+}
+
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// the four values of four codes
+__device__ __forceinline__ float4 decode4(uint32_t w)
+{
+    const __half2 lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
+    const __half2 hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+    const float2 a = __half22float2(lo), b = __half22float2(hi);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Largest value over the CTA (256 threads); `slots` holds 8 words.
+__device__ __forceinline__ uint32_t block_max_u32(uint32_t v, uint32_t *slots)
+{
+    v = __reduce_max_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+    __syncthreads();
+    uint32_t m = slots[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max(m, slots[i]);
+    return m;
+}
+
+struct QuantParams {
+    const __nv_bfloat16 *k, *v;  // [units, P, 256]
+    uint8_t *k8, *v8;
+    float *k_scale, *v_scale;    // [units, nblk]
+    const int32_t *valid_len;
+    uint32_t *err;
+    int Hkv, P, nblk, blk0;     // blk0: first block written
+};
+
+// One CTA per (block of rows, unit, K or V): every value is read once, held
+// in registers for the block's maximum and then encoded.  Bound by HBM
+// (2 bytes read and 1 written per value).
+template <int BLOCK>
+__global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p)
+{
+    __shared__ uint32_t slots[8];
+    const int unit = blockIdx.y, which = blockIdx.z;
+    const int n = p.blk0 + blockIdx.x;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int vl = clamped_len(p.valid_len, unit / p.Hkv, p.P, p.err,
+                               threadIdx.x == 0 && blockIdx.x == 0 && which == 0 && unit % p.Hkv == 0);
+    const int rows = min(BLOCK, vl - n * BLOCK);
+    if (rows <= 0) return;
+    constexpr int kPasses = BLOCK / 16;  // 16 rows a pass, 16 values a thread
+    const int r0 = threadIdx.x >> 4, col = (threadIdx.x & 15) * 16;
+    const size_t row0 = static_cast<size_t>(unit) * p.P + static_cast<size_t>(n) * BLOCK;
+    const __nv_bfloat16 *src = (which ? p.v : p.k) + row0 * kHeadDim + col;
+    uint4 v[kPasses][2];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        const int r = i * 16 + r0;
+        if (r < rows) {
+            const uint4 *a = reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * kHeadDim);
+            v[i][0] = __ldg(a);
+            v[i][1] = __ldg(a + 1);
+        }
+    }
+    // bf16 magnitudes order like their bit patterns; 0x7f80 and above are
+    // infinities and NaN, which set no scale and become NaN codes
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+        }
+    uint32_t amax = block_max_u32(max(top & 0xffffu, top >> 16), slots);
+    const bool odd = amax >= 0x7f80u;
+    if (odd) {
+        uint32_t fin = 0u;
+        for (int i = 0; i < kPasses; ++i)
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
+                    fin = max(fin, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                }
+            }
+        __syncthreads();
+        amax = block_max_u32(fin, slots);
+    }
+    const float s = pow2_scale(__uint_as_float(amax << 16)), inv = pow2_inverse(s);
+    if (threadIdx.x == 0) (which ? p.v_scale : p.k_scale)[static_cast<size_t>(unit) * p.nblk + n] = s;
+    uint8_t *dst = (which ? p.v8 : p.k8) + row0 * kRowBytes8 + col;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int r = i * 16 + r0;
+        if (r >= rows) break;
+        uint32_t o[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t a = w[2 * e], b = w[2 * e + 1];
+                uint32_t c = encode4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
+                                     __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv);
+                if (odd) {
+                    if ((a & 0x7fffu) >= 0x7f80u) c |= kCodeNan;
+                    if ((a >> 16 & 0x7fffu) >= 0x7f80u) c |= kCodeNan << 8;
+                    if ((b & 0x7fffu) >= 0x7f80u) c |= kCodeNan << 16;
+                    if ((b >> 16 & 0x7fffu) >= 0x7f80u) c |= kCodeNan << 24;
+                }
+                o[2 * h + e] = c;
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(r) * kRowBytes8) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ------------------------------------------------------------------ eviction
+
+struct SelectParams {
+    const float *mass;          // [units, P]
+    const int32_t *valid_len;
+    const uint8_t *mask;        // [B, P] or nullptr
+    float *mass_out;            // [units, Pout]
+    int32_t *pos;               // [units, Pout]
+    int32_t *valid_out;         // [B]
+    uint32_t *err;
+    int Hkv, P, Pout, n_keep, n_first, n_last;
+};
+
+constexpr int kSelectThreads = 512;
+
+// Sort key of a position: 0 hidden, 1 NaN, then the weights in ascending
+// order (-0 counts as +0), the largest for a protected position.
+__device__ __forceinline__ uint32_t select_key(const SelectParams &p, const float *mass, const uint8_t *mask, int vl,
+                                               int j)
+{
+    if (j >= vl || (mask != nullptr && mask[j] == 0)) return 0u;
+    if (j < p.n_first || j >= vl - p.n_last) return 0xffffffffu;
+    const float m = mass[j] + 0.0f;
+    if (m != m) return 1u;
+    const uint32_t u = __float_as_uint(m);
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// Inclusive scan of one int per thread over the CTA; returns the exclusive
+// prefix and the total.  `slots` holds kSelectThreads / 32 words.
+__device__ __forceinline__ int block_scan(int v, int *slots, int *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
+    }
+    __syncthreads();
+    if (lane == 31) slots[warp] = s;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < kSelectThreads / 32; ++w) {
+        const int t = slots[w];
+        if (w < warp) before += t;
+        all += t;
+    }
+    *total = all;
+    return before + s - v;
+}
+
+// One CTA per (sample, KV head): the key of the n_keep-th wanted position by
+// a radix selection (four 8-bit digits, from the top), then one pass that
+// writes the kept positions in ascending order, the lowest ones first among
+// equals.
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p)
+{
+    __shared__ int hist[256];
+    __shared__ int slots[kSelectThreads / 32];
+    __shared__ int pick[2];
+    const int unit = blockIdx.x, b = unit / p.Hkv;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int vl = clamped_len(p.valid_len, b, p.P, p.err, threadIdx.x == 0 && unit % p.Hkv == 0);
+    const float *mass = p.mass + static_cast<size_t>(unit) * p.P;
+    const uint8_t *mask = p.mask ? p.mask + static_cast<size_t>(b) * p.P : nullptr;
+    int seen = 0;
+    for (int j = threadIdx.x; j < vl; j += kSelectThreads) seen += mask == nullptr || mask[j] != 0;
+    int count = 0;
+    block_scan(seen, slots, &count);
+    const int keep = min(p.n_keep, count);
+    if (threadIdx.x == 0 && unit % p.Hkv == 0) p.valid_out[b] = keep;
+    int32_t *pos = p.pos + static_cast<size_t>(unit) * p.Pout;
+    float *mass_out = p.mass_out + static_cast<size_t>(unit) * p.Pout;
+    uint32_t prefix = 0u, known = 0u;
+    int want = keep;  // how many of the keys that match the prefix are kept
+    if (keep > 0) {
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+            __syncthreads();
+            for (int j = threadIdx.x; j < vl; j += kSelectThreads) {
+                const uint32_t k = select_key(p, mass, mask, vl, j);
+                if (k != 0u && (k & known) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+            }
+            __syncthreads();
+            // thread t holds digit 255 - t: the number of larger digits' keys
+            const int mine = threadIdx.x < 256 ? hist[255 - threadIdx.x] : 0;
+            int total = 0;
+            const int above = block_scan(mine, slots, &total);
+            if (threadIdx.x < 256 && above < want && above + mine >= want) {
+                pick[0] = 255 - static_cast<int>(threadIdx.x);
+                pick[1] = want - above;
+            }
+            __syncthreads();
+            prefix |= static_cast<uint32_t>(pick[0]) << shift;
+            known |= 255u << shift;
+            want = pick[1];
+        }
+    }
+    // prefix is the key of the last kept position, want how many of its equals are kept
+    int base = 0, ties = 0;
+    for (int j0 = 0; keep > 0 && j0 < vl; j0 += kSelectThreads) {
+        const int j = j0 + threadIdx.x;
+        const uint32_t k = j < vl ? select_key(p, mass, mask, vl, j) : 0u;
+        const bool tie = k != 0u && k == prefix;
+        int n_tie = 0, n_kept = 0;
+        const int tie_at = ties + block_scan(tie ? 1 : 0, slots, &n_tie);
+        const bool kept = k > prefix || (tie && tie_at < want);
+        const int at = base + block_scan(kept ? 1 : 0, slots, &n_kept);
+        if (kept) {
+            pos[at] = j;
+            mass_out[at] = mass[j];
+        }
+        ties += n_tie;
+        base += n_kept;
+    }
+    for (int i = keep + threadIdx.x; i < p.Pout; i += kSelectThreads) {
+        pos[i] = -1;
+        mass_out[i] = 0.0f;
+    }
+}
+
+struct GatherParams {
+    const uint8_t *k, *v;               // [units, P] rows
+    uint8_t *k_out, *v_out;             // [units, Pout] rows
+    const float *k_scale, *v_scale;     // 8-bit: [units, nblk]
+    float *k_scale_out, *v_scale_out;   // 8-bit: [units, nblk_out]
+    const int32_t *pos;      // [units, Pout]
+    const int32_t *valid;    // [B]: kept rows
+    int Hkv, P, Pout, nblk, nblk_out, shift;  // shift: log2 of the block
+};
+
+// bf16 rows: one warp moves four rows of K and V at a time, 512 bytes each.
+__global__ void __launch_bounds__(256) gather_rows_kernel(const GatherParams p)
+{
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int unit = blockIdx.y;
+    const int lane = threadIdx.x & 31;
+    const int n = __ldg(p.valid + unit / p.Hkv);
+    const int i0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4;
+    if (i0 >= n) return;
+    const int32_t *pos = p.pos + static_cast<size_t>(unit) * p.Pout;
+    const size_t in0 = static_cast<size_t>(unit) * p.P, out0 = static_cast<size_t>(unit) * p.Pout;
+    uint4 v[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (i0 + r < n) {
+            const size_t off = (in0 + static_cast<size_t>(__ldg(pos + i0 + r))) * 512 + lane * 16;
+            v[r][0] = *reinterpret_cast<const uint4 *>(p.k + off);
+            v[r][1] = *reinterpret_cast<const uint4 *>(p.v + off);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (i0 + r < n) {
+            const size_t off = (out0 + i0 + r) * 512 + lane * 16;
+            *reinterpret_cast<uint4 *>(p.k_out + off) = v[r][0];
+            *reinterpret_cast<uint4 *>(p.v_out + off) = v[r][1];
+        }
+    }
+}
+
+// 8-bit rows: one CTA per (block of new rows, unit, K or V).  The kept rows
+// come from blocks with scales of their own; their largest value sets the
+// new block's scale by the quantiser's rule and every code is rounded to it.
+template <int BLOCK>
+__global__ void __launch_bounds__(256) gather_codes_kernel(const GatherParams p)
+{
+    __shared__ uint32_t slots[8];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int unit = blockIdx.y, which = blockIdx.z, nb = blockIdx.x;
+    const int n = __ldg(p.valid + unit / p.Hkv);
+    const int rows = min(BLOCK, n - nb * BLOCK);
+    if (rows <= 0) return;
+    constexpr int kPasses = BLOCK / 16;
+    const int r0 = threadIdx.x >> 4, col = (threadIdx.x & 15) * 16;
+    const int32_t *pos = p.pos + static_cast<size_t>(unit) * p.Pout + nb * BLOCK;
+    const float *scale = (which ? p.v_scale : p.k_scale) + static_cast<size_t>(unit) * p.nblk;
+    uint4 v[kPasses];
+    float s[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int r = i * 16 + r0;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        s[i] = 0.0f;
+        if (r < rows) {
+            const int j = __ldg(pos + r);
+            v[i] = *reinterpret_cast<const uint4 *>(
+                (which ? p.v : p.k) + (static_cast<size_t>(unit) * p.P + j) * kRowBytes8 + col);
+            s[i] = __ldg(scale + (j >> p.shift));
+        }
+    }
+    // magnitudes of e4m3 codes order like their bits (NaN codes set no scale)
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t top = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a = w[e] & 0x7f7f7f7fu;
+            top = __vmaxu4(top, a & ~__vcmpeq4(a, 0x7f7f7f7fu));
+        }
+        top = __vmaxu4(top, top >> 16);
+        top = __vmaxu4(top, top >> 8) & 0xffu;
+        amax = fmaxf(amax, decode4(top).x * s[i]);
+    }
+    amax = __uint_as_float(block_max_u32(__float_as_uint(amax), slots));
+    const float t = pow2_scale(amax), inv = pow2_inverse(t);
+    if (threadIdx.x == 0) (which ? p.v_scale_out : p.k_scale_out)[static_cast<size_t>(unit) * p.nblk_out + nb] = t;
+    uint8_t *dst = (which ? p.v_out : p.k_out) + (static_cast<size_t>(unit) * p.Pout + nb * BLOCK) * kRowBytes8 + col;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int r = i * 16 + r0;
+        if (r >= rows) break;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 x = decode4(w[e]);
+            o[e] = encode4(x.x * s[i] * inv, x.y * s[i] * inv, x.z * s[i] * inv, x.w * s[i] * inv);
+        }
+        *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(r) * kRowBytes8) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+}  // namespace cache
+}  // namespace dm05

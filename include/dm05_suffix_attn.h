@@ -332,6 +332,116 @@ int dm05_post_attention(const void *attn, const void *h, const void *scale, cons
 int dm05_post_attention_reserve(int B, int S, int Hq, int D, int Hd, int F, cudaStream_t stream);
 
 /*
+ * Prefix-cache compression -- the operators that let one prefix cache serve
+ * its denoising steps from fewer bytes: an 8-bit cache, the suffix attention
+ * over it, the attention weight each cached position received, and the
+ * eviction of the positions that received least.  The source pages have no
+ * counterpart (their cache is bf16 and keeps every position).  All are
+ * asynchronous on `stream`, deterministic, use no atomics on results and can
+ * be captured into a CUDA graph; the first call on a device creates the
+ * error word and must run outside capture.  They own no workspace, so any
+ * number of calls and captured graphs may run at once on different streams.
+ * Sizes: D == 256, P <= 2^24, B * Hkv <= 65535.  bf16 and code tensors
+ * 16-byte, fp32 and int32 arrays 4-byte aligned; outputs must not overlap
+ * inputs unless a call says so.  Values of a valid-length array outside
+ * [0, P] are clamped and flagged in the error word; rows at or past the
+ * valid length are never read as data, so they may hold any bits.
+ *
+ * The 8-bit cache: codes e4m3 [B, Hkv, P, D] (the type's NaN-only, no-infinity
+ * form; largest value 448) for K and for V, and fp32 scales
+ * [B, Hkv, ceil(P / block)], block = 16, 32, 64 or 128 consecutive positions:
+ * row j stands for scale[j / block] * code[j].
+ *
+ * dm05_kv8_quantize -- writes the 8-bit form of rows [first,
+ * clamp(valid_len[b], 0, P)) of k and v (bf16 [B, Hkv, P, D]); valid_len
+ * int32 [B] or NULL (every row); `first` a multiple of block below P, so that
+ * a prefix can be quantised in pieces.  Per block, with a = the largest
+ * finite |x| of its rows in range:
+ *   scale = the smallest power of two >= 2^-64 with a <= 448 scale (1 if a == 0);
+ *   code  = x / scale rounded to nearest even (NaN if x is not finite).
+ * Codes of rows outside the range, and scales of blocks without a row in it,
+ * are left as they were.
+ */
+int dm05_kv8_quantize(const void *k, const void *v, const int32_t *valid_len, void *k8, void *v8, float *k_scale,
+                      float *v_scale, int B, int Hkv, int P, int D, int block, int first, cudaStream_t stream);
+
+/*
+ * dm05_suffix_attn_kv8 -- dm05_suffix_attn over an 8-bit prefix cache: K_x
+ * and V_x of prefix row j are scale[j / block] * code[j]; everything else
+ * (suffix K/V in bf16, masks, out, lse, layouts) as there.  Scales may be any
+ * positive finite numbers in [2^-64, 2^64].  Hidden rows, too, may hold any
+ * codes and blocks without a visible row any scale.  k8, v8 and the scales
+ * may be NULL iff P == 0.
+ *
+ * `workspace` holds the partial results of a call that splits a (sample, KV
+ * head) over several CTAs: device memory, 16-byte aligned, at least the
+ * bytes dm05_suffix_attn_kv8_plan gives for the sizes (NULL if 0), which the
+ * caller keeps until the call has run and shares with no call that may run
+ * at the same time; DM05_ERR_WORKSPACE if it is too small.
+ * Supported: (Hq / Hkv) * S <= 128.
+ */
+int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const float *k_scale, const float *v_scale,
+                         int block, const int32_t *prefix_valid_len, const uint8_t *prefix_mask, const void *k_suffix,
+                         const void *v_suffix, void *out, float *lse, void *workspace, size_t workspace_bytes, int B,
+                         int Hq, int Hkv, int P, int S, int D, cudaStream_t stream);
+
+/* Work plan of a dm05_suffix_attn_kv8 call with these sizes on the current
+ * device, as dm05_suffix_attn_plan (the overrides apply), and the workspace
+ * it needs.  Any output pointer may be NULL. */
+int dm05_suffix_attn_kv8_plan(int B, int Hq, int Hkv, int P, int S, int D, int *splits_per_head, int *tile_rows,
+                              int *row_blocks, size_t *workspace_bytes);
+
+/*
+ * dm05_prefix_attn_mass -- the attention weight each prefix position
+ * received in a suffix-attention call with these q, masks and lse:
+ *   mass[b,g,j] = mass_in[b,g,j] + sum over heads h of group g and queries i
+ *                 of exp(<q[b,h,i,:], k[b,g,j,:]> / sqrt(D) - lse[b,h,i])
+ * for visible j; mass_in[b,g,j] (0 if mass_in is NULL) for every other j < P.
+ *   q         bf16 [B, Hq, S, D], k_prefix bf16 [B, Hkv, P, D]
+ *   lse       fp32 [B, Hq, S]: what the attention wrote (a row of -inf adds nothing)
+ *   mass_in   fp32 [B, Hkv, P] or NULL; may be the same array as mass
+ *   mass      fp32 [B, Hkv, P], written
+ * Supported: (Hq / Hkv) * S <= 128.  Hidden rows may hold any bits.
+ * dm05_prefix_attn_mass_kv8 reads the keys of an 8-bit cache instead.
+ */
+int dm05_prefix_attn_mass(const void *q, const void *k_prefix, const int32_t *prefix_valid_len,
+                          const uint8_t *prefix_mask, const float *lse, const float *mass_in, float *mass, int B,
+                          int Hq, int Hkv, int P, int S, int D, cudaStream_t stream);
+int dm05_prefix_attn_mass_kv8(const void *q, const void *k8, const float *k_scale, int block,
+                              const int32_t *prefix_valid_len, const uint8_t *prefix_mask, const float *lse,
+                              const float *mass_in, float *mass, int B, int Hq, int Hkv, int P, int S, int D,
+                              cudaStream_t stream);
+
+/*
+ * dm05_prefix_evict -- keeps, for every (sample, KV head), the
+ *   n = min(n_keep, number of visible positions of the sample)
+ * most wanted visible positions and writes them, in ascending order, to a
+ * cache of bucket P_out >= n_keep.  Wanted first: positions < n_first and
+ * positions >= valid length - n_last; then those of larger mass; among
+ * equals the lower position (-0 equals +0, NaN comes last).
+ *   k, v       bf16 [B, Hkv, P, D]; mass fp32 [B, Hkv, P]
+ *   valid_len  int32 [B] or NULL; mask uint8 [B, P] or NULL: the visible positions
+ *   k_out, v_out  bf16 [B, Hkv, P_out, D]: rows [0, n) written, others left as they were
+ *   mass_out   fp32 [B, Hkv, P_out]: their mass, then 0
+ *   positions  int32 [B, Hkv, P_out]: where each row came from, then -1
+ *   valid_out  int32 [B]: n, the valid length of the new cache
+ * Every position of the new cache below valid_out is visible, so no mask
+ * goes with it.  n_keep may be 0.
+ * dm05_prefix_evict_kv8 does the same on an 8-bit cache: the kept rows form
+ * new blocks, whose scales follow dm05_kv8_quantize's rule over the values
+ * scale * code, and are rounded to them (scales of blocks without a kept row
+ * are left as they were).
+ */
+int dm05_prefix_evict(const void *k, const void *v, const float *mass, const int32_t *valid_len, const uint8_t *mask,
+                      void *k_out, void *v_out, float *mass_out, int32_t *positions, int32_t *valid_out, int B,
+                      int Hkv, int P, int P_out, int D, int n_keep, int n_first, int n_last, cudaStream_t stream);
+int dm05_prefix_evict_kv8(const void *k8, const void *v8, const float *k_scale, const float *v_scale, int block,
+                          const float *mass, const int32_t *valid_len, const uint8_t *mask, void *k8_out,
+                          void *v8_out, float *k_scale_out, float *v_scale_out, float *mass_out, int32_t *positions,
+                          int32_t *valid_out, int B, int Hkv, int P, int P_out, int D, int n_keep, int n_first,
+                          int n_last, cudaStream_t stream);
+
+/*
  * dm05_suffix_attn_noalloc -- the same attention as dm05_suffix_attn, for
  * callers that must not allocate device memory.  The source pages have no
  * counterpart of this entry point; it exists for embedding.
