@@ -28,11 +28,12 @@
 //     smallest step of the second term (2^-9) is 2^-15 of the largest weight.
 //
 // One CTA walks a contiguous run of a unit's key tiles: the suffix tiles (64
-// rows of bf16, kind::f16), then prefix tiles of 128 codes.  K and V tiles
-// (32 KB each) alternate in one ring of shared memory filled by TMA.  Warp
+// rows of bf16, kind::f16), then prefix tiles of 128 codes, each 32 KB of K
+// and of V in two rings of shared memory filled by TMA.  Warp
 // roles, split over a cluster and the merge are those of the bf16 kernel
-// (suffix_attn_kernel.cuh): warp 8 loads, warp 9 issues the MMAs, warps 0-7
-// run the softmax (two warps per 32 query rows, half of a tile's columns
+// (suffix_attn_kernel.cuh), but for the softmax: warps 16 and 18 load (Q and
+// K; V), warp 17 issues the MMAs, and warps 0-15 are two groups that take
+// the tiles in turn (two warps per 32 query rows, half of a tile's columns
 // each).  Q lands in shared memory as bf16; the CTA with suffix tiles copies
 // it to tensor memory (into the second S buffer, which is not in use yet),
 // and the softmax warps rewrite it in place as the two e4m3 terms.
@@ -76,6 +77,22 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool b_mn_ma
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// 32 lanes x 32 bit, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// The largest of three (a NaN operand is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 }  // namespace ptx
 
 namespace kv8 {
@@ -83,7 +100,12 @@ namespace kv8 {
 constexpr int kTile = 128;           // prefix rows of a tile
 constexpr int kSufTile = 64;         // suffix rows of a tile
 constexpr int kSlotBytes = 32768;    // one K or V tile of either kind
-constexpr int kSlots = 4;
+constexpr int kSlots = 2;            // of K and of V
+constexpr int kSoftWarps = 16;       // two groups of eight, each two warps per TMEM lane quarter
+constexpr int kLoadWarp = 16;        // Q and K
+constexpr int kIssueWarp = 17;
+constexpr int kLoadVWarp = 18;
+constexpr int kThreads8 = 608;
 constexpr uint32_t kTmemO8 = 0;      // O: columns [0, 256)
 constexpr uint32_t kTmemS8 = 256;    // two S / P buffers of 128 columns
 constexpr float kTopBits = 6.0f;     // a new maximum's weight is 2^6 ...
@@ -97,29 +119,38 @@ constexpr float kSuffixBits = 7.0f;
 
 struct Smem {
     static constexpr int kQChunkBytes = kMRows * 128;
-    static constexpr int kQBytes = 4 * kQChunkBytes;  // bf16, then [hi: 2 chunks][lo: 2 chunks] of e4m3
-    static constexpr int kRing = kQBytes;
-    static constexpr int kDataEnd = kRing + kSlots * kSlotBytes;
+    static constexpr int kQBytes = 4 * kQChunkBytes;  // bf16, then two e4m3 terms in the same bytes
+    static constexpr int kK = kQBytes;
+    static constexpr int kV = kK + kSlots * kSlotBytes;
+    static constexpr int kDataEnd = kV + kSlots * kSlotBytes;
     static constexpr int kBarQFull = 0;
     static constexpr int kBarQFree = 1;   // Q copied to tensor memory
     static constexpr int kBarQConv = 2;   // Q rewritten as two e4m3 terms
-    static constexpr int kBarFull = 3;
-    static constexpr int kBarEmpty = kBarFull + kSlots;
-    static constexpr int kBarSFull = kBarEmpty + kSlots;
+    static constexpr int kBarKFull = 3;
+    static constexpr int kBarKEmpty = kBarKFull + kSlots;
+    static constexpr int kBarVFull = kBarKEmpty + kSlots;
+    static constexpr int kBarVEmpty = kBarVFull + kSlots;
+    static constexpr int kBarSFull = kBarVEmpty + kSlots;
     static constexpr int kBarPReady = kBarSFull + 2;
     static constexpr int kBarPFree = kBarPReady + 2;
     static constexpr int kBarMmaFinal = kBarPFree + 2;
     static constexpr int kBarMerge = kBarMmaFinal + 1;
-    static constexpr int kBarPair = kBarMerge + 1;
-    static constexpr int kNumBars = kBarPair + 4;
+    static constexpr int kBarRow = kBarMerge + 1;   // per lane quarter: its four warps
+    static constexpr int kBarPair = kBarRow + 4;    // per group and lane quarter: its two warps
+    static constexpr int kBarMax = kBarPair + 8;    // per lane quarter: tile t's reference maximum is known
+    static constexpr int kNumBars = kBarMax + 4;
     static constexpr int kBarOff = kDataEnd;
     static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
-    static constexpr int kXchgOff = (kTmemSlotOff + 16 + 15) / 16 * 16;  // row maxima [2][2][128], sums [2][128]
-    static constexpr int kEnd = kXchgOff + (4 + 2) * kMRows * 4;
+    // tile maxima [2 groups][2 halves][128], reference maxima [2][128], sums
+    // [4][128], visibility limits [16 warps][64]
+    static constexpr int kXchgOff = (kTmemSlotOff + 16 + 15) / 16 * 16;
+    static constexpr int kEnd = kXchgOff + (4 + 2 + 4) * kMRows * 4 + kSoftWarps * 64 * 4;
     static constexpr int kAllocBytes = kEnd + 1024;
     static constexpr int kStageStride = kHeadDim * 4 + 16;  // a partial row: D fp32 of O, then {m, l, l, 0}
+    static constexpr int kOutStride = kHeadDim * 2 + 16;    // an output row on its way out
     static_assert(kDataEnd >= (kMRows + 16) * kStageStride, "the merge receives at most 144 rows");
-    static_assert(6 * kMRows * 4 >= kMRows * 8, "the merge keeps one output row index per row in the exchange area");
+    static_assert(10 * kMRows * 4 >= kMRows * 8, "the merge keeps one output row index per row in the exchange area");
+    static_assert(kAllocBytes <= 232448, "shared memory of a CTA");
 };
 
 struct Params {
@@ -149,18 +180,28 @@ __device__ __forceinline__ int uses_before(int t, int ns)
     return ns + (k >> 1);
 }
 
-// Two fp32 values as two e4m3 terms each: hi | lo << 16 (two codes each).
-__device__ __forceinline__ uint32_t two_terms(float a, float b)
+// Four values as two e4m3 terms each (four codes a word): x = fp16(v), hi =
+// e4m3(x), lo = e4m3(x - hi), where x - hi is exact.
+__device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3, uint32_t &hi, uint32_t &lo)
 {
-    const __half2 x = __floats2half2_rn(a, b);
-    const __nv_fp8x2_storage_t hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3));
-    const __nv_fp8x2_storage_t lo =
-        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, __NV_E4M3);
-    return static_cast<uint32_t>(hi) | static_cast<uint32_t>(lo) << 16;
+    asm("{\n\t.reg .b16 h0, h1, l0, l1;\n\t.reg .b32 x0, x1, b0, b1;\n\t"
+        "cvt.rn.f16x2.f32 x0, %3, %2;\n\t"
+        "cvt.rn.f16x2.f32 x1, %5, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h0, x0;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h1, x1;\n\t"
+        "mov.b32 %0, {h0, h1};\n\t"
+        "cvt.rn.f16x2.e4m3x2 b0, h0;\n\t"
+        "cvt.rn.f16x2.e4m3x2 b1, h1;\n\t"
+        "sub.rn.f16x2 x0, x0, b0;\n\t"
+        "sub.rn.f16x2 x1, x1, b1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l0, x0;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l1, x1;\n\t"
+        "mov.b32 %1, {l0, l1};\n\t}"
+        : "=r"(hi), "=r"(lo)
+        : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads8, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
                 const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ks,
                 const __grid_constant__ CUtensorMap tm_vs, const Params p)
@@ -185,29 +226,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         ptx::mbar_init(&bars[L::kBarQFull], 1);
         ptx::mbar_init(&bars[L::kBarQFree], 1);
-        ptx::mbar_init(&bars[L::kBarQConv], kSoftmaxWarps * 32);
-        for (int s = 0; s < kSlots; ++s) {
-            ptx::mbar_init(&bars[L::kBarFull + s], 1);
-            ptx::mbar_init(&bars[L::kBarEmpty + s], 1);
+        ptx::mbar_init(&bars[L::kBarQConv], kSoftWarps * 32);
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(&bars[L::kBarKFull + i], 1);
+            ptx::mbar_init(&bars[L::kBarKEmpty + i], 1);
+            ptx::mbar_init(&bars[L::kBarVFull + i], 1);
+            ptx::mbar_init(&bars[L::kBarVEmpty + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bars[L::kBarSFull + i], 1);
-            ptx::mbar_init(&bars[L::kBarPReady + i], kSoftmaxWarps * 32);
+            ptx::mbar_init(&bars[L::kBarPReady + i], kSoftWarps / 2 * 32);
             ptx::mbar_init(&bars[L::kBarPFree + i], 1);
         }
         ptx::mbar_init(&bars[L::kBarMmaFinal], 1);
         ptx::mbar_init(&bars[L::kBarMerge], 1);
-        for (int i = 0; i < 4; ++i) ptx::mbar_init(&bars[L::kBarPair + i], 64);
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(&bars[L::kBarRow + i], 128);
+            ptx::mbar_init(&bars[L::kBarPair + i], 64);
+            ptx::mbar_init(&bars[L::kBarPair + 4 + i], 64);
+            ptx::mbar_init(&bars[L::kBarMax + i], 64);
+        }
         ptx::fence_mbar_init();
     }
-    if (warp == kProducerWarp && lane == 0) {
+    if (warp == kLoadWarp && lane == 0) {
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_kp);
         ptx::prefetch_tensormap(&tm_vp);
         ptx::prefetch_tensormap(&tm_ks);
         ptx::prefetch_tensormap(&tm_vs);
     }
-    if (warp == kMmaWarp) {
+    if (warp == kIssueWarp) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
     }
@@ -217,6 +265,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     ptx::griddep_wait();
+
+    // Q, and the first suffix tile of the CTA that starts with it, do not
+    // depend on the valid length: requested before it has been read.
+    auto k_slot = [&](int t) { return smem + L::kK + (t % kSlots) * kSlotBytes; };
+    auto v_slot = [&](int t) { return smem + L::kV + (t % kSlots) * kSlotBytes; };
+    const bool first = rank == 0;
+    uint64_t pol = 0;
+    if (warp == kLoadWarp && lane == 0) {
+        pol = ptx::policy_evict_first();
+        if (p.row_blocks == 1) {
+            ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], L::kQBytes);
+            ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, 0, 0, unit);
+        } else {
+            ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(p.G * kChunks * p.SQ * 128));
+            for (int h = 0; h < p.G; ++h)
+                for (int c = 0; c < kChunks; ++c)
+                    ptx::tma_load_3d(smem + c * L::kQChunkBytes + h * rph * 128, &tm_q, &bars[L::kBarQFull],
+                                     c * kChunkElems, h * p.S + q0, unit);
+        }
+        if (first) {
+            ptx::mbar_arrive_expect_tx(&bars[L::kBarKFull], kSlotBytes);
+            ptx::tma_load_4d_hint(k_slot(0), &tm_ks, &bars[L::kBarKFull], 0, 0, 0, unit, pol);
+        }
+    }
+    if (warp == kLoadVWarp && lane == 0) {
+        pol = ptx::policy_evict_first();
+        if (first) {
+            ptx::mbar_arrive_expect_tx(&bars[L::kBarVFull], kSlotBytes);
+            ptx::tma_load_4d_hint(v_slot(0), &tm_vs, &bars[L::kBarVFull], 0, 0, 0, unit, pol);
+        }
+    }
 
     const int vl = cache::clamped_len(p.valid_len, b, p.P, p.err,
                                       threadIdx.x == 0 && rank == 0 && rb == 0 && unit % p.Hkv == 0);
@@ -229,82 +308,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     // first row of local tile t and how many of its rows are in range
     auto row0_of = [&](int t) { return t < ns ? (t_begin + t) * kSufTile : (t_begin + t - TS) * kTile; };
     auto rows_of = [&](int t) { return t < ns ? min(kSufTile, p.S - row0_of(t)) : min(kTile, vl - row0_of(t)); };
-    auto slot_at = [&](int i) { return smem + L::kRing + (i % kSlots) * kSlotBytes; };  // item 2t: K of tile t, 2t+1: V
     bool failed = false;
 
-    if (warp == kProducerWarp) {
-        // ================================================== TMA producer
-        if (lane == 0 && T > 0) {
-            const uint64_t pol = ptx::policy_evict_first();
-            if (p.row_blocks == 1) {
-                ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], L::kQBytes);
-                ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, 0, 0, unit);
-            } else {
-                ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(p.G * kChunks * p.SQ * 128));
-                for (int h = 0; h < p.G; ++h)
-                    for (int c = 0; c < kChunks; ++c)
-                        ptx::tma_load_3d(smem + c * L::kQChunkBytes + h * rph * 128, &tm_q, &bars[L::kBarQFull],
-                                         c * kChunkElems, h * p.S + q0, unit);
-            }
-            int issued = 0;
-            for (int i = 0; i < 2 * T; ++i) {
-                const int s = i % kSlots, n = i / kSlots;
-                if (n > 0 && !ptx::mbar_wait(&bars[L::kBarEmpty + s], (n - 1) & 1, kWaitLimitNs)) {
+    if (warp == kLoadWarp || warp == kLoadVWarp) {
+        // ================================================== TMA producers (K, V)
+        if (lane == 0) {
+            const bool is_v = warp == kLoadVWarp;
+            uint64_t *full = &bars[is_v ? L::kBarVFull : L::kBarKFull];
+            uint64_t *empty = &bars[is_v ? L::kBarVEmpty : L::kBarKEmpty];
+            const CUtensorMap *ms = is_v ? &tm_vs : &tm_ks, *mp = is_v ? &tm_vp : &tm_kp;
+            uint8_t *ring = smem + (is_v ? L::kV : L::kK);
+            // (rank 0 has no tile when there are more CTAs than tiles: its early
+            // one is then only drained)
+            int issued = first ? 1 : 0;
+            for (int t = issued; t < T; ++t) {
+                const int s = t % kSlots, n = t / kSlots;
+                if (n > 0 && !ptx::mbar_wait(&empty[s], (n - 1) & 1, kWaitLimitNs)) {
                     failed = true;
                     break;
                 }
-                const int t = i >> 1;
-                const CUtensorMap *map = t < ns ? ((i & 1) ? &tm_vs : &tm_ks) : ((i & 1) ? &tm_vp : &tm_kp);
-                ptx::mbar_arrive_expect_tx(&bars[L::kBarFull + s], kSlotBytes);
-                ptx::tma_load_4d_hint(slot_at(i), map, &bars[L::kBarFull + s], 0, row0_of(t), 0, unit, pol);
-                issued = i + 1;
+                ptx::mbar_arrive_expect_tx(&full[s], kSlotBytes);
+                ptx::tma_load_4d_hint(ring + s * kSlotBytes, t < ns ? ms : mp, &full[s], 0, row0_of(t), 0, unit, pol);
+                issued = t + 1;
             }
             // every copy this thread issued has landed before the CTA may exit
-            if (!ptx::mbar_wait(&bars[L::kBarQFull], 0, kWaitLimitNs)) failed = true;
-            for (int i = max(0, issued - kSlots); i < issued; ++i)
-                if (!ptx::mbar_wait(&bars[L::kBarFull + i % kSlots], (i / kSlots) & 1, kWaitLimitNs)) failed = true;
+            if (!is_v && !ptx::mbar_wait(&bars[L::kBarQFull], 0, kWaitLimitNs)) failed = true;
+            for (int t = max(0, issued - kSlots); t < issued; ++t)
+                if (!ptx::mbar_wait(&full[t % kSlots], (t / kSlots) & 1, kWaitLimitNs)) failed = true;
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kIssueWarp) {
         // ================================================== MMA issuer
         if (lane == 0 && T > 0) {
             constexpr uint32_t id_qk = ptx::idesc_e4m3_f32(kMRows, kTile, false);
             constexpr uint32_t id_pv = ptx::idesc_e4m3_f32(kMRows, kHeadDim, true);
             constexpr uint32_t id_qk16 = ptx::idesc_bf16_f32(kMRows, kSufTile, false);
             constexpr uint32_t id_pv16 = ptx::idesc_bf16_f32(kMRows, kHeadDim, true);
-            const uint32_t ring = ptx::smem_addr(smem + L::kRing);
             const uint64_t qdesc = ptx::sw128_desc(ptx::smem_addr(smem), 16, 1024);
-            const uint64_t kdesc0 = ptx::sw128_desc(ring, 16, 1024);                // K-major, 128-byte chunks
-            const uint64_t vdesc0 = ptx::sw128_desc(ring, kTile * 128, 1024);       // MN-major, column chunks apart
-            const uint64_t vdesc16 = ptx::sw128_desc(ring, kSufTile * 128, 1024);
-            auto slot_off = [&](int i) { return static_cast<uint64_t>(((i % kSlots) * kSlotBytes) >> 4); };
+            const uint64_t kdesc0 = ptx::sw128_desc(ptx::smem_addr(smem + L::kK), 16, 1024);  // K-major, 128-byte chunks
+            const uint64_t vdesc0 = ptx::sw128_desc(ptx::smem_addr(smem + L::kV), kTile * 128, 1024);  // MN-major, column chunks apart
+            const uint64_t vdesc16 = ptx::sw128_desc(ptx::smem_addr(smem + L::kV), kSufTile * 128, 1024);
+            auto slot_off = [&](int t) { return static_cast<uint64_t>(((t % kSlots) * kSlotBytes) >> 4); };
             auto issue_pv = [&](int u) -> bool {
-                const int pb = buffer_of(u, ns), i = 2 * u + 1;
+                const int pb = buffer_of(u, ns), s = u % kSlots;
                 if (!ptx::mbar_wait(&bars[L::kBarPReady + pb], uses_before(u, ns) & 1, kWaitLimitNs)) return false;
-                if (!ptx::mbar_wait(&bars[L::kBarFull + i % kSlots], (i / kSlots) & 1, kWaitLimitNs)) return false;
+                if (!ptx::mbar_wait(&bars[L::kBarVFull + s], (u / kSlots) & 1, kWaitLimitNs)) return false;
                 ptx::tc_fence_after_sync();
                 const uint32_t a = tmem + kTmemS8 + pb * kTile;
                 const int n = rows_of(u);
                 if (u < ns) {
-                    const uint64_t vd = vdesc16 + slot_off(i);
+                    const uint64_t vd = vdesc16 + slot_off(u);
                     const int nk = (n + 15) / 16;
 #pragma unroll
                     for (int kk = 0; kk < kSufTile / 16; ++kk) {
                         if (kk >= nk) break;
-                        ptx::mma_bf16_ts(tmem + kTmemO8, a + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4),
-                                         id_pv16, (u > 0 || kk > 0) ? 1u : 0u);
+                        ptx::mma_bf16_ts(tmem + kTmemO8, a + (kk >> 1) * 32 + (kk & 1) * 8,
+                                         vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv16,
+                                         (u > 0 || kk > 0) ? 1u : 0u);
                     }
                 } else {
-                    const uint64_t vd = vdesc0 + slot_off(i);
+                    const uint64_t vd = vdesc0 + slot_off(u);
                     const int nk = (n + 31) / 32;  // 32-row steps that hold rows in range
 #pragma unroll
                     for (int kk = 0; kk < kTile / 32; ++kk) {
                         if (kk >= nk) break;
                         const uint64_t vk = vd + static_cast<uint64_t>((kk * 32 * 128) >> 4);
-                        ptx::mma_f8_ts(tmem + kTmemO8, a + kk * 8, vk, id_pv, (u > 0 || kk > 0) ? 1u : 0u);
-                        ptx::mma_f8_ts(tmem + kTmemO8, a + 32 + kk * 8, vk, id_pv, 1u);
+                        const uint32_t ak = a + (kk >> 1) * 64 + (kk & 1) * 16;
+                        ptx::mma_f8_ts(tmem + kTmemO8, ak, vk, id_pv, (u > 0 || kk > 0) ? 1u : 0u);
+                        ptx::mma_f8_ts(tmem + kTmemO8, ak + 8, vk, id_pv, 1u);
                     }
                 }
-                ptx::mma_commit(&bars[L::kBarEmpty + i % kSlots]);
+                ptx::mma_commit(&bars[L::kBarVEmpty + s]);
                 ptx::mma_commit(&bars[L::kBarPFree + pb]);
                 return true;
             };
@@ -318,14 +391,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mma_commit(&bars[L::kBarQFree]);
             }
             for (int t = 0; t < T && ok; ++t) {
-                const int sb = buffer_of(t, ns), before = uses_before(t, ns), i = 2 * t;
+                const int sb = buffer_of(t, ns), before = uses_before(t, ns), s = t % kSlots;
                 // a second suffix tile shares its predecessor's buffer: that PV goes first
                 const bool pv_first = t > 0 && t < ns;
                 if (pv_first && !issue_pv(t - 1)) {
                     ok = false;
                     break;
                 }
-                if (!ptx::mbar_wait(&bars[L::kBarFull + i % kSlots], (i / kSlots) & 1, kWaitLimitNs)) ok = false;
+                if (!ptx::mbar_wait(&bars[L::kBarKFull + s], (t / kSlots) & 1, kWaitLimitNs)) ok = false;
                 // S(t) overwrites the P its buffer held: that PV must have completed
                 if (ok && before > 0 && !ptx::mbar_wait(&bars[L::kBarPFree + sb], (before - 1) & 1, kWaitLimitNs)) ok = false;
                 if (ok && t == ns) {
@@ -336,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
-                const uint64_t kd = kdesc0 + slot_off(i);
+                const uint64_t kd = kdesc0 + slot_off(t);
                 const uint32_t d = tmem + kTmemS8 + sb * kTile;
                 if (t < ns) {
 #pragma unroll
@@ -346,13 +419,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          id_qk16, kk > 0 ? 1u : 0u);
                 } else {
 #pragma unroll
-                    for (int kk = 0; kk < 16; ++kk) {  // eight 32-column steps of hi, then of lo
-                        const uint32_t off = (((kk & 7) >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                        ptx::mma_f8_ss(d, qdesc + off + static_cast<uint64_t>(kk < 8 ? 0 : (2 * L::kQChunkBytes) >> 4),
-                                       kd + off, id_qk, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 16; ++kk) {
+                        // 32 columns j of K against the first, then the second term of
+                        // Q's: 32 of the 64 bytes that their bf16 form took
+                        const int j = kk >> 1;
+                        const uint32_t qo = ((j >> 1) * L::kQChunkBytes + (j & 1) * 64 + (kk & 1) * 32) >> 4;
+                        const uint32_t ko = ((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4;
+                        ptx::mma_f8_ss(d, qdesc + qo, kd + ko, id_qk, kk > 0 ? 1u : 0u);
                     }
                 }
-                ptx::mma_commit(&bars[L::kBarEmpty + i % kSlots]);
+                ptx::mma_commit(&bars[L::kBarKEmpty + s]);
                 ptx::mma_commit(&bars[L::kBarSFull + sb]);
                 if (t > 0 && !pv_first && !issue_pv(t - 1)) ok = false;
             }
@@ -363,80 +439,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ================================================== softmax warps
-        const int q4 = warp & 3, hf = warp >> 2;
+        // The two groups take the tiles in turn, so that one group's waits and
+        // reductions run beside the other's exponentials.  Warp w of a group:
+        // lane quarter w % 4 (32 query rows), half w / 4 of its tiles' columns.
+        const int q4 = warp & 3, hf = (warp >> 2) & 1, grp = warp >> 3;
+        const int c4 = warp >> 2;  // column quarter of Q and of O
         const int row = q4 * 32 + lane;
         const int row_h = row / rph, row_j = row - row_h * rph;
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
         const uint8_t *mask_row = p.mask ? p.mask + static_cast<size_t>(b) * p.P : nullptr;
         const float *ksc = p.k_scale + static_cast<size_t>(unit) * p.nblk;
         const float *vsc = p.v_scale + static_cast<size_t>(unit) * p.nblk;
-        float *xmax = reinterpret_cast<float *>(smem + L::kXchgOff);  // [2 tile parity][2 half][128 rows]
-        float *xl = xmax + 2 * 2 * kMRows;                            // [2 half][128]
-        uint64_t *pair_bar = &bars[L::kBarPair + q4];
-        int pair_phase = 0;
-        auto pair_sync = [&]() -> bool {
+        float *xmax = reinterpret_cast<float *>(smem + L::kXchgOff) + grp * 2 * kMRows;  // [2 halves][128] of this group
+        float *mref = reinterpret_cast<float *>(smem + L::kXchgOff) + 4 * kMRows;        // [2 tile parity][128]
+        float *xl = mref + 2 * kMRows;                                                   // [4][128]
+        float *lim = xl + 4 * kMRows + warp * 64;  // this warp's columns: +inf visible, -inf hidden
+        uint64_t *row_bar = &bars[L::kBarRow + q4], *pair_bar = &bars[L::kBarPair + grp * 4 + q4];
+        uint64_t *max_bar = &bars[L::kBarMax + q4];
+        int row_phase = 0, pair_phase = 0;
+        auto row_sync = [&]() -> bool {  // the four warps of this lane quarter
+            ptx::mbar_arrive(row_bar);
+            return warp_wait(row_bar, row_phase++ & 1);
+        };
+        auto pair_sync = [&]() -> bool {  // the two of this group
             ptx::mbar_arrive(pair_bar);
-            const bool ok = warp_wait(pair_bar, pair_phase & 1);
-            ++pair_phase;
-            return ok;
+            return warp_wait(pair_bar, pair_phase++ & 1);
         };
         float sqs = 0.0f;  // this row's query scale * log2(e) / sqrt(D)
         if (T > 0) {
-            // ---- Q as two e4m3 terms, in place: this thread's half row (128 values)
+            // ---- Q as two e4m3 terms: this thread's 64 values of its row.  The 64
+            // bytes of 32 bf16 values become their 32 first terms, then their
+            // 32 second ones, so every thread rewrites only what it reads.
             failed = !warp_wait(&bars[L::kBarQFull], 0);
             if (!failed && ns > 0) failed = !warp_wait(&bars[L::kBarQFree], 0);
-            uint4 v[16];
-            uint32_t top = 0u;
-            uint8_t *qrow = smem + row * 128;
+            uint8_t *qrow = smem + c4 * L::kQChunkBytes + row * 128;
             const uint32_t sw = static_cast<uint32_t>(row & 7);
             if (!failed) {
-#pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    v[u] = *reinterpret_cast<const uint4 *>(qrow + (2 * hf + (u >> 3)) * L::kQChunkBytes +
-                                                            (((u & 7) ^ sw) << 4));
-                    top = __vmaxu2(top, v[u].x & 0x7fff7fffu);
-                    top = __vmaxu2(top, v[u].y & 0x7fff7fffu);
-                    top = __vmaxu2(top, v[u].z & 0x7fff7fffu);
-                    top = __vmaxu2(top, v[u].w & 0x7fff7fffu);
+                uint32_t top = 0u;
+#pragma unroll 4
+                for (int u = 0; u < 8; ++u) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(qrow + ((u ^ sw) << 4));
+                    top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
+                    top = __vmaxu2(top, v.w & 0x7fff7fffu);
                 }
-                xmax[hf * kMRows + row] = __uint_as_float(max(top & 0xffffu, top >> 16) << 16);
-                failed = !pair_sync();
+                xl[c4 * kMRows + row] = __uint_as_float(max(top & 0xffffu, top >> 16) << 16);
+                failed = !row_sync();
             }
             if (!failed) {
                 // magnitudes order like their bits; a row with a non-finite element becomes NaN
-                const float amax = __uint_as_float(max(__float_as_uint(xmax[row]), __float_as_uint(xmax[kMRows + row])));
+                uint32_t bits = 0u;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) bits = max(bits, __float_as_uint(xl[c * kMRows + row]));
+                const float amax = __uint_as_float(bits);
                 const float s = amax < INFINITY ? cache::pow2_scale(amax) : 1.0f;
                 const float inv = cache::pow2_inverse(s);
                 sqs = amax < INFINITY ? s * p.scale_log2 : __int_as_float(0x7fffffff);
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    uint4 *unit16[4];
+                    uint4 v[4];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint4 &src = v[2 * u + (e >> 1)];
-                        const uint32_t w0 = (e & 1) ? src.z : src.x, w1 = (e & 1) ? src.w : src.y;
-                        const uint32_t a = two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv);
-                        const uint32_t c = two_terms(__uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv);
-                        hi[e] = __byte_perm(a, c, 0x5410);
-                        lo[e] = __byte_perm(a, c, 0x7632);
+                    for (int u = 0; u < 4; ++u) {
+                        unit16[u] = reinterpret_cast<uint4 *>(qrow + (((g * 4 + u) ^ sw) << 4));
+                        v[u] = *unit16[u];
                     }
-                    uint8_t *dst = qrow + hf * L::kQChunkBytes + ((static_cast<uint32_t>(u) ^ sw) << 4);
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(dst + 2 * L::kQChunkBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint4 &src = v[e >> 1];
+                        const uint32_t w0 = (e & 1) ? src.z : src.x, w1 = (e & 1) ? src.w : src.y;
+                        two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
+                                  __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
+                    }
+                    *unit16[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *unit16[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                    *unit16[2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *unit16[3] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(&bars[L::kBarQConv]);
-                // xmax is read above and written again by tile 0: both halves are past it
-                failed = !pair_sync();
             }
         }
-        float m_used = -INFINITY;  // weights are 2^(z + log2 vs - m_used)
-        float l = 0.0f;            // this half's sum of p in the same units
-        // What tile t needs from global memory, one tile ahead: the mask bytes
-        // of this lane's columns, and (lanes 0-3) the scales of the half's
-        // four 16-column groups (a block never ends inside a group).
+        float m_l = -INFINITY;  // what this thread's sum refers to
+        float l = 0.0f;         // its sum of p, in units of 2^m_l
+        // What tile t needs from global memory, one of the group's tiles ahead:
+        // the mask bytes of this lane's two columns, and (lanes 0-3) the scales
+        // of the half's four 16-column groups (a block never ends inside one).
         uint32_t mask_next[2];
-        float ks_next = 1.0f, vs_next = 1.0f;
+        float ks_next, vs_next;
         auto load_next = [&](int t) {
             mask_next[0] = mask_next[1] = 1u;
             ks_next = vs_next = 1.0f;
@@ -455,85 +545,125 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vs_next = __ldg(vsc + ((r0 + c) >> p.shift));
             }
         };
-        load_next(0);
-        for (int t = 0; t < T && !failed; ++t) {
+        load_next(grp);
+        for (int t = grp; t < T && !failed; t += 2) {
             const int sb = buffer_of(t, ns), before = uses_before(t, ns);
             const uint32_t mask_cur[2] = {mask_next[0], mask_next[1]};
             float ks_cur = ks_next, vs_cur = vs_next;
-            load_next(t + 1);
-            if (!warp_wait(&bars[L::kBarSFull + sb], before & 1)) {
-                failed = true;
-                break;
-            }
-            ptx::tc_fence_after_sync();
-            const uint32_t scol = tmem + lane_base + kTmemS8 + sb * kTile;
+            load_next(t + 2);
             const int n = rows_of(t);
-            float hmax;
-            float s[64];
-            float ag[4], bg[4], ig[4];
             uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
-            if (t < ns) {
-                uint32_t raw[2][16];
-                ptx::tmem_ld16(scol + hf * 32, raw[0]);
-                ptx::tmem_ld16(scol + hf * 32 + 16, raw[1]);
-                ptx::tmem_ld_wait();
-                float m2[2] = {-INFINITY, -INFINITY};
+            float ag[4], bg[4], ig[4];
+            const bool partial = n < kTile || mask_row != nullptr;
+            if (t >= ns) {
+                if (partial) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    s[c] = hf * 32 + c < n ? __uint_as_float(raw[c >> 4][c & 15]) : -INFINITY;
-                    m2[c & 1] = fmaxf(m2[c & 1], s[c]);
-                }
-                hmax = fmaf(fmaxf(m2[0], m2[1]), p.scale_log2, -kSuffixBits);
-            } else {
-                uint32_t raw[4][16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) ptx::tmem_ld16(scol + hf * 64 + j * 16, raw[j]);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(raw[c >> 4][c & 15]);
-                if (n < kTile || mask_row != nullptr) {
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-                        vis[w] = __ballot_sync(0xffffffffu, hf * 64 + w * 32 + lane < n && mask_cur[w] != 0u);
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (!((vis[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
+                    for (int w = 0; w < 2; ++w) {
+                        const bool see = hf * 64 + w * 32 + lane < n && mask_cur[w] != 0u;
+                        vis[w] = __ballot_sync(0xffffffffu, see);
+                        lim[w * 32 + lane] = see ? INFINITY : -INFINITY;
+                    }
+                    __syncwarp();
                     // a group without a visible key may have any scale: it gets 1
                     const uint32_t mine = (lane & 2) ? vis[1] : vis[0];
                     if (((lane & 1) ? mine >> 16 : mine & 0xffffu) == 0u) ks_cur = vs_cur = 1.0f;
                 }
                 const float lv = ptx::lg2(vs_cur), iv = 1.0f / vs_cur;
-                hmax = -INFINITY;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     ag[g] = __shfl_sync(0xffffffffu, ks_cur, g) * sqs;
                     bg[g] = __shfl_sync(0xffffffffu, lv, g);
                     ig[g] = __shfl_sync(0xffffffffu, iv, g);
-                    float a = s[g * 16], c = s[g * 16 + 1];
-#pragma unroll
-                    for (int e = 2; e < 16; e += 2) {
-                        a = fmaxf(a, s[g * 16 + e]);
-                        c = fmaxf(c, s[g * 16 + e + 1]);
-                    }
-                    // rounding is monotone: this is the largest of the group's exponents
-                    hmax = fmaxf(hmax, fmaf(fmaxf(a, c), ag[g], bg[g]));
+                }
+            } else if (t > 0) {
+                // the second suffix tile follows the first in one buffer: its
+                // barrier's earlier phase is past once the first maximum is known
+                if (!warp_wait(max_bar, (t - 1) & 1)) {
+                    failed = true;
+                    break;
                 }
             }
-            xmax[((t & 1) * 2 + hf) * kMRows + row] = hmax;
+            if (!warp_wait(&bars[L::kBarSFull + sb], before & 1)) {
+                failed = true;
+                break;
+            }
+            ptx::tc_fence_after_sync();
+            const uint32_t scol = tmem + lane_base + kTmemS8 + sb * kTile + hf * (t < ns ? 32 : 64);
+            uint32_t raw[2][16];
+            float hmax = -INFINITY;
+            if (t < ns) {
+                ptx::tmem_ld16(scol, raw[0]);
+                ptx::tmem_ld16(scol + 16, raw[1]);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    uint32_t &x = raw[c >> 4][c & 15];
+                    if (hf * 32 + c >= n) x = 0xff800000u;
+                    hmax = fmaxf(hmax, __uint_as_float(x));
+                }
+                hmax = fmaf(hmax, p.scale_log2, -kSuffixBits);
+            } else {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    ptx::tmem_ld16(scol + w * 32, raw[0]);
+                    ptx::tmem_ld16(scol + w * 32 + 16, raw[1]);
+                    ptx::tmem_ld_wait();
+                    if (partial) {
+                        // min(x, -inf) is -inf for any x, NaN included
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(lim + w * 32 + c);
+                            const float fe[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t &x = raw[(c + e) >> 4][(c + e) & 15];
+                                x = __float_as_uint(fminf(__uint_as_float(x), fe[e]));
+                            }
+                        }
+                        ptx::tmem_st16(scol + w * 32, raw[0]);
+                        ptx::tmem_st16(scol + w * 32 + 16, raw[1]);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float a = __uint_as_float(raw[g][0]), c = __uint_as_float(raw[g][1]);
+#pragma unroll
+                        for (int e = 2; e < 14; e += 4) {
+                            a = ptx::max3(a, __uint_as_float(raw[g][e]), __uint_as_float(raw[g][e + 1]));
+                            c = ptx::max3(c, __uint_as_float(raw[g][e + 2]), __uint_as_float(raw[g][e + 3]));
+                        }
+                        a = ptx::max3(a, __uint_as_float(raw[g][14]), __uint_as_float(raw[g][15]));
+                        // rounding is monotone: this is the largest of the group's exponents
+                        hmax = fmaxf(hmax, fmaf(fmaxf(a, c), ag[w * 2 + g], bg[w * 2 + g]));
+                    }
+                }
+                if (partial) ptx::tmem_st_wait();
+            }
+            xmax[hf * kMRows + row] = hmax;
             if (!pair_sync()) {
                 failed = true;
                 break;
             }
-            const float tmax = fmaxf(hmax, xmax[((t & 1) * 2 + (hf ^ 1)) * kMRows + row]);
-            float factor = 1.0f;
-            bool rescale = false;
-            if (t == 0) {
-                m_used = tmax - kTopBits;
-            } else if (tmax > m_used + kMaxBits) {
-                factor = ptx::ex2(m_used - (tmax - kTopBits));  // 0 when m_used is -inf
-                rescale = true;
-                l *= factor;
-                m_used = tmax - kTopBits;
+            const float tmax = fmaxf(hmax, xmax[(hf ^ 1) * kMRows + row]);
+            // Tile t - 1's reference, from the other group.  The parity is exact:
+            // phase t - 2 completed before this group's S(t) could exist, and
+            // phase t needs this warp.
+            float m_old = -INFINITY;
+            if (t > 0) {
+                if (!warp_wait(max_bar, (t - 1) & 1)) {
+                    failed = true;
+                    break;
+                }
+                m_old = mref[((t - 1) & 1) * kMRows + row];
+            }
+            // weights of this tile are 2^(z + log2 vs - m_used)
+            const bool grow = t == 0 || tmax > m_old + kMaxBits;
+            const float m_used = grow ? tmax - kTopBits : m_old;
+            const bool rescale = grow && t > 0;
+            if (hf == 0) mref[(t & 1) * kMRows + row] = m_used;
+            ptx::mbar_arrive(max_bar);
+            if (m_l != m_used) {
+                if (l != 0.0f) l *= ptx::ex2(m_l - m_used);
+                m_l = m_used;
             }
             const float msub = m_used == -INFINITY ? 0.0f : m_used;
             if (t < ns) {
@@ -542,40 +672,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t pk[16];
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
-                    const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(ptx::f32x2(s[c], s[c + 1]), a2, c2));
+                    const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
+                        ptx::f32x2(__uint_as_float(raw[c >> 4][c & 15]), __uint_as_float(raw[c >> 4][(c & 15) + 1])), a2, c2));
                     const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
                     pk[c >> 1] = pack_bf16x2(p0, p1);
                     l2 = ptx::add_f32x2(l2, ptx::f32x2(p0, p1));
                 }
                 const float2 lp = ptx::unpack_f32x2(l2);
                 l += lp.x + lp.y;
-                ptx::tmem_st16(scol + hf * 16, pk);
+                ptx::tmem_st16(scol, pk);
             } else {
-                uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float cg = bg[g] - msub;
-                    const uint64_t a2 = ptx::f32x2(ag[g], ag[g]), c2 = ptx::f32x2(cg, cg);
-                    uint64_t l2 = ptx::f32x2(0.0f, 0.0f);
+                for (int w = 0; w < 2; ++w) {
+                    ptx::tmem_ld16(scol + w * 32, raw[0]);
+                    ptx::tmem_ld16(scol + w * 32 + 16, raw[1]);
+                    ptx::tmem_ld_wait();
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const int c = g * 16 + e;
-                        const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(ptx::f32x2(s[c], s[c + 1]), a2, c2));
-                        const float2 y = ptx::unpack_f32x2(ptx::fma_f32x2(ptx::f32x2(s[c + 2], s[c + 3]), a2, c2));
-                        const float w0 = ptx::ex2(x.x), w1 = ptx::ex2(x.y), w2 = ptx::ex2(y.x), w3 = ptx::ex2(y.y);
-                        l2 = ptx::add_f32x2(l2, ptx::f32x2(w0, w1));
-                        l2 = ptx::add_f32x2(l2, ptx::f32x2(w2, w3));
-                        const uint32_t u = two_terms(w0, w1), v = two_terms(w2, w3);
-                        hi[c >> 2] = __byte_perm(u, v, 0x5410);
-                        lo[c >> 2] = __byte_perm(u, v, 0x7632);
+                    for (int g = 0; g < 2; ++g) {
+                        const float cg = bg[w * 2 + g] - msub;
+                        const uint64_t a2 = ptx::f32x2(ag[w * 2 + g], ag[w * 2 + g]), c2 = ptx::f32x2(cg, cg);
+                        uint64_t l2 = ptx::f32x2(0.0f, 0.0f);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
+                                ptx::f32x2(__uint_as_float(raw[g][e]), __uint_as_float(raw[g][e + 1])), a2, c2));
+                            const float2 y = ptx::unpack_f32x2(ptx::fma_f32x2(
+                                ptx::f32x2(__uint_as_float(raw[g][e + 2]), __uint_as_float(raw[g][e + 3])), a2, c2));
+                            const float w0 = ptx::ex2(x.x), w1 = ptx::ex2(x.y), w2 = ptx::ex2(y.x), w3 = ptx::ex2(y.y);
+                            l2 = ptx::add_f32x2(l2, ptx::f32x2(w0, w1));
+                            l2 = ptx::add_f32x2(l2, ptx::f32x2(w2, w3));
+                            two_terms(w0, w1, w2, w3, hi[g * 4 + (e >> 2)], lo[g * 4 + (e >> 2)]);
+                        }
+                        const float2 lp = ptx::unpack_f32x2(l2);
+                        l = fmaf(lp.x + lp.y, ig[w * 2 + g], l);  // the weights without their scale
                     }
-                    const float2 lp = ptx::unpack_f32x2(l2);
-                    l = fmaf(lp.x + lp.y, ig[g], l);  // the weights without their scale
+                    // in the first 16 columns of the half for its first 32 keys, then
+                    // the next 16: where only this warp's own logits were
+                    ptx::tmem_st8(scol + w * 16, hi);
+                    ptx::tmem_st8(scol + w * 16 + 8, lo);
                 }
-                ptx::tmem_st16(scol + hf * 16, hi);
-                ptx::tmem_st16(scol + 32 + hf * 16, lo);
             }
-            if (t > 0 && __any_sync(0xffffffffu, rescale)) {
+            if (__any_sync(0xffffffffu, rescale)) {
                 // O holds the sum through PV(t-1) once that PV has completed; PV(t)
                 // waits for this warp's arrival below, so the parity is exact
                 if (!warp_wait(&bars[L::kBarPFree + buffer_of(t - 1, ns)], uses_before(t - 1, ns) & 1)) {
@@ -583,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 ptx::tc_fence_after_sync();
+                const float factor = rescale ? ptx::ex2(m_old - m_used) : 1.0f;  // 0 when m_old is -inf
 #pragma unroll 1
                 for (int j = 0; j < kHeadDim / 32; ++j) {
                     uint32_t o[16];
@@ -595,20 +734,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ptx::tmem_st_wait();
-            if (t >= ns) {
+            if (t >= ns && partial) {
                 // hidden rows, and rows past the valid length that the last
                 // 32-row step reads, may hold NaN codes, and 0 * NaN would
                 // poison O: they are cleared.  The half's four warps take them in turn.
-                const int left = (n + 31) / 32 * 32 - hf * 64;  // columns of this half that PV reads
+                const int left = (n + 31) / 32 * 32 - hf * 64;  // rows of this half that PV reads
                 uint64_t hidden = ~(static_cast<uint64_t>(vis[1]) << 32 | vis[0]);
                 hidden &= left <= 0 ? 0ull : left >= 64 ? ~0ull : (1ull << left) - 1ull;
                 if (hidden != 0ull) {
-                    const int i = 2 * t + 1;
-                    if (!warp_wait(&bars[L::kBarFull + i % kSlots], (i / kSlots) & 1)) {
+                    if (!warp_wait(&bars[L::kBarVFull + t % kSlots], (t / kSlots) & 1)) {
                         failed = true;
                         break;
                     }
-                    uint8_t *vt = slot_at(i) + hf * 64 * 128;
+                    uint8_t *vt = v_slot(t) + hf * 64 * 128;
                     for (int k = 0; hidden != 0ull; ++k, hidden &= hidden - 1ull) {
                         const int r = __ffsll(static_cast<long long>(hidden)) - 1;
                         if ((k & 3) == q4 && lane < 16)
@@ -622,24 +760,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_arrive(&bars[L::kBarPReady + sb]);
         }
 
-        const bool have_o = T > 0 && !failed;
-        if (have_o) {
-            if (!warp_wait(&bars[L::kBarPFree + buffer_of(T - 1, ns)], uses_before(T - 1, ns) & 1)) failed = true;
+        // The last reference, then the last PV (its barrier's earlier phase is
+        // past once the last tile's maximum is known).  Both warps of the pair
+        // have published their own last tile before the other group's is awaited.
+        float m_end = -INFINITY;
+        if (T > 0 && !failed) {
+            failed = !pair_sync() || !warp_wait(max_bar, (T - 1) & 1) ||
+                     !warp_wait(&bars[L::kBarPFree + buffer_of(T - 1, ns)], uses_before(T - 1, ns) & 1);
             ptx::tc_fence_after_sync();
+            m_end = mref[((T - 1) & 1) * kMRows + row];
+            if (l != 0.0f && m_l != m_end) l *= ptx::ex2(m_l - m_end);
         }
-        xl[hf * kMRows + row] = l;
-        if (!failed && !pair_sync()) failed = true;
-        const float l_row = l + xl[(hf ^ 1) * kMRows + row];
+        if (T == 0) {
+            // Q and an early tile still land in the shared memory used below
+            failed = !warp_wait(&bars[L::kBarQFull], 0) ||
+                     (first && (!warp_wait(&bars[L::kBarKFull], 0) || !warp_wait(&bars[L::kBarVFull], 0)));
+        }
+        const bool have_o = T > 0 && !failed;
+        xl[c4 * kMRows + row] = l;
+        if (!failed && !row_sync()) failed = true;
+        const float l_row = (xl[row] + xl[kMRows + row]) + (xl[2 * kMRows + row] + xl[3 * kMRows + row]);
         const bool row_valid = row_h < p.G && row_j < nq;
         const int row_k = row_h * nq + row_j;
         const size_t out_row = unit_row0 + static_cast<size_t>(row_h) * p.S + q0 + row_j;
-        const float inv_l = C == 1 ? 1.0f / l_row : 1.0f;
-        uint8_t *srow = smem + row * L::kStageStride;
+        const float inv_l = 1.0f / l_row;
+        // Rows leave through shared memory: a thread's columns of its row, then
+        // one bulk store of the whole row (16-byte stores of 32 rows at once
+        // took 5k cycles a CTA).
+        uint8_t *srow = smem + row * (C == 1 ? L::kOutStride : L::kStageStride);
         if (have_o && !failed) {
 #pragma unroll 1
-            for (int j = 0; j < kHeadDim / 64; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 uint32_t o[2][16];
-                const int col = hf * (kHeadDim / 2) + j * 32;
+                const int col = c4 * (kHeadDim / 4) + j * 32;
                 ptx::tmem_ld16(tmem + lane_base + kTmemO8 + col, o[0]);
                 ptx::tmem_ld16(tmem + lane_base + kTmemO8 + col + 16, o[1]);
                 ptx::tmem_ld_wait();
@@ -650,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 16; ++e)
                         w[e] = pack_bf16x2(__uint_as_float(o[e >> 3][2 * (e & 7)]) * inv_l,
                                            __uint_as_float(o[e >> 3][2 * (e & 7) + 1]) * inv_l);
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + out_row * kHeadDim + col);
+                    uint4 *dst = reinterpret_cast<uint4 *>(srow + col * 2);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                 } else {
@@ -662,25 +815,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (C == 1) {
-            if (hf == 0 && row_valid && p.lse != nullptr)
-                p.lse[out_row] = (m_used + ptx::lg2(l_row)) * 0.69314718055994531f;
-        } else {
-            if (row_valid) {
+        if (row_valid) {
+            if (C > 1 && c4 == 0) {
                 const float used = have_o && !failed ? l_row : 0.0f;
-                if (hf == 0)
-                    *reinterpret_cast<float4 *>(srow + kHeadDim * 4) = make_float4(m_used, used, used, 0.0f);
-                ptx::fence_proxy_async_smem();
+                *reinterpret_cast<float4 *>(srow + kHeadDim * 4) = make_float4(m_end, used, used, 0.0f);
             }
-            if (!failed && !pair_sync()) failed = true;  // both halves of the row staged
-            if (row_valid && hf == 0) {
+            ptx::fence_proxy_async_smem();
+        }
+        if (!failed && !row_sync()) failed = true;  // the whole row staged
+        if (row_valid && c4 == 0 && !failed) {
+            if (C == 1) {
+                ptx::bulk_store_s2g(p.out + out_row * kHeadDim, ptx::smem_addr(srow), kHeadDim * 2);
+                if (p.lse != nullptr) p.lse[out_row] = (m_end + ptx::lg2(l_row)) * 0.69314718055994531f;
+            } else {
                 const size_t prow = (static_cast<size_t>(cl) * C + rank) * (p.G * p.SQ) + row_k;
                 ptx::bulk_store_s2g(reinterpret_cast<uint8_t *>(p.part) + prow * L::kStageStride, ptx::smem_addr(srow),
                                     L::kStageStride);
-                ptx::bulk_commit();
-                ptx::bulk_wait_all();
-                ptx::fence_proxy_async_global();
             }
+            ptx::bulk_commit();
+            ptx::bulk_wait_all();
+            ptx::fence_proxy_async_global();
         }
     }
 
@@ -704,16 +858,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (nr > 0) {
             if (!warp_wait(&bars[L::kBarMerge], 0)) failed = true;
-            merge_weights<L>(smem, C, nr, p.lse, unit_row0, r_lo, nq, p.S, q0, nq, orow_s);
+            merge_weights<L, kThreads8>(smem, C, nr, p.lse, unit_row0, r_lo, nq, p.S, q0, nq, orow_s);
             __syncthreads();
-            merge_rows<L>(smem, C, nr, p.out, orow_s);
+            merge_rows<L, kThreads8>(smem, C, nr, p.out, orow_s);
         }
     }
     if (failed) atomicOr(p.err, kEwTimeout);
     __syncwarp();
     ptx::tc_fence_before_sync();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kIssueWarp) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }

@@ -91,7 +91,7 @@ int kv8_state(const Device &dev, Kv8State *out) noexcept
             for (int c = dm05::kMaxSplits; c >= 2; --c) {
                 cudaLaunchConfig_t cfg = {};
                 cfg.gridDim = dim3(static_cast<unsigned>(c), 1, 1);
-                cfg.blockDim = dim3(dm05::kThreads, 1, 1);
+                cfg.blockDim = dim3(dm05::kv8::kThreads8, 1, 1);
                 cfg.dynamicSmemBytes = dm05::kv8::Smem::kAllocBytes;
                 cudaLaunchAttribute at[1];
                 at[0].id = cudaLaunchAttributeClusterDimension;
@@ -389,7 +389,7 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     ap.scale_log2 = static_cast<float>(kLog2e / std::sqrt(static_cast<double>(D)));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(dm05::kThreads, 1, 1);
+    cfg.blockDim = dim3(dm05::kv8::kThreads8, 1, 1);
     cfg.dynamicSmemBytes = dm05::kv8::Smem::kAllocBytes;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
