@@ -85,6 +85,14 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
+// a * b, lane-wise, rounded to nearest
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // The largest of three (a NaN operand is passed over).
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -199,6 +207,57 @@ __device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3
         "mov.b32 %1, {l0, l1};\n\t}"
         : "=r"(hi), "=r"(lo)
         : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
+}
+
+// A query row is cut into four chunks of 64 bf16 (128 swizzled bytes each;
+// sw: the row's swizzle).  Largest magnitude of one chunk of a row, as bf16
+// bits: magnitudes order like their bits.
+__device__ __forceinline__ uint32_t chunk_max(const uint8_t *chunk, uint32_t sw)
+{
+    uint32_t top = 0u;
+#pragma unroll 4
+    for (int u = 0; u < 8; ++u) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(chunk + ((u ^ sw) << 4));
+        top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
+        top = __vmaxu2(top, v.w & 0x7fff7fffu);
+    }
+    return max(top & 0xffffu, top >> 16);
+}
+
+// Power-of-two scale of a query row whose largest element has these bf16
+// bits, so that the scaled row's largest element lies in (224, 448].
+__device__ __forceinline__ float row_scale(uint32_t bits)
+{
+    return bits < 0x7f80u ? cache::pow2_scale(__uint_as_float(bits << 16)) : 1.0f;
+}
+
+// Rewrites one chunk of a scaled row as two e4m3 terms: the 64 bytes of 32
+// bf16 values become their 32 first terms, then their 32 second ones, so a
+// thread rewrites only what it has read.
+__device__ __forceinline__ void split_chunk(uint8_t *chunk, uint32_t sw, float inv)
+{
+#pragma unroll 1
+    for (int g = 0; g < 2; ++g) {
+        uint4 *unit16[4];
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            unit16[u] = reinterpret_cast<uint4 *>(chunk + (((g * 4 + u) ^ sw) << 4));
+            v[u] = *unit16[u];
+        }
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint4 &src = v[e >> 1];
+            const uint32_t w0 = (e & 1) ? src.z : src.x, w1 = (e & 1) ? src.w : src.y;
+            two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
+                      __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
+        }
+        *unit16[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *unit16[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+        *unit16[2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *unit16[3] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads8, 1)
@@ -467,55 +526,21 @@ __global__ void __launch_bounds__(kThreads8, 1)
         };
         float sqs = 0.0f;  // this row's query scale * log2(e) / sqrt(D)
         if (T > 0) {
-            // ---- Q as two e4m3 terms: this thread's 64 values of its row.  The 64
-            // bytes of 32 bf16 values become their 32 first terms, then their
-            // 32 second ones, so every thread rewrites only what it reads.
+            // ---- Q as two e4m3 terms: this thread's 64 values of its row
             failed = !warp_wait(&bars[L::kBarQFull], 0);
             if (!failed && ns > 0) failed = !warp_wait(&bars[L::kBarQFree], 0);
-            uint8_t *qrow = smem + c4 * L::kQChunkBytes + row * 128;
-            const uint32_t sw = static_cast<uint32_t>(row & 7);
+            uint8_t *chunk = smem + c4 * L::kQChunkBytes + row * 128;
+            uint32_t *qmax = reinterpret_cast<uint32_t *>(xl) + row;  // [4][128]
             if (!failed) {
-                uint32_t top = 0u;
-#pragma unroll 4
-                for (int u = 0; u < 8; ++u) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(qrow + ((u ^ sw) << 4));
-                    top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
-                    top = __vmaxu2(top, v.w & 0x7fff7fffu);
-                }
-                xl[c4 * kMRows + row] = __uint_as_float(max(top & 0xffffu, top >> 16) << 16);
+                qmax[c4 * kMRows] = chunk_max(chunk, row & 7);
                 failed = !row_sync();
             }
             if (!failed) {
-                // magnitudes order like their bits; a row with a non-finite element becomes NaN
-                uint32_t bits = 0u;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) bits = max(bits, __float_as_uint(xl[c * kMRows + row]));
-                const float amax = __uint_as_float(bits);
-                const float s = amax < INFINITY ? cache::pow2_scale(amax) : 1.0f;
-                const float inv = cache::pow2_inverse(s);
-                sqs = amax < INFINITY ? s * p.scale_log2 : __int_as_float(0x7fffffff);
-#pragma unroll 1
-                for (int g = 0; g < 2; ++g) {
-                    uint4 *unit16[4];
-                    uint4 v[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        unit16[u] = reinterpret_cast<uint4 *>(qrow + (((g * 4 + u) ^ sw) << 4));
-                        v[u] = *unit16[u];
-                    }
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint4 &src = v[e >> 1];
-                        const uint32_t w0 = (e & 1) ? src.z : src.x, w1 = (e & 1) ? src.w : src.y;
-                        two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
-                                  __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
-                    }
-                    *unit16[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *unit16[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                    *unit16[2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    *unit16[3] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-                }
+                const uint32_t bits = max(max(qmax[0], qmax[kMRows]), max(qmax[2 * kMRows], qmax[3 * kMRows]));
+                const float s = row_scale(bits);
+                // a row with a non-finite element becomes NaN
+                sqs = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
+                split_chunk(chunk, row & 7, cache::pow2_inverse(s));
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(&bars[L::kBarQConv]);
             }

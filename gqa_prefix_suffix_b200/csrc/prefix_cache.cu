@@ -194,6 +194,45 @@ int encode_rows16_chunk(CUtensorMap *map, const void *base, int rows, int units,
     return dm05::internal::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box);
 }
 
+// ---------------------------------------------------------------- accumulated weight
+
+bool g_mass_ready[kMaxDevices];  // guarded by g_kv8_mu
+
+int mass_attributes(const Device &dev) noexcept
+{
+    if (dev.ordinal < 0 || dev.ordinal >= kMaxDevices) return DM05_ERR_CUDA;
+    try {
+        std::lock_guard<std::mutex> lk(g_kv8_mu);
+        if (g_mass_ready[dev.ordinal]) return DM05_OK;
+        if (cudaFuncSetAttribute(&dm05::mass::mass_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dm05::mass::Smem<false>::kAllocBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(&dm05::mass::mass_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dm05::mass::Smem<true>::kAllocBytes) != cudaSuccess)
+            return DM05_ERR_CUDA;
+        g_mass_ready[dev.ordinal] = true;
+        return DM05_OK;
+    } catch (...) {
+        return DM05_ERR_CUDA;
+    }
+}
+
+// CTAs per unit: the fewest waves x (set-up + tiles a CTA walks), set-up
+// counted as two tiles.
+int mass_splits(int units, int tiles, int num_sms)
+{
+    int best = 1;
+    long long best_cost = -1;
+    for (int s = 1; s <= std::min(tiles, num_sms); ++s) {
+        const long long waves = (static_cast<long long>(units) * s + num_sms - 1) / num_sms;
+        const long long cost = waves * (2 + (tiles + s - 1) / s);
+        if (best_cost < 0 || cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 int mass_call(bool kv8, const void *q, const void *k, const float *k_scale, int shift, const int32_t *valid_len,
               const uint8_t *mask, const float *lse, const float *mass_in, float *mass, int B, int Hq, int Hkv, int P,
               int S, int D, cudaStream_t stream)
@@ -210,9 +249,14 @@ int mass_call(bool kv8, const void *q, const void *k, const float *k_scale, int 
     Device dev;
     rc = dm05::internal::device(stream, true, &dev);
     if (rc != DM05_OK) return rc;
+    if ((rc = mass_attributes(dev)) != DM05_OK) return rc;
+    const int units = B * Hkv, GS = Hq / Hkv * S, N = (GS + 15) / 16 * 16;
+    CUtensorMap tq, tk;
+    if (encode_rows16(&tq, q, GS, units, N) != DM05_OK ||
+        (kv8 ? encode_rows8(&tk, k, P, units, dm05::mass::kTile) : encode_rows16(&tk, k, P, units, dm05::mass::kTile)) !=
+            DM05_OK)
+        return DM05_ERR_CUDA;
     dm05::mass::Params mp = {};
-    mp.q = static_cast<const __nv_bfloat16 *>(q);
-    mp.k = static_cast<const uint8_t *>(k);
     mp.k_scale = k_scale;
     mp.lse = lse;
     mp.valid_len = valid_len;
@@ -222,13 +266,25 @@ int mass_call(bool kv8, const void *q, const void *k, const float *k_scale, int 
     mp.err = dev.err;
     mp.Hkv = Hkv;
     mp.P = P;
-    mp.GS = Hq / Hkv * S;
+    mp.GS = GS;
+    mp.N = N;
     mp.nblk = blocks_of(P, shift);
     mp.shift = shift;
     mp.scale_log2 = static_cast<float>(kLog2e / std::sqrt(static_cast<double>(D)));
-    const dim3 grid(static_cast<unsigned>((P + 7) / 8), static_cast<unsigned>(B * Hkv));
-    return kv8 ? launch(dm05::mass::mass_kernel<true>, grid, 256, 0, stream, mp)
-               : launch(dm05::mass::mass_kernel<false>, grid, 256, 0, stream, mp);
+    const int splits = mass_splits(units, (P + dm05::mass::kTile - 1) / dm05::mass::kTile, dev.num_sms);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(units), 1);
+    cfg.blockDim = dim3(dm05::mass::kThreadsM, 1, 1);
+    cfg.dynamicSmemBytes = kv8 ? dm05::mass::Smem<true>::kAllocBytes : dm05::mass::Smem<false>::kAllocBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = kv8 ? cudaLaunchKernelEx(&cfg, &dm05::mass::mass_kernel<true>, tq, tk, mp)
+                              : cudaLaunchKernelEx(&cfg, &dm05::mass::mass_kernel<false>, tq, tk, mp);
+    return e == cudaSuccess ? DM05_OK : DM05_ERR_CUDA;
 }
 
 int evict_checks(const void *k, const void *v, const float *mass, const int32_t *valid_len, const void *k_out,

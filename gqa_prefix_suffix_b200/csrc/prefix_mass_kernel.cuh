@@ -1,63 +1,297 @@
-// prefix_mass_kernel.cuh -- the attention weight each prefix position
-// received: mass[j] = mass_in[j] + sum over a KV head's query heads and the
-// S queries of exp(<q, k_j> / sqrt(D) - lse).
+// prefix_mass_kernel.cuh -- sm_100a kernel of the attention weight that each
+// prefix position received:
+//   mass[j] = mass_in[j] + sum_i exp(<q_i, k_j> / sqrt(D) - lse_i)
+// over the GS query rows i of a (sample, KV head) unit.
+//
+// With the logits transposed, S^T = K Q^T, a tile of 128 keys is the MMA's M
+// and the unit's query rows are its N: every thread then owns one key and
+// sums along its row, without a reduction over lanes, and a hidden key's
+// garbage stays in its own row.  No maximum is needed (the lse is given), so
+// a tile is one matrix product, one exponential a logit, and one sum.
+// The queries stay in shared memory for all of a CTA's tiles; the tiles of a
+// unit are dealt to CTAs in contiguous runs, each key to exactly one, so
+// the result has one order of sums and no atomics.
+//
+// A bf16 cache multiplies in kind::f16 (64 KB a tile); an 8-bit one in
+// kind::f8f6f4 straight from its codes (32 KB), with the query rows as two
+// e4m3 terms of their scaled values as in the 8-bit attention, the scales of
+// key and query applied in the exponent.
+//
+// Warp roles: warp 16 loads, warp 17 issues the MMAs, warps 0-15 take the
+// logits (four warps per 32 keys, each the 16-column groups c, c + 4).  Four
+// logit buffers of 128 columns fill the tensor memory, so the MMAs run ahead.
 #pragma once
 
-#include "prefix_cache_kernels.cuh"
+#include "kv8_attn_kernel.cuh"
 
 namespace dm05 {
 namespace mass {
 
+constexpr int kTile = 128;     // keys of a tile
+constexpr int kSoftWarps = 16;
+constexpr int kLoadWarp = 16;
+constexpr int kIssueWarp = 17;
+constexpr int kThreadsM = 576;
+constexpr int kBufs = 4;       // logit buffers of 128 columns
+
+template <bool KV8>
+struct Smem {
+    static constexpr int kQBytes = 65536;
+    static constexpr int kSlotBytes = KV8 ? 32768 : 65536;
+    static constexpr int kSlots = KV8 ? 4 : 2;
+    static constexpr int kRing = kQBytes;
+    static constexpr int kBarOff = kRing + kSlots * kSlotBytes;
+    static constexpr int kBarQFull = 0;
+    static constexpr int kBarQReady = 1;   // query rows split (8-bit), row constants written
+    static constexpr int kBarFull = 2;
+    static constexpr int kBarEmpty = kBarFull + kSlots;
+    static constexpr int kBarSFull = kBarEmpty + kSlots;
+    static constexpr int kBarSFree = kBarSFull + kBufs;
+    static constexpr int kBarRow = kBarSFree + kBufs;
+    static constexpr int kBarFinal = kBarRow + 4;
+    static constexpr int kNumBars = kBarFinal + 1;
+    static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
+    // per query row {scale, -lse log2(e)}, then partial sums [2 parities][4][128]
+    static constexpr int kRowOff = (kTmemSlotOff + 16 + 15) / 16 * 16;
+    static constexpr int kSumOff = kRowOff + 128 * 8;
+    static constexpr int kEnd = kSumOff + 8 * 128 * 4;
+    static constexpr int kAllocBytes = kEnd + 1024;
+    static_assert(kAllocBytes <= 232448, "shared memory of a CTA");
+};
+
 struct Params {
-    const __nv_bfloat16 *q;  // [units, GS, 256]
-    const uint8_t *k;        // [units, P, 256] bf16 or e4m3
     const float *k_scale;    // 8-bit: [units, nblk]
     const float *lse;        // [units, GS]
     const int32_t *valid_len;
-    const uint8_t *mask;
-    const float *mass_in;    // or nullptr
-    float *mass;
+    const uint8_t *mask;     // [B, P] or nullptr
+    const float *mass_in;    // [units, P] or nullptr
+    float *mass;             // [units, P]
     uint32_t *err;
-    int Hkv, P, GS, nblk, shift;
+    int Hkv, P, GS, N;       // N: GS rounded up to 16, the MMA's N
+    int nblk, shift;
     float scale_log2;
 };
 
-// One warp per key.
 template <bool KV8>
-__global__ void __launch_bounds__(256) mass_kernel(const Params p)
+__global__ void __launch_bounds__(kThreadsM, 1)
+    mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const Params p)
 {
+    using L = Smem<KV8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemSlotOff);
+    float2 *rows = reinterpret_cast<float2 *>(smem + L::kRowOff);
+    float *sums = reinterpret_cast<float *>(smem + L::kSumOff);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = blockIdx.y, b = unit / p.Hkv;
-    const int lane = threadIdx.x & 31, j = blockIdx.x * 8 + (threadIdx.x >> 5);
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int vl = cache::clamped_len(p.valid_len, b, p.P, p.err, threadIdx.x == 0 && blockIdx.x == 0 && unit % p.Hkv == 0);
-    if (j >= p.P) return;
-    const size_t at = static_cast<size_t>(unit) * p.P + j;
-    const bool seen = j < vl && (p.mask == nullptr || p.mask[static_cast<size_t>(b) * p.P + j] != 0);
-    float total = p.mass_in != nullptr ? p.mass_in[at] : 0.0f;
-    if (seen) {
-        float k[8];
-        if (KV8) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(p.k + at * 256 + lane * 8);
-            const float s = p.k_scale[static_cast<size_t>(unit) * p.nblk + (j >> p.shift)];
-            const float4 a = cache::decode4(w.x), c = cache::decode4(w.y);
-            const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-            for (int e = 0; e < 8; ++e) k[e] = v[e] * s;
-        } else {
-            const __nv_bfloat16 *row = reinterpret_cast<const __nv_bfloat16 *>(p.k) + at * 256 + lane * 8;
-            for (int e = 0; e < 8; ++e) k[e] = __bfloat162float(row[e]);
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&bars[L::kBarQFull], 1);
+        ptx::mbar_init(&bars[L::kBarQReady], kSoftWarps * 32);
+        for (int i = 0; i < L::kSlots; ++i) {
+            ptx::mbar_init(&bars[L::kBarFull + i], 1);
+            ptx::mbar_init(&bars[L::kBarEmpty + i], 1);
         }
-        for (int i = 0; i < p.GS; ++i) {
-            const size_t qi = static_cast<size_t>(unit) * p.GS + i;
-            const __nv_bfloat16 *row = p.q + qi * 256 + lane * 8;
-            float dot = 0.0f;
-            for (int e = 0; e < 8; ++e) dot = fmaf(__bfloat162float(row[e]), k[e], dot);
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            const float l = p.lse[qi];
-            if (l != -INFINITY) total += exp2f(dot * p.scale_log2 - l * 1.4426950408889634f);
+        for (int i = 0; i < kBufs; ++i) {
+            ptx::mbar_init(&bars[L::kBarSFull + i], 1);
+            ptx::mbar_init(&bars[L::kBarSFree + i], kSoftWarps * 32);
         }
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&bars[L::kBarRow + i], 128);
+        ptx::mbar_init(&bars[L::kBarFinal], 1);
+        ptx::fence_mbar_init();
     }
-    if (lane == 0) p.mass[at] = total;
+    if (warp == kLoadWarp && lane == 0) {
+        ptx::prefetch_tensormap(&tm_q);
+        ptx::prefetch_tensormap(&tm_k);
+    }
+    if (warp == kIssueWarp) {
+        ptx::tmem_alloc(tmem_slot, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_launch_dependents();
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    ptx::griddep_wait();
+
+    const int vl = cache::clamped_len(p.valid_len, b, p.P, p.err,
+                                      threadIdx.x == 0 && blockIdx.x == 0 && unit % p.Hkv == 0);
+    const int t_in = (vl + kTile - 1) / kTile;
+    // this CTA's run of the tiles in range, and its share of the rest (whose
+    // mass is only carried over)
+    const int t0 = static_cast<int>(static_cast<long long>(t_in) * blockIdx.x / gridDim.x);
+    const int T = static_cast<int>(static_cast<long long>(t_in) * (blockIdx.x + 1) / gridDim.x) - t0;
+    bool failed = false;
+
+    if (warp == kLoadWarp) {
+        if (lane == 0 && T > 0) {
+            const uint64_t pol = ptx::policy_evict_first();
+            ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(p.N) * 512u);
+            ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, 0, 0, unit);
+            int issued = 0;
+            for (int t = 0; t < T; ++t) {
+                const int s = t % L::kSlots, n = t / L::kSlots;
+                if (n > 0 && !ptx::mbar_wait(&bars[L::kBarEmpty + s], (n - 1) & 1, kWaitLimitNs)) {
+                    failed = true;
+                    break;
+                }
+                ptx::mbar_arrive_expect_tx(&bars[L::kBarFull + s], L::kSlotBytes);
+                ptx::tma_load_4d_hint(smem + L::kRing + s * L::kSlotBytes, &tm_k, &bars[L::kBarFull + s], 0,
+                                      (t0 + t) * kTile, 0, unit, pol);
+                issued = t + 1;
+            }
+            // every copy this thread issued has landed before the CTA may exit
+            if (!ptx::mbar_wait(&bars[L::kBarQFull], 0, kWaitLimitNs)) failed = true;
+            for (int t = max(0, issued - L::kSlots); t < issued; ++t)
+                if (!ptx::mbar_wait(&bars[L::kBarFull + t % L::kSlots], (t / L::kSlots) & 1, kWaitLimitNs)) failed = true;
+        }
+    } else if (warp == kIssueWarp) {
+        if (lane == 0 && T > 0) {
+            const int qpitch = p.N * 128;  // bytes of a 64-column chunk of the query rows
+            const uint32_t idesc = KV8 ? ptx::idesc_e4m3_f32(kTile, p.N, false) : ptx::idesc_bf16_f32(kTile, p.N, false);
+            const uint64_t qdesc = ptx::sw128_desc(ptx::smem_addr(smem), 16, 1024);
+            const uint64_t kdesc = ptx::sw128_desc(ptx::smem_addr(smem + L::kRing), 16, 1024);
+            bool ok = ptx::mbar_wait(&bars[L::kBarQFull], 0, kWaitLimitNs) &&
+                      ptx::mbar_wait(&bars[L::kBarQReady], 0, kWaitLimitNs);
+            for (int t = 0; t < T && ok; ++t) {
+                const int s = t % L::kSlots, sb = t % kBufs;
+                ok = ptx::mbar_wait(&bars[L::kBarFull + s], (t / L::kSlots) & 1, kWaitLimitNs) &&
+                     (t < kBufs || ptx::mbar_wait(&bars[L::kBarSFree + sb], (t / kBufs - 1) & 1, kWaitLimitNs));
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                const uint64_t kd = kdesc + static_cast<uint64_t>((s * L::kSlotBytes) >> 4);
+                const uint32_t d = tmem + sb * 128;
+#pragma unroll
+                for (int kk = 0; kk < 16; ++kk) {
+                    if (KV8) {
+                        // 32 columns j against both terms of the queries
+                        const int j = kk >> 1;
+                        const uint32_t qo = ((j >> 1) * qpitch + (j & 1) * 64 + (kk & 1) * 32) >> 4;
+                        const uint32_t ko = ((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4;
+                        ptx::mma_f8_ss(d, kd + ko, qdesc + qo, idesc, kk > 0 ? 1u : 0u);
+                    } else {
+                        const uint32_t qo = ((kk >> 2) * qpitch + (kk & 3) * 32) >> 4;
+                        const uint32_t ko = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+                        ptx::mma_bf16_ss(d, kd + ko, qdesc + qo, idesc, kk > 0 ? 1u : 0u);
+                    }
+                }
+                ptx::mma_commit(&bars[L::kBarEmpty + s]);
+                ptx::mma_commit(&bars[L::kBarSFull + sb]);
+            }
+            // every MMA issued above has completed before tensor memory is freed
+            ptx::mma_commit(&bars[L::kBarFinal]);
+            if (!ptx::mbar_wait(&bars[L::kBarFinal], 0, kWaitLimitNs)) ok = false;
+            failed = !ok;
+        }
+    } else {
+        const int q4 = warp & 3, c4 = warp >> 2;
+        const int row = q4 * 32 + lane;  // a key of the tile; a query row while those are prepared
+        const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+        uint64_t *row_bar = &bars[L::kBarRow + q4];
+        int row_phase = 0;
+        auto row_sync = [&]() -> bool {  // the four warps of these 32 rows
+            ptx::mbar_arrive(row_bar);
+            return warp_wait(row_bar, row_phase++ & 1);
+        };
+        if (T > 0) {
+            // ---- query rows: their constants, and the two terms for an 8-bit cache
+            float scale = p.scale_log2;
+            if (KV8) {
+                failed = !warp_wait(&bars[L::kBarQFull], 0);
+                uint8_t *chunk = smem + c4 * p.N * 128 + row * 128;
+                uint32_t *qmax = reinterpret_cast<uint32_t *>(sums) + row;  // [4][128]
+                if (!failed) {
+                    qmax[c4 * 128] = row < p.N ? kv8::chunk_max(chunk, row & 7) : 0u;
+                    failed = !row_sync();
+                }
+                if (!failed) {
+                    const uint32_t bits = max(max(qmax[0], qmax[128]), max(qmax[256], qmax[384]));
+                    const float s = kv8::row_scale(bits);
+                    // a row with a non-finite element becomes NaN
+                    scale = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
+                    if (row < p.N) kv8::split_chunk(chunk, row & 7, cache::pow2_inverse(s));
+                    ptx::fence_proxy_async_smem();
+                    failed = !row_sync();  // qmax is read: the sums may be written
+                }
+            }
+            if (c4 == 0) {
+                // rows that do not exist, and rows that saw no key (-inf), add 2^-inf
+                float l = INFINITY;
+                if (row < p.GS) l = __ldg(p.lse + static_cast<size_t>(unit) * p.GS + row);
+                if (l == -INFINITY) l = INFINITY;
+                rows[row] = make_float2(scale, -l * 1.4426950408889634f);
+            }
+            ptx::mbar_arrive(&bars[L::kBarQReady]);
+            if (!failed) failed = !warp_wait(&bars[L::kBarQReady], 0);
+        }
+        const int groups = p.N >> 4;
+        const size_t unit_key0 = static_cast<size_t>(unit) * p.P;
+        for (int t = 0; t < T && !failed; ++t) {
+            const int sb = t % kBufs;
+            const int j = (t0 + t) * kTile + row;
+            // what the last step needs of global memory, requested before the wait
+            float before = 0.0f, ks = 1.0f;
+            bool see = j < vl;
+            if (KV8 && see) ks = __ldg(p.k_scale + static_cast<size_t>(unit) * p.nblk + (j >> p.shift));
+            if (c4 == 0 && j < p.P) {
+                if (p.mass_in != nullptr) before = p.mass_in[unit_key0 + j];
+                if (see && p.mask != nullptr) see = __ldg(p.mask + static_cast<size_t>(b) * p.P + j) != 0;
+            }
+            if (!warp_wait(&bars[L::kBarSFull + sb], (t / kBufs) & 1)) {
+                failed = true;
+                break;
+            }
+            ptx::tc_fence_after_sync();
+            uint32_t raw[2][16];
+            const uint32_t col = tmem + lane_base + sb * 128;
+            const bool one = c4 < groups, two = c4 + 4 < groups;
+            if (one) ptx::tmem_ld16(col + c4 * 16, raw[0]);
+            if (two) ptx::tmem_ld16(col + c4 * 16 + 64, raw[1]);
+            ptx::tmem_ld_wait();
+            ptx::tc_fence_before_sync();
+            ptx::mbar_arrive(&bars[L::kBarSFree + sb]);
+            uint64_t acc[2] = {ptx::f32x2(0.0f, 0.0f), ptx::f32x2(0.0f, 0.0f)};
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (g == 0 ? !one : !two) break;
+                const float4 *rc = reinterpret_cast<const float4 *>(rows + (c4 + 4 * g) * 16);
+                const uint64_t ks2 = ptx::f32x2(ks, ks);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float4 r = rc[e >> 1];  // {scale, -lse} of two query rows
+                    uint64_t f = ptx::f32x2(r.x, r.z);
+                    if (KV8) f = ptx::mul_f32x2(f, ks2);
+                    const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
+                        ptx::f32x2(__uint_as_float(raw[g][e]), __uint_as_float(raw[g][e + 1])), f, ptx::f32x2(r.y, r.w)));
+                    acc[(e >> 1) & 1] = ptx::add_f32x2(acc[(e >> 1) & 1], ptx::f32x2(ptx::ex2(x.x), ptx::ex2(x.y)));
+                }
+            }
+            const float2 s2 = ptx::unpack_f32x2(ptx::add_f32x2(acc[0], acc[1]));
+            float *xs = sums + (t & 1) * 4 * 128 + row;
+            if (c4 != 0) xs[c4 * 128] = s2.x + s2.y;
+            if (!row_sync()) {
+                failed = true;
+                break;
+            }
+            if (c4 == 0 && j < p.P)
+                p.mass[unit_key0 + j] = see ? before + (((s2.x + s2.y) + xs[128]) + (xs[256] + xs[384])) : before;
+        }
+        // positions past the tiles in range keep what they had
+        const int first = t_in * kTile;
+        for (long long j = first + static_cast<long long>(blockIdx.x) * (kSoftWarps * 32) + threadIdx.x; j < p.P;
+             j += static_cast<long long>(gridDim.x) * (kSoftWarps * 32))
+            p.mass[unit_key0 + j] = p.mass_in != nullptr ? p.mass_in[unit_key0 + j] : 0.0f;
+    }
+    if (failed) atomicOr(p.err, kEwTimeout);
+    __syncwarp();
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kIssueWarp) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, 512);
+    }
 }
 
 }  // namespace mass
