@@ -312,10 +312,12 @@ def dm05_suffix_attn_plan(B, Hq, Hkv, P, S, D):
 
 
 def dm05_set_split_override(splits_per_head: int) -> int:
+    _kv8_workspace_bytes.clear()
     return lib().dm05_set_split_override(splits_per_head)
 
 
 def dm05_set_row_block_override(row_blocks: int) -> int:
+    _kv8_workspace_bytes.clear()
     return lib().dm05_set_row_block_override(row_blocks)
 
 
@@ -547,64 +549,84 @@ class EvictedPrefixKv8(NamedTuple):
     valid_len: "torch.Tensor"
 
 
-def _need(name, t, dtype, shape, device):
-    """A dense CUDA tensor of this type and shape on `device`, or ValueError."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {list(shape)} on {device}")
+def _need(name, t, dtype, shape, index):
+    """A dense tensor of this type and shape on CUDA device `index`, or ValueError."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != index or index < 0 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {list(shape)}"
+                         + (f" on cuda:{index}" if index >= 0 else ""))
 
 
-def _need_prefix(valid_len, mask, B, P, device):
+def _need_prefix(valid_len, mask, B, P, index):
     import torch
     if valid_len is not None:
-        _need("prefix_valid_len", valid_len, torch.int32, (B,), device)
+        _need("prefix_valid_len", valid_len, torch.int32, (B,), index)
     if mask is not None:
-        _need("prefix_mask", mask, torch.uint8, (B, P), device)
+        _need("prefix_mask", mask, torch.uint8, (B, P), index)
 
 
-def _need_cache(name, cache, device=None):
+def _need_cache(name, cache, index):
     """Checks an 8-bit cache; returns its (B, Hkv, P, D)."""
     import torch
-    if cache.k.dim() != 4:
+    k, v, ks, vs, block = cache
+    if k.dim() != 4:
         raise ValueError(f"{name}.k must be [B,Hkv,P,D]")
-    B, Hkv, P, D = cache.k.shape
-    if cache.block not in (16, 32, 64, 128):
+    shape = k.shape
+    B, Hkv, P, D = shape
+    if block not in (16, 32, 64, 128):
         raise ValueError(f"{name}.block must be 16, 32, 64 or 128")
-    device = cache.k.device if device is None else device
-    scales = (B, Hkv, -(-P // cache.block))
-    _need(f"{name}.k", cache.k, torch.float8_e4m3fn, (B, Hkv, P, D), device)
-    _need(f"{name}.v", cache.v, torch.float8_e4m3fn, (B, Hkv, P, D), device)
-    _need(f"{name}.k_scale", cache.k_scale, torch.float32, scales, device)
-    _need(f"{name}.v_scale", cache.v_scale, torch.float32, scales, device)
+    scales = (B, Hkv, -(-P // block))
+    _need(f"{name}.k", k, torch.float8_e4m3fn, shape, index)
+    _need(f"{name}.v", v, torch.float8_e4m3fn, shape, index)
+    _need(f"{name}.k_scale", ks, torch.float32, scales, index)
+    _need(f"{name}.v_scale", vs, torch.float32, scales, index)
     return B, Hkv, P, D
 
 
-@contextlib.contextmanager
-def _other_device_or_stream(device, stream):
+def _current_stream_handle(index):
+    """Handle of the current stream of CUDA device `index`."""
     import torch
-    with torch.cuda.device(device):
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object (3 us)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _on(index, stream, call):
+    """call(stream handle) with the tensors' device current and `stream` the
+    stream that newly allocated tensors belong to."""
+    import torch
+    if stream is None and torch.cuda.current_device() == index:
+        return call(_current_stream_handle(index))
+    with torch.cuda.device(index):
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-            return
+            return call(_current_stream_handle(index))
         if not hasattr(stream, "cuda_stream"):
             h = int(stream)
-            stream = torch.cuda.ExternalStream(h, device=device) if h else torch.cuda.default_stream(device)
-        if stream.device != device:
-            raise ValueError(f"stream must be on {device} like the tensors")
-        with torch.cuda.stream(stream):  # what is allocated here belongs to that stream
-            yield stream.cuda_stream
-
-
-def _on(device, stream):
-    """Context in which the library is called: the tensors' device current,
-    new tensors allocated for `stream`; yields the stream's handle."""
-    import torch
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext(torch.cuda.current_stream().cuda_stream)
-    return _other_device_or_stream(device, stream)
+            stream = torch.cuda.ExternalStream(h, device=index) if h else torch.cuda.default_stream(index)
+        if stream.device.index != index:
+            raise ValueError(f"stream must be on cuda:{index} like the tensors")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _check(rc, what):
+    if rc != DM05_OK:
+        raise Dm05Error(rc, what)
+
+
+def _codes(shape, index):
+    import torch
+    return torch.zeros(shape, dtype=torch.uint8, device=index).view(torch.float8_e4m3fn)
+
+
+def _empty_cache(B, Hkv, P, D, block, index):
+    """Zero codes and unit scales."""
+    import torch
+    shape, scales = (B, Hkv, P, D), (B, Hkv, -(-P // block))
+    ones = [torch.ones(scales, dtype=torch.float32, device=index) for _ in range(2)]
+    return Kv8Cache(_codes(shape, index), _codes(shape, index), ones[0], ones[1], block)
 
 
 def kv8_quantize(k, v, block: int = 64, valid_len=None, first: int = 0, out: Optional[Kv8Cache] = None, stream=None):
@@ -617,26 +639,40 @@ def kv8_quantize(k, v, block: int = 64, valid_len=None, first: int = 0, out: Opt
     import torch
     if k.dim() != 4:
         raise ValueError("k must be [B,Hkv,P,D]")
-    B, Hkv, P, D = k.shape
-    dev = k.device
-    _need("k", k, torch.bfloat16, (B, Hkv, P, D), dev)
-    _need("v", v, torch.bfloat16, (B, Hkv, P, D), dev)
+    shape = k.shape
+    B, Hkv, P, D = shape
+    dev = k.get_device()
+    _need("k", k, torch.bfloat16, shape, dev)
+    _need("v", v, torch.bfloat16, shape, dev)
     if valid_len is not None:
         _need("valid_len", valid_len, torch.int32, (B,), dev)
-    if out is not None and _need_cache("out", out, dev) != (B, Hkv, P, D):
+    if out is None:
+        if block not in (16, 32, 64, 128):
+            raise ValueError("block must be 16, 32, 64 or 128")
+    elif _need_cache("out", out, dev) != (B, Hkv, P, D):
         raise ValueError("out must be a cache of k's sizes")
-    if out is None and block not in (16, 32, 64, 128):
-        raise ValueError("block must be 16, 32, 64 or 128")
-    with _on(dev, stream) as s:
-        if out is None:
-            codes = lambda: torch.zeros((B, Hkv, P, D), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)  # noqa: E731
-            ones = lambda: torch.ones((B, Hkv, -(-P // block)), dtype=torch.float32, device=dev)  # noqa: E731
-            out = Kv8Cache(codes(), codes(), ones(), ones(), block)
-        rc = dm05_kv8_quantize(k.data_ptr(), v.data_ptr(), _ptr(valid_len), out.k.data_ptr(), out.v.data_ptr(),
-                               out.k_scale.data_ptr(), out.v_scale.data_ptr(), B, Hkv, P, D, out.block, first, s)
-    if rc != DM05_OK:
-        raise Dm05Error(rc, "dm05_kv8_quantize")
-    return out
+
+    def call(s):
+        c = _empty_cache(B, Hkv, P, D, block, dev) if out is None else out
+        _check(dm05_kv8_quantize(k.data_ptr(), v.data_ptr(), _ptr(valid_len), c.k.data_ptr(), c.v.data_ptr(),
+                                 c.k_scale.data_ptr(), c.v_scale.data_ptr(), B, Hkv, P, D, c.block, first, s),
+               "dm05_kv8_quantize")
+        return c
+    return _on(dev, stream, call)
+
+
+_kv8_workspace_bytes: dict = {}  # sizes and device -> bytes; the overrides change plans and clear it
+
+
+def _kv8_workspace(key):
+    need = _kv8_workspace_bytes.get(key)
+    if need is None:
+        rc, _, _, _, need = dm05_suffix_attn_kv8_plan(*key[:6])
+        _check(rc, "dm05_suffix_attn_kv8")
+        if len(_kv8_workspace_bytes) > 4096:
+            _kv8_workspace_bytes.clear()
+        _kv8_workspace_bytes[key] = need
+    return need
 
 
 def suffix_attn_kv8(q, cache: Kv8Cache, k_suffix, v_suffix, prefix_valid_len=None, prefix_mask=None, out=None,
@@ -649,42 +685,43 @@ def suffix_attn_kv8(q, cache: Kv8Cache, k_suffix, v_suffix, prefix_valid_len=Non
     import torch
     if q.dim() != 4:
         raise ValueError("q must be [B,Hq,S,D]")
-    B, Hq, S, D = q.shape
-    dev = q.device
+    shape = q.shape
+    B, Hq, S, D = shape
+    dev = q.get_device()
     bf = torch.bfloat16
-    _need("q", q, bf, (B, Hq, S, D), dev)
+    _need("q", q, bf, shape, dev)
     Bc, Hkv, P, Dc = _need_cache("cache", cache, dev)
     if Bc != B or Dc != D:
         raise ValueError("cache must have q's batch and head size")
-    _need("k_suffix", k_suffix, bf, (B, Hkv, S, D), dev)
-    _need("v_suffix", v_suffix, bf, (B, Hkv, S, D), dev)
+    suffix = (B, Hkv, S, D)
+    _need("k_suffix", k_suffix, bf, suffix, dev)
+    _need("v_suffix", v_suffix, bf, suffix, dev)
     _need_prefix(prefix_valid_len, prefix_mask, B, P, dev)
     if out is not None:
-        _need("out", out, bf, (B, Hq, S, D), dev)
+        _need("out", out, bf, shape, dev)
     if lse is not None:
         _need("lse", lse, torch.float32, (B, Hq, S), dev)
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
-                                  or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous CUDA uint8 tensor on {dev}")
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((B, Hq, S, D), dtype=bf, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty((B, Hq, S), dtype=torch.float32, device=dev)
-        if workspace is None:
-            rc, _, _, _, need = dm05_suffix_attn_kv8_plan(B, Hq, Hkv, P, S, D)
-            if rc != DM05_OK:
-                raise Dm05Error(rc, "dm05_suffix_attn_kv8")
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        rc = dm05_suffix_attn_kv8(q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-                                  cache.v_scale.data_ptr(), cache.block, _ptr(prefix_valid_len), _ptr(prefix_mask),
-                                  k_suffix.data_ptr(), v_suffix.data_ptr(), out.data_ptr(), _ptr(lse),
-                                  _ptr(workspace), 0 if workspace is None else workspace.numel(), B, Hq, Hkv, P, S, D,
-                                  s)
-    if rc != DM05_OK:
-        raise Dm05Error(rc, "dm05_suffix_attn_kv8")
-    return out, lse
+    if workspace is not None:
+        _need("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
+
+    def call(s):
+        o = torch.empty(shape, dtype=bf, device=dev) if out is None else out
+        ls = torch.empty((B, Hq, S), dtype=torch.float32, device=dev) if lse is None and want_lse else lse
+        key = (B, Hq, Hkv, P, S, D, dev)
+        for attempt in range(2):
+            ws = workspace
+            if ws is None:
+                need = _kv8_workspace(key)
+                ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+            rc = dm05_suffix_attn_kv8(q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+                                      cache.v_scale.data_ptr(), cache.block, _ptr(prefix_valid_len), _ptr(prefix_mask),
+                                      k_suffix.data_ptr(), v_suffix.data_ptr(), o.data_ptr(), _ptr(ls), _ptr(ws),
+                                      0 if ws is None else ws.numel(), B, Hq, Hkv, P, S, D, s)
+            if rc != DM05_ERR_WORKSPACE or workspace is not None or _kv8_workspace_bytes.pop(key, None) is None:
+                break  # else a plan was forced past this module: ask for its workspace again
+        _check(rc, "dm05_suffix_attn_kv8")
+        return o, ls
+    return _on(dev, stream, call)
 
 
 def _mass(q, k, k_scale, block, lse, valid_len, mask, mass_in, mass, stream):
@@ -693,7 +730,7 @@ def _mass(q, k, k_scale, block, lse, valid_len, mask, mass_in, mass, stream):
         raise ValueError("q must be [B,Hq,S,D] and the keys [B,Hkv,P,D]")
     B, Hq, S, D = q.shape
     Hkv, P = k.shape[1], k.shape[2]
-    dev = q.device
+    dev = q.get_device()
     _need("q", q, torch.bfloat16, (B, Hq, S, D), dev)
     if k_scale is None:
         _need("k_prefix", k, torch.bfloat16, (B, Hkv, P, D), dev)
@@ -708,19 +745,19 @@ def _mass(q, k, k_scale, block, lse, valid_len, mask, mass_in, mass, stream):
         _need("mass_in", mass_in, torch.float32, (B, Hkv, P), dev)
     if mass is not None:
         _need("mass", mass, torch.float32, (B, Hkv, P), dev)
-    with _on(dev, stream) as s:
-        if mass is None:
-            mass = torch.empty((B, Hkv, P), dtype=torch.float32, device=dev)
+
+    def call(s):
+        m = torch.empty((B, Hkv, P), dtype=torch.float32, device=dev) if mass is None else mass
         if k_scale is None:
             rc = dm05_prefix_attn_mass(q.data_ptr(), k.data_ptr(), _ptr(valid_len), _ptr(mask), lse.data_ptr(),
-                                       _ptr(mass_in), mass.data_ptr(), B, Hq, Hkv, P, S, D, s)
+                                       _ptr(mass_in), m.data_ptr(), B, Hq, Hkv, P, S, D, s)
         else:
             rc = dm05_prefix_attn_mass_kv8(q.data_ptr(), k.data_ptr(), k_scale.data_ptr(), block, _ptr(valid_len),
-                                           _ptr(mask), lse.data_ptr(), _ptr(mass_in), mass.data_ptr(), B, Hq, Hkv, P,
-                                           S, D, s)
-    if rc != DM05_OK:
-        raise Dm05Error(rc, "dm05_prefix_attn_mass")
-    return mass
+                                           _ptr(mask), lse.data_ptr(), _ptr(mass_in), m.data_ptr(), B, Hq, Hkv, P, S,
+                                           D, s)
+        _check(rc, "dm05_prefix_attn_mass")
+        return m
+    return _on(dev, stream, call)
 
 
 def prefix_attn_mass(q, k_prefix, lse, prefix_valid_len=None, prefix_mask=None, mass_in=None, mass=None, stream=None):
@@ -739,26 +776,26 @@ def prefix_attn_mass_kv8(q, k8, k_scale, block, lse, prefix_valid_len=None, pref
     return _mass(q, k8, k_scale, block, lse, prefix_valid_len, prefix_mask, mass_in, mass, stream)
 
 
-def _need_evicted(mass, B, Hkv, P, P_out, valid_len_in, mask, mass_out, positions, valid_len, dev):
+def _need_evicted(mass, B, Hkv, P, P_out, valid_len_in, mask, mass_out, positions, valid_len, index):
     import torch
-    _need("mass", mass, torch.float32, (B, Hkv, P), dev)
-    _need_prefix(valid_len_in, mask, B, P, dev)
+    _need("mass", mass, torch.float32, (B, Hkv, P), index)
+    _need_prefix(valid_len_in, mask, B, P, index)
     if mass_out is not None:
-        _need("mass_out", mass_out, torch.float32, (B, Hkv, P_out), dev)
+        _need("mass_out", mass_out, torch.float32, (B, Hkv, P_out), index)
     if positions is not None:
-        _need("positions", positions, torch.int32, (B, Hkv, P_out), dev)
+        _need("positions", positions, torch.int32, (B, Hkv, P_out), index)
     if valid_len is not None:
-        _need("valid_len", valid_len, torch.int32, (B,), dev)
+        _need("valid_len", valid_len, torch.int32, (B,), index)
 
 
-def _evict_outputs(B, Hkv, P_out, mass_out, positions, valid_len, dev):
+def _evict_outputs(B, Hkv, P_out, mass_out, positions, valid_len, index):
     import torch
     if mass_out is None:
-        mass_out = torch.empty((B, Hkv, P_out), dtype=torch.float32, device=dev)
+        mass_out = torch.empty((B, Hkv, P_out), dtype=torch.float32, device=index)
     if positions is None:
-        positions = torch.empty((B, Hkv, P_out), dtype=torch.int32, device=dev)
+        positions = torch.empty((B, Hkv, P_out), dtype=torch.int32, device=index)
     if valid_len is None:
-        valid_len = torch.empty((B,), dtype=torch.int32, device=dev)
+        valid_len = torch.empty((B,), dtype=torch.int32, device=index)
     return mass_out, positions, valid_len
 
 
@@ -774,7 +811,7 @@ def prefix_evict(k, v, mass, n_keep: int, n_first: int = 0, n_last: int = 0, pre
     if k.dim() != 4:
         raise ValueError("k must be [B,Hkv,P,D]")
     B, Hkv, P, D = k.shape
-    dev = k.device
+    dev = k.get_device()
     bf = torch.bfloat16
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out must be given together")
@@ -787,17 +824,17 @@ def prefix_evict(k, v, mass, n_keep: int, n_first: int = 0, n_last: int = 0, pre
         _need("k_out", k_out, bf, (B, Hkv, bucket, D), dev)
         _need("v_out", v_out, bf, (B, Hkv, bucket, D), dev)
     _need_evicted(mass, B, Hkv, P, bucket, prefix_valid_len, prefix_mask, mass_out, positions, valid_len, dev)
-    with _on(dev, stream) as s:
-        if k_out is None:
-            k_out = torch.zeros((B, Hkv, bucket, D), dtype=bf, device=dev)
-            v_out = torch.zeros((B, Hkv, bucket, D), dtype=bf, device=dev)
-        mass_out, positions, valid_len = _evict_outputs(B, Hkv, bucket, mass_out, positions, valid_len, dev)
-        rc = dm05_prefix_evict(k.data_ptr(), v.data_ptr(), mass.data_ptr(), _ptr(prefix_valid_len), _ptr(prefix_mask),
-                               k_out.data_ptr(), v_out.data_ptr(), mass_out.data_ptr(), positions.data_ptr(),
-                               valid_len.data_ptr(), B, Hkv, P, bucket, D, n_keep, n_first, n_last, s)
-    if rc != DM05_OK:
-        raise Dm05Error(rc, "dm05_prefix_evict")
-    return EvictedPrefix(k_out, v_out, mass_out, positions, valid_len)
+
+    def call(s):
+        ko, vo = k_out, v_out
+        if ko is None:
+            ko, vo = [torch.zeros((B, Hkv, max(bucket, 0), D), dtype=bf, device=dev) for _ in range(2)]
+        mo, po, vl = _evict_outputs(B, Hkv, max(bucket, 0), mass_out, positions, valid_len, dev)
+        _check(dm05_prefix_evict(k.data_ptr(), v.data_ptr(), mass.data_ptr(), _ptr(prefix_valid_len),
+                                 _ptr(prefix_mask), ko.data_ptr(), vo.data_ptr(), mo.data_ptr(), po.data_ptr(),
+                                 vl.data_ptr(), B, Hkv, P, bucket, D, n_keep, n_first, n_last, s), "dm05_prefix_evict")
+        return EvictedPrefix(ko, vo, mo, po, vl)
+    return _on(dev, stream, call)
 
 
 def prefix_evict_kv8(cache: Kv8Cache, mass, n_keep: int, n_first: int = 0, n_last: int = 0, prefix_valid_len=None,
@@ -806,26 +843,22 @@ def prefix_evict_kv8(cache: Kv8Cache, mass, n_keep: int, n_first: int = 0, n_las
     """prefix_evict on an 8-bit cache: the kept rows form blocks of the same
     size with scales of their own (a fresh `out` has zero codes and unit
     scales behind them)."""
-    import torch
-    B, Hkv, P, D = _need_cache("cache", cache)
-    dev = cache.k.device
+    dev = cache.k.get_device()
+    B, Hkv, P, D = _need_cache("cache", cache, dev)
     if out is not None and bucket is None and out.k.dim() == 4:
         bucket = out.k.shape[2]
     bucket = n_keep if bucket is None else bucket
     if out is not None and (_need_cache("out", out, dev) != (B, Hkv, bucket, D) or out.block != cache.block):
         raise ValueError(f"out must be a cache of {bucket} rows with cache's other sizes and block")
     _need_evicted(mass, B, Hkv, P, bucket, prefix_valid_len, prefix_mask, mass_out, positions, valid_len, dev)
-    with _on(dev, stream) as s:
-        if out is None:
-            codes = lambda: torch.zeros((B, Hkv, bucket, D), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)  # noqa: E731
-            ones = lambda: torch.ones((B, Hkv, -(-bucket // cache.block)), dtype=torch.float32, device=dev)  # noqa: E731
-            out = Kv8Cache(codes(), codes(), ones(), ones(), cache.block)
-        mass_out, positions, valid_len = _evict_outputs(B, Hkv, bucket, mass_out, positions, valid_len, dev)
-        rc = dm05_prefix_evict_kv8(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-                                   cache.v_scale.data_ptr(), cache.block, mass.data_ptr(), _ptr(prefix_valid_len),
-                                   _ptr(prefix_mask), out.k.data_ptr(), out.v.data_ptr(), out.k_scale.data_ptr(),
-                                   out.v_scale.data_ptr(), mass_out.data_ptr(), positions.data_ptr(),
-                                   valid_len.data_ptr(), B, Hkv, P, bucket, D, n_keep, n_first, n_last, s)
-    if rc != DM05_OK:
-        raise Dm05Error(rc, "dm05_prefix_evict_kv8")
-    return EvictedPrefixKv8(out, mass_out, positions, valid_len)
+
+    def call(s):
+        c = _empty_cache(B, Hkv, max(bucket, 0), D, cache.block, dev) if out is None else out
+        mo, po, vl = _evict_outputs(B, Hkv, max(bucket, 0), mass_out, positions, valid_len, dev)
+        _check(dm05_prefix_evict_kv8(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+                                     cache.v_scale.data_ptr(), cache.block, mass.data_ptr(), _ptr(prefix_valid_len),
+                                     _ptr(prefix_mask), c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(),
+                                     c.v_scale.data_ptr(), mo.data_ptr(), po.data_ptr(), vl.data_ptr(), B, Hkv, P,
+                                     bucket, D, n_keep, n_first, n_last, s), "dm05_prefix_evict_kv8")
+        return EvictedPrefixKv8(c, mo, po, vl)
+    return _on(dev, stream, call)
