@@ -117,7 +117,7 @@ def lib() -> ctypes.CDLL:
             L.dm05_kv8_quantize.restype = i
             L.dm05_suffix_attn_kv8.argtypes = [p] * 5 + [i] + [p] * 7 + [sz] + [i] * 6 + [p]
             L.dm05_suffix_attn_kv8.restype = i
-            L.dm05_suffix_attn_kv8_plan.argtypes = [i] * 6 + [ctypes.POINTER(i)] * 3 + [ctypes.POINTER(sz)]
+            L.dm05_suffix_attn_kv8_plan.argtypes = [i] * 6 + [ctypes.POINTER(i)] * 2 + [ctypes.POINTER(sz)]
             L.dm05_suffix_attn_kv8_plan.restype = i
             L.dm05_prefix_attn_mass.argtypes = [p] * 7 + [i] * 6 + [p]
             L.dm05_prefix_attn_mass.restype = i
@@ -235,11 +235,10 @@ def dm05_suffix_attn_kv8(q, k8, v8, k_scale, v_scale, block, prefix_valid_len, p
 
 
 def dm05_suffix_attn_kv8_plan(B, Hq, Hkv, P, S, D):
-    """Returns (status, splits_per_head, tile_rows, row_blocks, workspace_bytes)."""
-    sp, tr, rb, ws = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
-    rc = lib().dm05_suffix_attn_kv8_plan(B, Hq, Hkv, P, S, D, ctypes.byref(sp), ctypes.byref(tr), ctypes.byref(rb),
-                                         ctypes.byref(ws))
-    return rc, sp.value, tr.value, rb.value, ws.value
+    """Returns (status, splits_per_head, tile_rows, workspace_bytes)."""
+    sp, tr, ws = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
+    rc = lib().dm05_suffix_attn_kv8_plan(B, Hq, Hkv, P, S, D, ctypes.byref(sp), ctypes.byref(tr), ctypes.byref(ws))
+    return rc, sp.value, tr.value, ws.value
 
 
 def dm05_prefix_attn_mass(q, k_prefix, prefix_valid_len, prefix_mask, lse, mass_in, mass, B, Hq, Hkv, P, S, D,
@@ -317,7 +316,6 @@ def dm05_set_split_override(splits_per_head: int) -> int:
 
 
 def dm05_set_row_block_override(row_blocks: int) -> int:
-    _kv8_workspace_bytes.clear()
     return lib().dm05_set_row_block_override(row_blocks)
 
 
@@ -661,13 +659,13 @@ def kv8_quantize(k, v, block: int = 64, valid_len=None, first: int = 0, out: Opt
     return _on(dev, stream, call)
 
 
-_kv8_workspace_bytes: dict = {}  # sizes and device -> bytes; the overrides change plans and clear it
+_kv8_workspace_bytes: dict = {}  # sizes and device -> bytes; a split override changes plans and clears it
 
 
 def _kv8_workspace(key):
     need = _kv8_workspace_bytes.get(key)
     if need is None:
-        rc, _, _, _, need = dm05_suffix_attn_kv8_plan(*key[:6])
+        rc, _, _, need = dm05_suffix_attn_kv8_plan(*key[:6])
         _check(rc, "dm05_suffix_attn_kv8")
         if len(_kv8_workspace_bytes) > 4096:
             _kv8_workspace_bytes.clear()

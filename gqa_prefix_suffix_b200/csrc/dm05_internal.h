@@ -13,7 +13,6 @@ struct Device {
     uint32_t *err = nullptr;  // the device error word
     int num_sms = 0;
     int split_override = 0;      // dm05_set_split_override
-    int row_block_override = 0;  // dm05_set_row_block_override
     int ordinal = 0;
 };
 

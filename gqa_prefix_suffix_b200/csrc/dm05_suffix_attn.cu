@@ -1667,7 +1667,6 @@ int device(cudaStream_t stream, bool need_err, Device *out) noexcept
         out->err = ds->err;
         out->num_sms = ds->num_sms;
         out->split_override = g_split_override;
-        out->row_block_override = g_row_block_override;
         out->ordinal = static_cast<int>(ds - g_dev.data());
         return DM05_OK;
     } catch (...) {

@@ -29,14 +29,19 @@
 //
 // One CTA walks a contiguous run of a unit's key tiles: the suffix tiles (64
 // rows of bf16, kind::f16), then prefix tiles of 128 codes, each 32 KB of K
-// and of V in two rings of shared memory filled by TMA.  Warp
-// roles, split over a cluster and the merge are those of the bf16 kernel
-// (suffix_attn_kernel.cuh), but for the softmax: warps 16 and 18 load (Q and
-// K; V), warp 17 issues the MMAs, and warps 0-15 are two groups that take
-// the tiles in turn (two warps per 32 query rows, half of a tile's columns
-// each).  Q lands in shared memory as bf16; the CTA with suffix tiles copies
-// it to tensor memory (into the second S buffer, which is not in use yet),
-// and the softmax warps rewrite it in place as the two e4m3 terms.
+// and of V in two rings of shared memory filled by TMA.  Warps 16 and 18 load
+// (Q and K; V), warp 17 issues the MMAs, and warps 0-15 are two softmax groups
+// that take the tiles in turn (two warps per 32 query rows, half of a tile's
+// columns each).  Q lands in shared memory as bf16; the CTA with suffix tiles
+// copies it to tensor memory (into the second S buffer, which is not in use
+// yet), and the softmax warps rewrite it in place as the two e4m3 terms.
+//
+// A unit's tiles may be split over any number of CTAs: each writes its
+// unnormalised O with {m, l} per row, and merge_kernel, launched behind it,
+// joins them.  (A cluster merge inside the kernel, as the bf16 kernel has,
+// limits a unit to 16 CTAs and the grid to what clusters leave resident: 15.3
+// instead of XX us at B = 1, P = 1024, S = 50 and 68 instead of XX us at B = 2,
+// P = 30016.)
 #pragma once
 
 #include "prefix_cache_kernels.cuh"
@@ -125,9 +130,11 @@ constexpr float kMaxBits = 8.0f;     // ... and may grow to 2^8 before O is resc
 // output's own rounding).
 constexpr float kSuffixBits = 7.0f;
 
+constexpr int kPartRow = kHeadDim * 4 + 16;  // a partial row: D fp32 of O, then {m, l, 0, 0}
+constexpr int kMaxSplits8 = 64;
+
 struct Smem {
-    static constexpr int kQChunkBytes = kMRows * 128;
-    static constexpr int kQBytes = 4 * kQChunkBytes;  // bf16, then two e4m3 terms in the same bytes
+    static constexpr int kQBytes = kMRows * 512;  // bf16, then two e4m3 terms in the same bytes
     static constexpr int kK = kQBytes;
     static constexpr int kV = kK + kSlots * kSlotBytes;
     static constexpr int kDataEnd = kV + kSlots * kSlotBytes;
@@ -142,8 +149,7 @@ struct Smem {
     static constexpr int kBarPReady = kBarSFull + 2;
     static constexpr int kBarPFree = kBarPReady + 2;
     static constexpr int kBarMmaFinal = kBarPFree + 2;
-    static constexpr int kBarMerge = kBarMmaFinal + 1;
-    static constexpr int kBarRow = kBarMerge + 1;   // per lane quarter: its four warps
+    static constexpr int kBarRow = kBarMmaFinal + 1;  // per lane quarter: its four warps
     static constexpr int kBarPair = kBarRow + 4;    // per group and lane quarter: its two warps
     static constexpr int kBarMax = kBarPair + 8;    // per lane quarter: tile t's reference maximum is known
     static constexpr int kNumBars = kBarMax + 4;
@@ -154,10 +160,9 @@ struct Smem {
     static constexpr int kXchgOff = (kTmemSlotOff + 16 + 15) / 16 * 16;
     static constexpr int kEnd = kXchgOff + (4 + 2 + 4) * kMRows * 4 + kSoftWarps * 64 * 4;
     static constexpr int kAllocBytes = kEnd + 1024;
-    static constexpr int kStageStride = kHeadDim * 4 + 16;  // a partial row: D fp32 of O, then {m, l, l, 0}
+    static constexpr int kStageStride = kPartRow;
     static constexpr int kOutStride = kHeadDim * 2 + 16;    // an output row on its way out
-    static_assert(kDataEnd >= (kMRows + 16) * kStageStride, "the merge receives at most 144 rows");
-    static_assert(10 * kMRows * 4 >= kMRows * 8, "the merge keeps one output row index per row in the exchange area");
+    static_assert(kDataEnd >= kMRows * kStageStride, "the rows staged on their way out");
     static_assert(kAllocBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -168,9 +173,10 @@ struct Params {
     __nv_bfloat16 *out;
     float *lse;
     uint32_t *err;
-    float *part;                     // splits > 1: partial rows, as in the bf16 kernel
-    int Hkv, P, S, GS, G;
-    int row_blocks, SQ, splits;
+    uint8_t *part;                   // splits > 1: partial rows [units][splits][GS], kPartRow bytes each
+    int Hkv, P, S, GS;               // GS: query rows of a unit
+    int qrows;                       // GS rounded up to 8: rows of a Q chunk in shared memory
+    int splits;                      // CTAs per unit
     int nblk, shift;
     float scale_log2;
 };
@@ -210,16 +216,16 @@ __device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3
 }
 
 // A query row is cut into four chunks of 64 bf16 (128 swizzled bytes each;
-// sw: the row's swizzle).  Largest magnitude of one chunk of a row, as bf16
-// bits: magnitudes order like their bits.
-__device__ __forceinline__ uint32_t chunk_max(const uint8_t *chunk, uint32_t sw)
+// sw: the row's swizzle).  A thread takes one chunk of a row: reads it and
+// returns its largest magnitude as bf16 bits (magnitudes order like their bits).
+__device__ __forceinline__ uint32_t read_chunk(const uint8_t *chunk, uint32_t sw, uint4 (&v)[8])
 {
     uint32_t top = 0u;
-#pragma unroll 4
+#pragma unroll
     for (int u = 0; u < 8; ++u) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(chunk + ((u ^ sw) << 4));
-        top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
-        top = __vmaxu2(top, v.w & 0x7fff7fffu);
+        v[u] = *reinterpret_cast<const uint4 *>(chunk + ((u ^ sw) << 4));
+        top = __vmaxu2(__vmaxu2(top, v[u].x & 0x7fff7fffu), __vmaxu2(v[u].y & 0x7fff7fffu, v[u].z & 0x7fff7fffu));
+        top = __vmaxu2(top, v[u].w & 0x7fff7fffu);
     }
     return max(top & 0xffffu, top >> 16);
 }
@@ -231,32 +237,26 @@ __device__ __forceinline__ float row_scale(uint32_t bits)
     return bits < 0x7f80u ? cache::pow2_scale(__uint_as_float(bits << 16)) : 1.0f;
 }
 
-// Rewrites one chunk of a scaled row as two e4m3 terms: the 64 bytes of 32
-// bf16 values become their 32 first terms, then their 32 second ones, so a
-// thread rewrites only what it has read.
-__device__ __forceinline__ void split_chunk(uint8_t *chunk, uint32_t sw, float inv)
+// Writes the chunk back as two e4m3 terms of its scaled values: the 64 bytes
+// of 32 bf16 values become their 32 first terms, then their 32 second ones, so
+// a thread rewrites only what it has read.
+__device__ __forceinline__ void split_chunk(uint8_t *chunk, uint32_t sw, float inv, const uint4 (&v)[8])
 {
-#pragma unroll 1
-    for (int g = 0; g < 2; ++g) {
-        uint4 *unit16[4];
-        uint4 v[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            unit16[u] = reinterpret_cast<uint4 *>(chunk + (((g * 4 + u) ^ sw) << 4));
-            v[u] = *unit16[u];
-        }
+    for (int g = 0; g < 2; ++g) {
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint4 &src = v[e >> 1];
+            const uint4 &src = v[g * 4 + (e >> 1)];
             const uint32_t w0 = (e & 1) ? src.z : src.x, w1 = (e & 1) ? src.w : src.y;
             two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
                       __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
         }
-        *unit16[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *unit16[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-        *unit16[2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *unit16[3] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+        auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + (((g * 4 + u) ^ sw) << 4)); };
+        *unit16(0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *unit16(1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+        *unit16(2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *unit16(3) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
     }
 }
 
@@ -272,15 +272,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemSlotOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int C = p.splits;
-    const int cl = blockIdx.x / C, rank = blockIdx.x - cl * C;
-    const int unit = cl / p.row_blocks, rb = cl - unit * p.row_blocks;
+    const int unit = blockIdx.x / C, rank = blockIdx.x - unit * C;
     const int b = unit / p.Hkv;
-    // row m of the MMA <-> head m / rph, query q0 + m % rph; compact row = head * nq + m % rph
-    const int q0 = rb * p.SQ;
-    const int nq = min(p.SQ, p.S - q0);
-    const int rph = p.row_blocks == 1 ? p.S : (p.SQ + 7) / 8 * 8;
-    const int NR = p.G * nq;
-    const size_t unit_row0 = static_cast<size_t>(unit) * p.GS;
+    const int qpitch = p.qrows * 128;  // bytes of a 64-column chunk of Q
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(&bars[L::kBarQFull], 1);
@@ -298,7 +292,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
             ptx::mbar_init(&bars[L::kBarPFree + i], 1);
         }
         ptx::mbar_init(&bars[L::kBarMmaFinal], 1);
-        ptx::mbar_init(&bars[L::kBarMerge], 1);
         for (int i = 0; i < 4; ++i) {
             ptx::mbar_init(&bars[L::kBarRow + i], 128);
             ptx::mbar_init(&bars[L::kBarPair + i], 64);
@@ -333,16 +326,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
     uint64_t pol = 0;
     if (warp == kLoadWarp && lane == 0) {
         pol = ptx::policy_evict_first();
-        if (p.row_blocks == 1) {
-            ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], L::kQBytes);
-            ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, 0, 0, unit);
-        } else {
-            ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(p.G * kChunks * p.SQ * 128));
-            for (int h = 0; h < p.G; ++h)
-                for (int c = 0; c < kChunks; ++c)
-                    ptx::tma_load_3d(smem + c * L::kQChunkBytes + h * rph * 128, &tm_q, &bars[L::kBarQFull],
-                                     c * kChunkElems, h * p.S + q0, unit);
-        }
+        // rows of the MMA past qrows read whatever lies behind: rows of their own
+        ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(4 * qpitch));
+        ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, 0, 0, unit);
         if (first) {
             ptx::mbar_arrive_expect_tx(&bars[L::kBarKFull], kSlotBytes);
             ptx::tma_load_4d_hint(k_slot(0), &tm_ks, &bars[L::kBarKFull], 0, 0, 0, unit, pol);
@@ -357,7 +343,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     }
 
     const int vl = cache::clamped_len(p.valid_len, b, p.P, p.err,
-                                      threadIdx.x == 0 && rank == 0 && rb == 0 && unit % p.Hkv == 0);
+                                      threadIdx.x == 0 && rank == 0 && unit % p.Hkv == 0);
     const int TS = (p.S + kSufTile - 1) / kSufTile;
     const int t_all = TS + (vl + kTile - 1) / kTile;
     const int t_begin = static_cast<int>((static_cast<long long>(t_all) * rank) / C);
@@ -446,7 +432,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                 for (int kk = 0; kk < kHeadDim / 16; ++kk)
                     ptx::tmem_cp_128x256b(tmem + kTmemS8 + kTile + kk * 8,
-                                          qdesc + static_cast<uint64_t>(((kk >> 2) * L::kQChunkBytes + (kk & 3) * 32) >> 4));
+                                          qdesc + static_cast<uint64_t>(((kk >> 2) * qpitch + (kk & 3) * 32) >> 4));
                 ptx::mma_commit(&bars[L::kBarQFree]);
             }
             for (int t = 0; t < T && ok; ++t) {
@@ -482,7 +468,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         // 32 columns j of K against the first, then the second term of
                         // Q's: 32 of the 64 bytes that their bf16 form took
                         const int j = kk >> 1;
-                        const uint32_t qo = ((j >> 1) * L::kQChunkBytes + (j & 1) * 64 + (kk & 1) * 32) >> 4;
+                        const uint32_t qo = ((j >> 1) * qpitch + (j & 1) * 64 + (kk & 1) * 32) >> 4;
                         const uint32_t ko = ((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4;
                         ptx::mma_f8_ss(d, qdesc + qo, kd + ko, id_qk, kk > 0 ? 1u : 0u);
                     }
@@ -504,7 +490,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
         const int q4 = warp & 3, hf = (warp >> 2) & 1, grp = warp >> 3;
         const int c4 = warp >> 2;  // column quarter of Q and of O
         const int row = q4 * 32 + lane;
-        const int row_h = row / rph, row_j = row - row_h * rph;
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
         const uint8_t *mask_row = p.mask ? p.mask + static_cast<size_t>(b) * p.P : nullptr;
         const float *ksc = p.k_scale + static_cast<size_t>(unit) * p.nblk;
@@ -529,18 +514,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
             // ---- Q as two e4m3 terms: this thread's 64 values of its row
             failed = !warp_wait(&bars[L::kBarQFull], 0);
             if (!failed && ns > 0) failed = !warp_wait(&bars[L::kBarQFree], 0);
-            uint8_t *chunk = smem + c4 * L::kQChunkBytes + row * 128;
+            uint8_t *chunk = smem + c4 * qpitch + row * 128;
             uint32_t *qmax = reinterpret_cast<uint32_t *>(xl) + row;  // [4][128]
+            const bool mine = row < p.GS;
+            uint4 v[8];
             if (!failed) {
-                qmax[c4 * kMRows] = chunk_max(chunk, row & 7);
+                if (mine) qmax[c4 * kMRows] = read_chunk(chunk, row & 7, v);
                 failed = !row_sync();
             }
             if (!failed) {
-                const uint32_t bits = max(max(qmax[0], qmax[kMRows]), max(qmax[2 * kMRows], qmax[3 * kMRows]));
-                const float s = row_scale(bits);
-                // a row with a non-finite element becomes NaN
-                sqs = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
-                split_chunk(chunk, row & 7, cache::pow2_inverse(s));
+                if (mine) {
+                    const uint32_t bits = max(max(qmax[0], qmax[kMRows]), max(qmax[2 * kMRows], qmax[3 * kMRows]));
+                    const float s = row_scale(bits);
+                    // a row with a non-finite element becomes NaN
+                    sqs = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
+                    split_chunk(chunk, row & 7, cache::pow2_inverse(s), v);
+                }
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(&bars[L::kBarQConv]);
             }
@@ -663,6 +652,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 }
                 if (partial) ptx::tmem_st_wait();
             }
+            if (row >= p.GS) hmax = -INFINITY;  // not a query row: never a reason to rescale
             xmax[hf * kMRows + row] = hmax;
             if (!pair_sync()) {
                 failed = true;
@@ -805,9 +795,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
         xl[c4 * kMRows + row] = l;
         if (!failed && !row_sync()) failed = true;
         const float l_row = (xl[row] + xl[kMRows + row]) + (xl[2 * kMRows + row] + xl[3 * kMRows + row]);
-        const bool row_valid = row_h < p.G && row_j < nq;
-        const int row_k = row_h * nq + row_j;
-        const size_t out_row = unit_row0 + static_cast<size_t>(row_h) * p.S + q0 + row_j;
+        const bool row_valid = row < p.GS;
+        const size_t out_row = static_cast<size_t>(unit) * p.GS + row;
         const float inv_l = 1.0f / l_row;
         // Rows leave through shared memory: a thread's columns of its row, then
         // one bulk store of the whole row (16-byte stores of 32 rows at once
@@ -842,8 +831,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         if (row_valid) {
             if (C > 1 && c4 == 0) {
-                const float used = have_o && !failed ? l_row : 0.0f;
-                *reinterpret_cast<float4 *>(srow + kHeadDim * 4) = make_float4(m_end, used, used, 0.0f);
+                *reinterpret_cast<float4 *>(srow + kHeadDim * 4) =
+                    make_float4(m_end, have_o && !failed ? l_row : 0.0f, 0.0f, 0.0f);
             }
             ptx::fence_proxy_async_smem();
         }
@@ -853,9 +842,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 ptx::bulk_store_s2g(p.out + out_row * kHeadDim, ptx::smem_addr(srow), kHeadDim * 2);
                 if (p.lse != nullptr) p.lse[out_row] = (m_end + ptx::lg2(l_row)) * 0.69314718055994531f;
             } else {
-                const size_t prow = (static_cast<size_t>(cl) * C + rank) * (p.G * p.SQ) + row_k;
-                ptx::bulk_store_s2g(reinterpret_cast<uint8_t *>(p.part) + prow * L::kStageStride, ptx::smem_addr(srow),
-                                    L::kStageStride);
+                const size_t prow = (static_cast<size_t>(unit) * C + rank) * p.GS + row;
+                ptx::bulk_store_s2g(p.part + prow * kPartRow, ptx::smem_addr(srow), kPartRow);
             }
             ptx::bulk_commit();
             ptx::bulk_wait_all();
@@ -863,31 +851,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
     }
 
-    __syncwarp();
-    if (C > 1) {
-        // ================================================== split merge, as in the bf16 kernel
-        ptx::cluster_sync();
-        const int r_lo = (NR * rank) / C, r_hi = (NR * (rank + 1)) / C;
-        const int nr = r_hi - r_lo;
-        long long *orow_s = reinterpret_cast<long long *>(smem + L::kXchgOff);
-        if (nr > 0 && warp == 0) {
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[L::kBarMerge], static_cast<uint32_t>(C * nr * L::kStageStride));
-            __syncwarp();
-            if (lane < C) {
-                ptx::fence_proxy_async_global();
-                ptx::bulk_load_g2s(ptx::smem_addr(smem) + static_cast<uint32_t>(lane * nr * L::kStageStride),
-                                   reinterpret_cast<const uint8_t *>(p.part) +
-                                       ((static_cast<size_t>(cl) * C + lane) * (p.G * p.SQ) + r_lo) * L::kStageStride,
-                                   static_cast<uint32_t>(nr * L::kStageStride), &bars[L::kBarMerge]);
-            }
-        }
-        if (nr > 0) {
-            if (!warp_wait(&bars[L::kBarMerge], 0)) failed = true;
-            merge_weights<L, kThreads8>(smem, C, nr, p.lse, unit_row0, r_lo, nq, p.S, q0, nq, orow_s);
-            __syncthreads();
-            merge_rows<L, kThreads8>(smem, C, nr, p.out, orow_s);
-        }
-    }
     if (failed) atomicOr(p.err, kEwTimeout);
     __syncwarp();
     ptx::tc_fence_before_sync();
@@ -896,6 +859,63 @@ __global__ void __launch_bounds__(kThreads8, 1)
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+struct MergeParams {
+    const uint8_t *part;   // [units][splits][GS] partial rows
+    __nv_bfloat16 *out;    // [units * GS, 256]
+    float *lse;            // [units * GS] or nullptr
+    int rows, GS, splits;  // rows: units * GS
+};
+
+// Joins the partial rows of a split call, one warp a row: with
+// M = max_c m_c and w_c = 2^(m_c - M), out = sum_c w_c O_c / sum_c w_c l_c and
+// lse = (M + log2 sum_c w_c l_c) ln 2.  A partial without keys (l = 0) has no
+// weight, whatever its O holds.
+__global__ void __launch_bounds__(128) merge_kernel(const MergeParams p)
+{
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int r = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= p.rows) return;
+    const int unit = r / p.GS, row = r - unit * p.GS;
+    const uint8_t *base = p.part + (static_cast<size_t>(unit) * p.splits * p.GS + row) * kPartRow;
+    const size_t step = static_cast<size_t>(p.GS) * kPartRow;
+    float m[2], l[2], M = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        float2 st = make_float2(-INFINITY, 0.0f);
+        if (c < p.splits) st = *reinterpret_cast<const float2 *>(base + c * step + kHeadDim * 4);
+        m[h] = st.x;
+        l[h] = st.y;
+        if (l[h] != 0.0f) M = fmaxf(M, m[h]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float w[2], total = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        w[h] = l[h] != 0.0f ? ptx::ex2(m[h] - M) : 0.0f;
+        total = fmaf(w[h], l[h], total);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int c = 0; c < p.splits; ++c) {
+        const float wc = __shfl_sync(0xffffffffu, c < 32 ? w[0] : w[1], c & 31);
+        const float4 *o = reinterpret_cast<const float4 *>(base + c * step);
+        const float4 x = o[lane], y = o[lane + 32];
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(wc, wc != 0.0f ? v[e] : 0.0f, acc[e]);
+    }
+    const float inv = 1.0f / total;
+    uint2 *out = reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(r) * kHeadDim);
+    out[lane] = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    out[lane + 32] = make_uint2(pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (lane == 0 && p.lse != nullptr) p.lse[r] = (M + ptx::lg2(total)) * 0.69314718055994531f;
 }
 
 }  // namespace kv8

@@ -64,53 +64,30 @@ int launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, c
 
 // ---------------------------------------------------------------- kv8 attention plan
 
-struct Kv8State {
-    bool ready = false;
-    int max_cluster = 1;
-    int active[dm05::kMaxSplits + 1] = {};  // clusters of c CTAs the device holds at once
-};
 constexpr int kMaxDevices = 64;
-std::mutex g_kv8_mu;
-Kv8State g_kv8[kMaxDevices];
+std::mutex g_attr_mu;
+bool g_kv8_ready[kMaxDevices];
+bool g_mass_ready[kMaxDevices];
 
-// Kernel attributes and cluster residency of the attention kernel, once per device.
-int kv8_state(const Device &dev, Kv8State *out) noexcept
+// Kernel attributes of the attention or of the weight kernels, once per device.
+int set_attributes(const Device &dev, bool mass) noexcept
 {
     if (dev.ordinal < 0 || dev.ordinal >= kMaxDevices) return DM05_ERR_CUDA;
     try {
-        std::lock_guard<std::mutex> lk(g_kv8_mu);
-        Kv8State &st = g_kv8[dev.ordinal];
-        if (!st.ready) {
-            auto *kernel = &dm05::kv8::attn_kernel;
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     dm05::kv8::Smem::kAllocBytes) != cudaSuccess ||
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-                return DM05_ERR_CUDA;
-            st.max_cluster = 1;
-            st.active[1] = dev.num_sms;
-            for (int c = dm05::kMaxSplits; c >= 2; --c) {
-                cudaLaunchConfig_t cfg = {};
-                cfg.gridDim = dim3(static_cast<unsigned>(c), 1, 1);
-                cfg.blockDim = dim3(dm05::kv8::kThreads8, 1, 1);
-                cfg.dynamicSmemBytes = dm05::kv8::Smem::kAllocBytes;
-                cudaLaunchAttribute at[1];
-                at[0].id = cudaLaunchAttributeClusterDimension;
-                at[0].val.clusterDim.x = static_cast<unsigned>(c);
-                at[0].val.clusterDim.y = 1;
-                at[0].val.clusterDim.z = 1;
-                cfg.attrs = at;
-                cfg.numAttrs = 1;
-                int n = 0;
-                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) {
-                    st.active[c] = n;
-                    st.max_cluster = std::max(st.max_cluster, c);
-                } else {
-                    cudaGetLastError();  // clear a refused size
-                }
-            }
-            st.ready = true;
-        }
-        *out = st;
+        std::lock_guard<std::mutex> lk(g_attr_mu);
+        bool &ready = (mass ? g_mass_ready : g_kv8_ready)[dev.ordinal];
+        if (ready) return DM05_OK;
+        constexpr cudaFuncAttribute kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        bool ok;
+        if (mass)
+            ok = cudaFuncSetAttribute(&dm05::mass::mass_kernel<false>, kSmem, dm05::mass::Smem<false>::kAllocBytes) ==
+                     cudaSuccess &&
+                 cudaFuncSetAttribute(&dm05::mass::mass_kernel<true>, kSmem, dm05::mass::Smem<true>::kAllocBytes) ==
+                     cudaSuccess;
+        else
+            ok = cudaFuncSetAttribute(&dm05::kv8::attn_kernel, kSmem, dm05::kv8::Smem::kAllocBytes) == cudaSuccess;
+        if (!ok) return DM05_ERR_CUDA;
+        ready = true;
         return DM05_OK;
     } catch (...) {
         return DM05_ERR_CUDA;
@@ -118,44 +95,27 @@ int kv8_state(const Device &dev, Kv8State *out) noexcept
 }
 
 struct Kv8Plan {
-    int splits = 1, row_blocks = 1, SQ = 1;
+    int splits = 1;    // CTAs per (sample, KV head)
     size_t bytes = 0;  // partial results
 };
 
-// CTAs (a cluster) per (sample, KV head, query block) and query blocks, as
-// for the bf16 call: the lowest estimated cost among the plans whose
-// clusters are all resident at once.
-Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev, const Kv8State &st)
+// The fewest CTAs per (sample, KV head) that make the longest run of tiles as
+// short as one wave allows; unsplit while that is as short.
+Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
 {
     const long long units = static_cast<long long>(B) * Hkv;
-    const int G = Hq / Hkv;
     const int tiles = (P + dm05::kv8::kTile - 1) / dm05::kv8::kTile + (S + dm05::kv8::kSufTile - 1) / dm05::kv8::kSufTile;
-    Kv8Plan best;
-    best.SQ = S;
-    double best_cost = 1e30;
-    for (int c = 1; c <= dm05::kMaxSplits; ++c) {
-        if (dev.split_override > 0 && c != std::min(dev.split_override, st.max_cluster)) continue;
-        if (st.active[c] == 0) continue;
-        if (dev.split_override == 0 && (c > tiles || (c & (c - 1)) != 0)) continue;
-        for (int r = 1; r <= 16; ++r) {
-            const int sq = (S + r - 1) / r;
-            if (r > 1 && (c == 1 || sq < 8 || (S + sq - 1) / sq != r || G * ((sq + 7) / 8 * 8) > dm05::kMRows)) continue;
-            if (dev.row_block_override > 0 && r != dev.row_block_override && r != 1) continue;
-            if (dev.split_override == 0 && c > 1 && (units * r * c > dev.num_sms || units * r > st.active[c])) continue;
-            double cost = 1.2 * ((tiles + c - 1) / c);
-            cost += c > 1 ? 6.9 + 0.04 * G * sq : 3.5;
-            if (dev.row_block_override > 0 && r == dev.row_block_override) cost -= 1e6;
-            if (cost < best_cost) {
-                best_cost = cost;
-                best.splits = c;
-                best.row_blocks = r;
-                best.SQ = sq;
-            }
-        }
+    const int most = static_cast<int>(std::min<long long>(
+        std::min(tiles, dm05::kv8::kMaxSplits8), std::max<long long>(1, dev.num_sms / units)));
+    Kv8Plan pl;
+    if (dev.split_override > 0) {
+        pl.splits = dev.split_override;
+    } else {
+        const int run = (tiles + most - 1) / most;
+        pl.splits = (tiles + run - 1) / run;
     }
-    if (best.splits > 1)
-        best.bytes = static_cast<size_t>(units) * best.row_blocks * best.splits * G * best.SQ * dm05::kv8::Smem::kStageStride;
-    return best;
+    if (pl.splits > 1) pl.bytes = static_cast<size_t>(units) * pl.splits * (Hq / Hkv) * S * dm05::kv8::kPartRow;
+    return pl;
 }
 
 int kv8_check(int B, int Hq, int Hkv, int P, int S, int D)
@@ -185,36 +145,7 @@ int encode_rows8(CUtensorMap *map, const void *base, int rows, int units, int bo
     return dm05::internal::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box);
 }
 
-// bf16 [units][rows][256] in boxes of 64 columns x box_rows rows (one query head's block)
-int encode_rows16_chunk(CUtensorMap *map, const void *base, int rows, int units, int box_rows)
-{
-    const cuuint64_t dims[3] = {256, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(units)};
-    const cuuint64_t strides[2] = {512, static_cast<cuuint64_t>(rows) * 512};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-    return dm05::internal::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box);
-}
-
 // ---------------------------------------------------------------- accumulated weight
-
-bool g_mass_ready[kMaxDevices];  // guarded by g_kv8_mu
-
-int mass_attributes(const Device &dev) noexcept
-{
-    if (dev.ordinal < 0 || dev.ordinal >= kMaxDevices) return DM05_ERR_CUDA;
-    try {
-        std::lock_guard<std::mutex> lk(g_kv8_mu);
-        if (g_mass_ready[dev.ordinal]) return DM05_OK;
-        if (cudaFuncSetAttribute(&dm05::mass::mass_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 dm05::mass::Smem<false>::kAllocBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(&dm05::mass::mass_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 dm05::mass::Smem<true>::kAllocBytes) != cudaSuccess)
-            return DM05_ERR_CUDA;
-        g_mass_ready[dev.ordinal] = true;
-        return DM05_OK;
-    } catch (...) {
-        return DM05_ERR_CUDA;
-    }
-}
 
 // CTAs per unit: the fewest waves x (set-up + tiles a CTA walks), set-up
 // counted as two tiles.
@@ -249,7 +180,7 @@ int mass_call(bool kv8, const void *q, const void *k, const float *k_scale, int 
     Device dev;
     rc = dm05::internal::device(stream, true, &dev);
     if (rc != DM05_OK) return rc;
-    if ((rc = mass_attributes(dev)) != DM05_OK) return rc;
+    if ((rc = set_attributes(dev, true)) != DM05_OK) return rc;
     const int units = B * Hkv, GS = Hq / Hkv * S, N = (GS + 15) / 16 * 16;
     CUtensorMap tq, tk;
     if (encode_rows16(&tq, q, GS, units, N) != DM05_OK ||
@@ -366,18 +297,15 @@ int dm05_kv8_quantize(const void *k, const void *v, const int32_t *valid_len, vo
 }
 
 int dm05_suffix_attn_kv8_plan(int B, int Hq, int Hkv, int P, int S, int D, int *splits_per_head, int *tile_rows,
-                              int *row_blocks, size_t *workspace_bytes)
+                              size_t *workspace_bytes)
 {
     int rc = kv8_check(B, Hq, Hkv, P, S, D);
     if (rc != DM05_OK) return rc;
     Device dev;
-    Kv8State st;
-    if ((rc = dm05::internal::device(nullptr, false, &dev)) != DM05_OK || (rc = kv8_state(dev, &st)) != DM05_OK)
-        return rc;
-    const Kv8Plan pl = kv8_plan(B, Hq, Hkv, P, S, dev, st);
+    if ((rc = dm05::internal::device(nullptr, false, &dev)) != DM05_OK) return rc;
+    const Kv8Plan pl = kv8_plan(B, Hq, Hkv, P, S, dev);
     if (splits_per_head) *splits_per_head = pl.splits;
     if (tile_rows) *tile_rows = dm05::kv8::kTile;
-    if (row_blocks) *row_blocks = pl.row_blocks;
     if (workspace_bytes) *workspace_bytes = pl.bytes;
     return DM05_OK;
 }
@@ -398,21 +326,17 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
         (P > 0 && (!aligned(k8, 16) || !aligned(v8, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))))
         return DM05_ERR_ALIGN;
     Device dev;
-    Kv8State st;
-    if ((rc = dm05::internal::device(stream, true, &dev)) != DM05_OK || (rc = kv8_state(dev, &st)) != DM05_OK)
+    if ((rc = dm05::internal::device(stream, true, &dev)) != DM05_OK || (rc = set_attributes(dev, false)) != DM05_OK)
         return rc;
-    const Kv8Plan pl = kv8_plan(B, Hq, Hkv, P, S, dev, st);
+    const Kv8Plan pl = kv8_plan(B, Hq, Hkv, P, S, dev);
     if (pl.bytes > 0) {
         if (workspace == nullptr || workspace_bytes < pl.bytes) return DM05_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return DM05_ERR_ALIGN;
     }
-    const int G = Hq / Hkv, units = B * Hkv;
-    const long long grid = static_cast<long long>(units) * pl.row_blocks * pl.splits;
-    if (grid > 0x7fffffffLL) return DM05_ERR_SHAPE;
+    const int GS = Hq / Hkv * S, units = B * Hkv, qrows = (GS + 7) / 8 * 8;
     CUtensorMap tq, tkp, tvp, tks, tvs;
-    const int rq = pl.row_blocks == 1 ? encode_rows16(&tq, q, G * S, units, dm05::kMRows)
-                                      : encode_rows16_chunk(&tq, q, G * S, units, pl.SQ);
-    if (rq != DM05_OK || encode_rows16(&tks, k_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK ||
+    if (encode_rows16(&tq, q, GS, units, qrows) != DM05_OK ||
+        encode_rows16(&tks, k_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK ||
         encode_rows16(&tvs, v_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK)
         return DM05_ERR_CUDA;
     if (P > 0) {
@@ -431,34 +355,37 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     ap.out = static_cast<__nv_bfloat16 *>(out);
     ap.lse = lse;
     ap.err = dev.err;
-    ap.part = static_cast<float *>(workspace);
+    ap.part = static_cast<uint8_t *>(workspace);
     ap.Hkv = Hkv;
     ap.P = P;
     ap.S = S;
-    ap.GS = G * S;
-    ap.G = G;
-    ap.row_blocks = pl.row_blocks;
-    ap.SQ = pl.SQ;
+    ap.GS = GS;
+    ap.qrows = qrows;
     ap.splits = pl.splits;
     ap.nblk = blocks_of(P, shift);
     ap.shift = shift;
     ap.scale_log2 = static_cast<float>(kLog2e / std::sqrt(static_cast<double>(D)));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(units * pl.splits), 1, 1);
     cfg.blockDim = dim3(dm05::kv8::kThreads8, 1, 1);
     cfg.dynamicSmemBytes = dm05::kv8::Smem::kAllocBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute at[2];
+    cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = static_cast<unsigned>(pl.splits);
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = pl.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, &dm05::kv8::attn_kernel, tq, tkp, tvp, tks, tvs, ap) == cudaSuccess ? DM05_OK
-                                                                                                         : DM05_ERR_CUDA;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, &dm05::kv8::attn_kernel, tq, tkp, tvp, tks, tvs, ap) != cudaSuccess)
+        return DM05_ERR_CUDA;
+    if (pl.splits == 1) return DM05_OK;
+    dm05::kv8::MergeParams mp = {};
+    mp.part = ap.part;
+    mp.out = ap.out;
+    mp.lse = lse;
+    mp.rows = units * GS;
+    mp.GS = GS;
+    mp.splits = pl.splits;
+    return launch(dm05::kv8::merge_kernel, dim3(static_cast<unsigned>((mp.rows + 3) / 4)), 128, 0, stream, mp);
 }
 
 int dm05_prefix_attn_mass(const void *q, const void *k_prefix, const int32_t *prefix_valid_len,

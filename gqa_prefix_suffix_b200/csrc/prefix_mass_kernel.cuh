@@ -202,16 +202,19 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 failed = !warp_wait(&bars[L::kBarQFull], 0);
                 uint8_t *chunk = smem + c4 * p.N * 128 + row * 128;
                 uint32_t *qmax = reinterpret_cast<uint32_t *>(sums) + row;  // [4][128]
+                uint4 v[8];
                 if (!failed) {
-                    qmax[c4 * 128] = row < p.N ? kv8::chunk_max(chunk, row & 7) : 0u;
+                    if (row < p.GS) qmax[c4 * 128] = kv8::read_chunk(chunk, row & 7, v);
                     failed = !row_sync();
                 }
                 if (!failed) {
-                    const uint32_t bits = max(max(qmax[0], qmax[128]), max(qmax[256], qmax[384]));
-                    const float s = kv8::row_scale(bits);
-                    // a row with a non-finite element becomes NaN
-                    scale = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
-                    if (row < p.N) kv8::split_chunk(chunk, row & 7, cache::pow2_inverse(s));
+                    if (row < p.GS) {
+                        const uint32_t bits = max(max(qmax[0], qmax[128]), max(qmax[256], qmax[384]));
+                        const float s = kv8::row_scale(bits);
+                        // a row with a non-finite element becomes NaN
+                        scale = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
+                        kv8::split_chunk(chunk, row & 7, cache::pow2_inverse(s), v);
+                    }
                     ptx::fence_proxy_async_smem();
                     failed = !row_sync();  // qmax is read: the sums may be written
                 }

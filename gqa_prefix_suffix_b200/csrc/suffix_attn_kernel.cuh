@@ -232,7 +232,7 @@ __device__ __forceinline__ size_t block_out_row(size_t unit_row0, int k, int nq,
 // statistic of each partial row, the LSE is written, and orow[rr] receives
 // the row's output row (or -1 when the row is not written), so that pass 2
 // does no index arithmetic.
-template <class L, int THREADS = kThreads>
+template <class L>
 __device__ __forceinline__ void merge_weights(uint8_t *recv, int C, int nr, float *lse, size_t unit_row0, int k_lo,
                                               int nq, int S, int q0, int jlim, long long *orow)
 {
@@ -243,7 +243,7 @@ __device__ __forceinline__ void merge_weights(uint8_t *recv, int C, int nr, floa
     const int seg = lane / W, c = lane - seg * W;
     const size_t cstride = static_cast<size_t>(nr) * L::kStageStride;
     // every lane of the warp runs the same number of rounds (shuffles need them all)
-    for (int base = warp * per_warp; base < nr; base += (THREADS / 32) * per_warp) {
+    for (int base = warp * per_warp; base < nr; base += (kThreads / 32) * per_warp) {
         const int rr = base + seg;
         const bool row_ok = rr < nr;
         float4 st = make_float4(-INFINITY, 0.f, 0.f, 0.f);
@@ -273,14 +273,14 @@ __device__ __forceinline__ void merge_weights(uint8_t *recv, int C, int nr, floa
 
 // Pass 2 (after a CTA barrier): one item per (row, 4-column quad):
 // out = sum_c wn_c O_c, two partials' loads in flight at a time.
-template <class L, int THREADS = kThreads>
+template <class L>
 __device__ __forceinline__ void merge_rows(const uint8_t *recv, int C, int nr, __nv_bfloat16 *out,
                                            const long long *orow)
 {
     const int items = nr * (kHeadDim / 4);
     const size_t cstride = static_cast<size_t>(nr) * L::kStageStride;
     int trace_n = 0;
-    for (int i = threadIdx.x; i < items; i += THREADS) {
+    for (int i = threadIdx.x; i < items; i += kThreads) {
         const int rr = i / (kHeadDim / 4), ch = i - rr * (kHeadDim / 4);
         if (threadIdx.x == 0 && trace_n < 2) DM05_TRACE_TILE(4 + trace_n, 22);
         ++trace_n;

@@ -386,10 +386,11 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
                          int Hq, int Hkv, int P, int S, int D, cudaStream_t stream);
 
 /* Work plan of a dm05_suffix_attn_kv8 call with these sizes on the current
- * device, as dm05_suffix_attn_plan (the overrides apply), and the workspace
- * it needs.  Any output pointer may be NULL. */
+ * device: CTAs per (sample, KV head) (dm05_set_split_override applies), key
+ * rows of a prefix tile, and the workspace the call needs.  Any output
+ * pointer may be NULL. */
 int dm05_suffix_attn_kv8_plan(int B, int Hq, int Hkv, int P, int S, int D, int *splits_per_head, int *tile_rows,
-                              int *row_blocks, size_t *workspace_bytes);
+                              size_t *workspace_bytes);
 
 /*
  * dm05_prefix_attn_mass -- the attention weight each prefix position

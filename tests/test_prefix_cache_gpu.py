@@ -229,15 +229,15 @@ def test_attention_queries_of_very_different_size():
     check_attention(g, 1, 8, 4, 300, 30, 64, q=q.to(BF))
 
 
-@pytest.mark.parametrize("splits,row_blocks", [(1, 0), (2, 1), (3, 1), (4, 2), (8, 3), (16, 1), (16, 4)])
-def test_attention_forced_plans(splits, row_blocks):
+@pytest.mark.parametrize("splits", [1, 2, 3, 4, 7, 8, 16])
+def test_attention_forced_plans(splits):
     try:
-        assert bd.dm05_set_split_override(splits) == 0 and bd.dm05_set_row_block_override(row_blocks) == 0
+        assert bd.dm05_set_split_override(splits) == 0
+        assert bd.dm05_suffix_attn_kv8_plan(2, 8, 4, 900, 50, 256)[1] == splits
         check_attention(gen(splits), 2, 8, 4, 900, 50, 64, [900, 130])
         check_attention(gen(splits), 1, 8, 4, 70, 11, 16, [3])   # more splits than tiles
     finally:
         bd.dm05_set_split_override(0)
-        bd.dm05_set_row_block_override(0)
 
 
 def test_attention_never_uses_hidden_rows():
