@@ -24,8 +24,10 @@
 //     for 128 x 256 x 32 with A in tensor memory; 2.1k cycles per 128 keys.
 //   * The running maximum is taken over z + log2(vs) (log2 units), that is
 //     over the weights the PV product sees, with the same lazy update as the
-//     bf16 kernel: p vs is at most 2^8 and a new maximum sits at 2^6, so the
-//     smallest step of the second term (2^-9) is 2^-15 of the largest weight.
+//     bf16 kernel: a new maximum sits at 2^4 and weights may grow to 2^8.75
+//     before O is rescaled, so the smallest step of the second term (2^-9) is
+//     at most 2^-13 of the largest weight.  (Any of 32 rows asks for a
+//     rescale: with 2^6 and 2^8 most tiles of a batch with peaked keys had one.)
 //
 // One CTA walks a contiguous run of a unit's key tiles: the suffix tiles (64
 // rows of bf16, kind::f16), then prefix tiles of 128 codes, each 32 KB of K
@@ -90,6 +92,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
+// 4-D tiled bulk tensor store shared -> global (rows past the tensor's end are
+// not written); completion by bulk group.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *smem_src, int c0, int c1, int c2, int c3)
+{
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_addr(smem_src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
 // a * b, lane-wise, rounded to nearest
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
 {
@@ -118,11 +130,12 @@ constexpr int kSoftWarps = 16;       // two groups of eight, each two warps per 
 constexpr int kLoadWarp = 16;        // Q and K
 constexpr int kIssueWarp = 17;
 constexpr int kLoadVWarp = 18;
-constexpr int kThreads8 = 608;
+constexpr int kClearWarp = 19;       // clears hidden V rows
+constexpr int kThreads8 = 640;
 constexpr uint32_t kTmemO8 = 0;      // O: columns [0, 256)
 constexpr uint32_t kTmemS8 = 256;    // two S / P buffers of 128 columns
-constexpr float kTopBits = 6.0f;     // a new maximum's weight is 2^6 ...
-constexpr float kMaxBits = 8.0f;     // ... and may grow to 2^8 before O is rescaled (e4m3 ends at 448)
+constexpr float kTopBits = 4.0f;     // a new maximum's weight is 2^4 ...
+constexpr float kMaxBits = 8.75f;    // ... and may grow to 2^8.75 before O is rescaled (e4m3 ends at 448 = 2^8.8)
 // Codes reach up to 448 where suffix values have their own size, so a suffix
 // weight (bf16, any size will do) counts 2^-7 of itself in the maximum: the
 // prefix weights of ordinary data then use the upper part of e4m3's range
@@ -152,7 +165,9 @@ struct Smem {
     static constexpr int kBarRow = kBarMmaFinal + 1;  // per lane quarter: its four warps
     static constexpr int kBarPair = kBarRow + 4;    // per group and lane quarter: its two warps
     static constexpr int kBarMax = kBarPair + 8;    // per lane quarter: tile t's reference maximum is known
-    static constexpr int kNumBars = kBarMax + 4;
+    static constexpr int kBarOut = kBarMax + 4;     // every row staged on its way out
+    static constexpr int kBarClear = kBarOut + 1;   // per V slot: its hidden rows cleared
+    static constexpr int kNumBars = kBarClear + kSlots;
     static constexpr int kBarOff = kDataEnd;
     static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
     // tile maxima [2 groups][2 halves][128], reference maxima [2][128], sums
@@ -160,9 +175,7 @@ struct Smem {
     static constexpr int kXchgOff = (kTmemSlotOff + 16 + 15) / 16 * 16;
     static constexpr int kEnd = kXchgOff + (4 + 2 + 4) * kMRows * 4 + kSoftWarps * 64 * 4;
     static constexpr int kAllocBytes = kEnd + 1024;
-    static constexpr int kStageStride = kPartRow;
-    static constexpr int kOutStride = kHeadDim * 2 + 16;    // an output row on its way out
-    static_assert(kDataEnd >= kMRows * kStageStride, "the rows staged on their way out");
+    static_assert(kDataEnd >= kMRows * kPartRow, "the rows staged on their way out");
     static_assert(kAllocBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -170,7 +183,6 @@ struct Params {
     const float *k_scale, *v_scale;  // [units, nblk]
     const int32_t *valid_len;
     const uint8_t *mask;
-    __nv_bfloat16 *out;
     float *lse;
     uint32_t *err;
     uint8_t *part;                   // splits > 1: partial rows [units][splits][GS], kPartRow bytes each
@@ -216,16 +228,16 @@ __device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3
 }
 
 // A query row is cut into four chunks of 64 bf16 (128 swizzled bytes each;
-// sw: the row's swizzle).  A thread takes one chunk of a row: reads it and
-// returns its largest magnitude as bf16 bits (magnitudes order like their bits).
-__device__ __forceinline__ uint32_t read_chunk(const uint8_t *chunk, uint32_t sw, uint4 (&v)[8])
+// sw: the row's swizzle).  A thread takes one chunk of a row: its largest
+// magnitude as bf16 bits (magnitudes order like their bits).
+__device__ __forceinline__ uint32_t chunk_max(const uint8_t *chunk, uint32_t sw)
 {
     uint32_t top = 0u;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-        v[u] = *reinterpret_cast<const uint4 *>(chunk + ((u ^ sw) << 4));
-        top = __vmaxu2(__vmaxu2(top, v[u].x & 0x7fff7fffu), __vmaxu2(v[u].y & 0x7fff7fffu, v[u].z & 0x7fff7fffu));
-        top = __vmaxu2(top, v[u].w & 0x7fff7fffu);
+        const uint4 v = *reinterpret_cast<const uint4 *>(chunk + ((u ^ sw) << 4));
+        top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
+        top = __vmaxu2(top, v.w & 0x7fff7fffu);
     }
     return max(top & 0xffffu, top >> 16);
 }
@@ -237,22 +249,25 @@ __device__ __forceinline__ float row_scale(uint32_t bits)
     return bits < 0x7f80u ? cache::pow2_scale(__uint_as_float(bits << 16)) : 1.0f;
 }
 
-// Writes the chunk back as two e4m3 terms of its scaled values: the 64 bytes
-// of 32 bf16 values become their 32 first terms, then their 32 second ones, so
+// Rewrites the chunk as two e4m3 terms of its scaled values: the 64 bytes of
+// 32 bf16 values become their 32 first terms, then their 32 second ones, so
 // a thread rewrites only what it has read.
-__device__ __forceinline__ void split_chunk(uint8_t *chunk, uint32_t sw, float inv, const uint4 (&v)[8])
+__device__ __forceinline__ void split_chunk(uint8_t *chunk, uint32_t sw, float inv)
 {
-#pragma unroll
+#pragma unroll 1
     for (int g = 0; g < 2; ++g) {
+        auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + (((g * 4 + u) ^ sw) << 4)); };
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = *unit16(u);
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint4 &src = v[g * 4 + (e >> 1)];
+            const uint4 &src = v[e >> 1];
             const uint32_t w0 = (e & 1) ? src.z : src.x, w1 = (e & 1) ? src.w : src.y;
             two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
                       __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
         }
-        auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + (((g * 4 + u) ^ sw) << 4)); };
         *unit16(0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *unit16(1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
         *unit16(2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -263,7 +278,8 @@ __device__ __forceinline__ void split_chunk(uint8_t *chunk, uint32_t sw, float i
 __global__ void __launch_bounds__(kThreads8, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
                 const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ks,
-                const __grid_constant__ CUtensorMap tm_vs, const Params p)
+                const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ CUtensorMap tm_out,
+                const Params p)
 {
     using L = Smem;
     extern __shared__ uint8_t smem_raw[];
@@ -285,6 +301,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             ptx::mbar_init(&bars[L::kBarKEmpty + i], 1);
             ptx::mbar_init(&bars[L::kBarVFull + i], 1);
             ptx::mbar_init(&bars[L::kBarVEmpty + i], 1);
+            ptx::mbar_init(&bars[L::kBarClear + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bars[L::kBarSFull + i], 1);
@@ -292,6 +309,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             ptx::mbar_init(&bars[L::kBarPFree + i], 1);
         }
         ptx::mbar_init(&bars[L::kBarMmaFinal], 1);
+        ptx::mbar_init(&bars[L::kBarOut], kSoftWarps * 32);
         for (int i = 0; i < 4; ++i) {
             ptx::mbar_init(&bars[L::kBarRow + i], 128);
             ptx::mbar_init(&bars[L::kBarPair + i], 64);
@@ -353,9 +371,57 @@ __global__ void __launch_bounds__(kThreads8, 1)
     // first row of local tile t and how many of its rows are in range
     auto row0_of = [&](int t) { return t < ns ? (t_begin + t) * kSufTile : (t_begin + t - TS) * kTile; };
     auto rows_of = [&](int t) { return t < ns ? min(kSufTile, p.S - row0_of(t)) : min(kTile, vl - row0_of(t)); };
+    const uint8_t *mask_row = p.mask ? p.mask + static_cast<size_t>(b) * p.P : nullptr;
+    // prefix tiles that may hold rows no query sees
+    auto partial_at = [&](int t) { return mask_row != nullptr || rows_of(t) < kTile; };
     bool failed = false;
 
-    if (warp == kLoadWarp || warp == kLoadVWarp) {
+    if (warp == kClearWarp) {
+        // ================================================== hidden V rows
+        // Hidden rows, and rows past the valid length that a tile's last 32-row
+        // step reads, may hold NaN codes, and 0 * NaN would poison O: they are
+        // cleared once the tile has landed (by the softmax warps, after their
+        // weights, this took 1k cycles a tile).  Every tile is passed on, so
+        // that no phase of its barrier goes by unseen here.
+        uint32_t see_next[4];
+        auto load_next = [&](int t) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int c = w * 32 + lane;
+                see_next[w] = t >= ns && t < T && c < rows_of(t) ? (mask_row != nullptr ? __ldg(mask_row + row0_of(t) + c) : 1u) : 0u;
+            }
+        };
+        load_next(0);
+        for (int t = 0; t < T; ++t) {
+            uint32_t hidden[4];
+            const int n32 = (rows_of(t) + 31) / 32;  // 32-row steps that PV reads
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                hidden[w] = __ballot_sync(0xffffffffu, see_next[w] == 0u);
+                if (w >= n32 || t < ns) hidden[w] = 0u;
+            }
+            load_next(t + 1);
+            if (!warp_wait(&bars[L::kBarVFull + t % kSlots], (t / kSlots) & 1)) {
+                failed = true;
+                break;
+            }
+            // two rows at a time, 16 lanes each
+            uint8_t *vt = v_slot(t) + ((lane & 15) >> 3) * (kTile * 128) + (lane & 7) * 16;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                for (uint32_t h = hidden[w]; h != 0u;) {
+                    const int r0 = __ffs(static_cast<int>(h)) - 1;
+                    h &= h - 1u;
+                    const int r1 = h != 0u ? __ffs(static_cast<int>(h)) - 1 : r0;
+                    h &= h - 1u;
+                    *reinterpret_cast<uint4 *>(vt + (w * 32 + (lane < 16 ? r0 : r1)) * 128) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars[L::kBarClear + t % kSlots]);
+        }
+    } else if (warp == kLoadWarp || warp == kLoadVWarp) {
         // ================================================== TMA producers (K, V)
         if (lane == 0) {
             const bool is_v = warp == kLoadVWarp;
@@ -397,6 +463,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const int pb = buffer_of(u, ns), s = u % kSlots;
                 if (!ptx::mbar_wait(&bars[L::kBarPReady + pb], uses_before(u, ns) & 1, kWaitLimitNs)) return false;
                 if (!ptx::mbar_wait(&bars[L::kBarVFull + s], (u / kSlots) & 1, kWaitLimitNs)) return false;
+                if (!ptx::mbar_wait(&bars[L::kBarClear + s], (u / kSlots) & 1, kWaitLimitNs)) return false;
                 ptx::tc_fence_after_sync();
                 const uint32_t a = tmem + kTmemS8 + pb * kTile;
                 const int n = rows_of(u);
@@ -491,7 +558,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
         const int c4 = warp >> 2;  // column quarter of Q and of O
         const int row = q4 * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
-        const uint8_t *mask_row = p.mask ? p.mask + static_cast<size_t>(b) * p.P : nullptr;
         const float *ksc = p.k_scale + static_cast<size_t>(unit) * p.nblk;
         const float *vsc = p.v_scale + static_cast<size_t>(unit) * p.nblk;
         float *xmax = reinterpret_cast<float *>(smem + L::kXchgOff) + grp * 2 * kMRows;  // [2 halves][128] of this group
@@ -517,9 +583,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
             uint8_t *chunk = smem + c4 * qpitch + row * 128;
             uint32_t *qmax = reinterpret_cast<uint32_t *>(xl) + row;  // [4][128]
             const bool mine = row < p.GS;
-            uint4 v[8];
             if (!failed) {
-                if (mine) qmax[c4 * kMRows] = read_chunk(chunk, row & 7, v);
+                if (mine) qmax[c4 * kMRows] = chunk_max(chunk, row & 7);
                 failed = !row_sync();
             }
             if (!failed) {
@@ -528,7 +593,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const float s = row_scale(bits);
                     // a row with a non-finite element becomes NaN
                     sqs = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
-                    split_chunk(chunk, row & 7, cache::pow2_inverse(s), v);
+                    split_chunk(chunk, row & 7, cache::pow2_inverse(s));
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(&bars[L::kBarQConv]);
@@ -568,7 +633,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const int n = rows_of(t);
             uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
             float ag[4], bg[4], ig[4];
-            const bool partial = n < kTile || mask_row != nullptr;
+            const bool partial = t >= ns && partial_at(t);
             if (t >= ns) {
                 if (partial) {
 #pragma unroll
@@ -738,39 +803,20 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 ptx::tc_fence_after_sync();
                 const float factor = rescale ? ptx::ex2(m_old - m_used) : 1.0f;  // 0 when m_old is -inf
 #pragma unroll 1
-                for (int j = 0; j < kHeadDim / 32; ++j) {
-                    uint32_t o[16];
-                    const uint32_t oc = tmem + lane_base + kTmemO8 + hf * (kHeadDim / 2) + j * 16;
-                    ptx::tmem_ld16(oc, o);
+                for (int j = 0; j < kHeadDim / 64; ++j) {
+                    uint32_t o[2][16];
+                    const uint32_t oc = tmem + lane_base + kTmemO8 + hf * (kHeadDim / 2) + j * 32;
+                    ptx::tmem_ld16(oc, o[0]);
+                    ptx::tmem_ld16(oc + 16, o[1]);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-                    ptx::tmem_st16(oc, o);
+                    for (int e = 0; e < 32; ++e)
+                        o[e >> 4][e & 15] = __float_as_uint(__uint_as_float(o[e >> 4][e & 15]) * factor);
+                    ptx::tmem_st16(oc, o[0]);
+                    ptx::tmem_st16(oc + 16, o[1]);
                 }
             }
             ptx::tmem_st_wait();
-            if (t >= ns && partial) {
-                // hidden rows, and rows past the valid length that the last
-                // 32-row step reads, may hold NaN codes, and 0 * NaN would
-                // poison O: they are cleared.  The half's four warps take them in turn.
-                const int left = (n + 31) / 32 * 32 - hf * 64;  // rows of this half that PV reads
-                uint64_t hidden = ~(static_cast<uint64_t>(vis[1]) << 32 | vis[0]);
-                hidden &= left <= 0 ? 0ull : left >= 64 ? ~0ull : (1ull << left) - 1ull;
-                if (hidden != 0ull) {
-                    if (!warp_wait(&bars[L::kBarVFull + t % kSlots], (t / kSlots) & 1)) {
-                        failed = true;
-                        break;
-                    }
-                    uint8_t *vt = v_slot(t) + hf * 64 * 128;
-                    for (int k = 0; hidden != 0ull; ++k, hidden &= hidden - 1ull) {
-                        const int r = __ffsll(static_cast<long long>(hidden)) - 1;
-                        if ((k & 3) == q4 && lane < 16)
-                            *reinterpret_cast<uint4 *>(vt + (lane >> 3) * (kTile * 128) + r * 128 + (lane & 7) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    ptx::fence_proxy_async_smem();
-                }
-            }
             ptx::tc_fence_before_sync();
             ptx::mbar_arrive(&bars[L::kBarPReady + sb]);
         }
@@ -796,32 +842,34 @@ __global__ void __launch_bounds__(kThreads8, 1)
         if (!failed && !row_sync()) failed = true;
         const float l_row = (xl[row] + xl[kMRows + row]) + (xl[2 * kMRows + row] + xl[3 * kMRows + row]);
         const bool row_valid = row < p.GS;
-        const size_t out_row = static_cast<size_t>(unit) * p.GS + row;
         const float inv_l = 1.0f / l_row;
-        // Rows leave through shared memory: a thread's columns of its row, then
-        // one bulk store of the whole row (16-byte stores of 32 rows at once
-        // took 5k cycles a CTA).
-        uint8_t *srow = smem + row * (C == 1 ? L::kOutStride : L::kStageStride);
+        // The rows leave through shared memory in one copy: bf16 rows in the
+        // layout of a Q tile, partial rows as they lie in the workspace.
+        // (16-byte stores of 32 rows at a time took 5k cycles a CTA, one bulk
+        // store a row 3.7k.)
         if (have_o && !failed) {
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
                 uint32_t o[2][16];
-                const int col = c4 * (kHeadDim / 4) + j * 32;
-                ptx::tmem_ld16(tmem + lane_base + kTmemO8 + col, o[0]);
-                ptx::tmem_ld16(tmem + lane_base + kTmemO8 + col + 16, o[1]);
+                const uint32_t oc = tmem + lane_base + kTmemO8 + c4 * (kHeadDim / 4) + j * 32;
+                ptx::tmem_ld16(oc, o[0]);
+                ptx::tmem_ld16(oc + 16, o[1]);
                 ptx::tmem_ld_wait();
                 if (!row_valid) continue;
                 if (C == 1) {
-                    uint32_t w[16];
+                    uint8_t *dst = smem + c4 * qpitch + row * 128;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        w[e] = pack_bf16x2(__uint_as_float(o[e >> 3][2 * (e & 7)]) * inv_l,
-                                           __uint_as_float(o[e >> 3][2 * (e & 7) + 1]) * inv_l);
-                    uint4 *dst = reinterpret_cast<uint4 *>(srow + col * 2);
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                        for (int f = 0; f < 4; ++f)
+                            w[f] = pack_bf16x2(__uint_as_float(o[e >> 1][(e & 1) * 8 + 2 * f]) * inv_l,
+                                               __uint_as_float(o[e >> 1][(e & 1) * 8 + 2 * f + 1]) * inv_l);
+                        *reinterpret_cast<uint4 *>(dst + (((j * 4 + e) ^ (row & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(srow + col * 4);
+                    uint4 *dst = reinterpret_cast<uint4 *>(smem + row * kPartRow + (c4 * (kHeadDim / 4) + j * 32) * 4);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e] = make_uint4(o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1], o[e >> 2][4 * (e & 3) + 2],
@@ -829,25 +877,28 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 }
             }
         }
-        if (row_valid) {
-            if (C > 1 && c4 == 0) {
-                *reinterpret_cast<float4 *>(srow + kHeadDim * 4) =
+        if (c4 == 0 && row_valid) {
+            if (C > 1)
+                *reinterpret_cast<float4 *>(smem + row * kPartRow + kHeadDim * 4) =
                     make_float4(m_end, have_o && !failed ? l_row : 0.0f, 0.0f, 0.0f);
-            }
-            ptx::fence_proxy_async_smem();
+            else if (p.lse != nullptr && !failed)
+                p.lse[static_cast<size_t>(unit) * p.GS + row] = (m_end + ptx::lg2(l_row)) * 0.69314718055994531f;
         }
-        if (!failed && !row_sync()) failed = true;  // the whole row staged
-        if (row_valid && c4 == 0 && !failed) {
-            if (C == 1) {
-                ptx::bulk_store_s2g(p.out + out_row * kHeadDim, ptx::smem_addr(srow), kHeadDim * 2);
-                if (p.lse != nullptr) p.lse[out_row] = (m_end + ptx::lg2(l_row)) * 0.69314718055994531f;
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&bars[L::kBarOut]);
+        if (threadIdx.x == 0 && !failed) {
+            if (ptx::mbar_wait(&bars[L::kBarOut], 0, kWaitLimitNs)) {
+                if (C == 1)
+                    ptx::tma_store_4d(&tm_out, smem, 0, 0, 0, unit);
+                else
+                    ptx::bulk_store_s2g(p.part + (static_cast<size_t>(unit) * C + rank) * p.GS * kPartRow,
+                                        ptx::smem_addr(smem), static_cast<uint32_t>(p.GS * kPartRow));
+                ptx::bulk_commit();
+                ptx::bulk_wait_all();
+                ptx::fence_proxy_async_global();
             } else {
-                const size_t prow = (static_cast<size_t>(unit) * C + rank) * p.GS + row;
-                ptx::bulk_store_s2g(p.part + prow * kPartRow, ptx::smem_addr(srow), kPartRow);
+                failed = true;
             }
-            ptx::bulk_commit();
-            ptx::bulk_wait_all();
-            ptx::fence_proxy_async_global();
         }
     }
 
@@ -868,19 +919,25 @@ struct MergeParams {
     int rows, GS, splits;  // rows: units * GS
 };
 
-// Joins the partial rows of a split call, one warp a row: with
+// Joins the partial rows of a split call, two warps a row: with
 // M = max_c m_c and w_c = 2^(m_c - M), out = sum_c w_c O_c / sum_c w_c l_c and
 // lse = (M + log2 sum_c w_c l_c) ln 2.  A partial without keys (l = 0) has no
-// weight, whatever its O holds.
-__global__ void __launch_bounds__(128) merge_kernel(const MergeParams p)
+// weight, whatever its O holds.  Latency is all there is: the first eight
+// partials are requested before their weights are known.
+__global__ void __launch_bounds__(256) merge_kernel(const MergeParams p)
 {
+    constexpr int kAhead = 8;
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int r = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 31, col4 = threadIdx.x & 63;
     if (r >= p.rows) return;
     const int unit = r / p.GS, row = r - unit * p.GS;
     const uint8_t *base = p.part + (static_cast<size_t>(unit) * p.splits * p.GS + row) * kPartRow;
     const size_t step = static_cast<size_t>(p.GS) * kPartRow;
+    ptx::griddep_wait();
+    float4 o[kAhead];
+#pragma unroll
+    for (int c = 0; c < kAhead; ++c)
+        if (c < p.splits) o[c] = *reinterpret_cast<const float4 *>(base + c * step + col4 * 16);
     float m[2], l[2], M = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -892,7 +949,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p)
         if (l[h] != 0.0f) M = fmaxf(M, m[h]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
     float w[2], total = 0.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -900,22 +957,25 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p)
         total = fmaf(w[h], l[h], total);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int c = 0; c < p.splits; ++c) {
+    for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](int c, const float4 &v) {
         const float wc = __shfl_sync(0xffffffffu, c < 32 ? w[0] : w[1], c & 31);
-        const float4 *o = reinterpret_cast<const float4 *>(base + c * step);
-        const float4 x = o[lane], y = o[lane + 32];
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const bool use = wc != 0.0f;
+        acc.x = fmaf(wc, use ? v.x : 0.0f, acc.x);
+        acc.y = fmaf(wc, use ? v.y : 0.0f, acc.y);
+        acc.z = fmaf(wc, use ? v.z : 0.0f, acc.z);
+        acc.w = fmaf(wc, use ? v.w : 0.0f, acc.w);
+    };
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(wc, wc != 0.0f ? v[e] : 0.0f, acc[e]);
-    }
+    for (int c = 0; c < kAhead; ++c)
+        if (c < p.splits) add(c, o[c]);
+#pragma unroll 4
+    for (int c = kAhead; c < p.splits; ++c) add(c, *reinterpret_cast<const float4 *>(base + c * step + col4 * 16));
     const float inv = 1.0f / total;
-    uint2 *out = reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(r) * kHeadDim);
-    out[lane] = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    out[lane + 32] = make_uint2(pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-    if (lane == 0 && p.lse != nullptr) p.lse[r] = (M + ptx::lg2(total)) * 0.69314718055994531f;
+    *reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(r) * kHeadDim + col4 * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (col4 == 0 && p.lse != nullptr) p.lse[r] = (M + ptx::lg2(total)) * 0.69314718055994531f;
 }
 
 }  // namespace kv8

@@ -334,8 +334,8 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
         if (!aligned(workspace, 16)) return DM05_ERR_ALIGN;
     }
     const int GS = Hq / Hkv * S, units = B * Hkv, qrows = (GS + 7) / 8 * 8;
-    CUtensorMap tq, tkp, tvp, tks, tvs;
-    if (encode_rows16(&tq, q, GS, units, qrows) != DM05_OK ||
+    CUtensorMap tq, tkp, tvp, tks, tvs, to;
+    if (encode_rows16(&tq, q, GS, units, qrows) != DM05_OK || encode_rows16(&to, out, GS, units, qrows) != DM05_OK ||
         encode_rows16(&tks, k_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK ||
         encode_rows16(&tvs, v_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK)
         return DM05_ERR_CUDA;
@@ -352,7 +352,6 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     ap.v_scale = v_scale;
     ap.valid_len = prefix_valid_len;
     ap.mask = prefix_mask;
-    ap.out = static_cast<__nv_bfloat16 *>(out);
     ap.lse = lse;
     ap.err = dev.err;
     ap.part = static_cast<uint8_t *>(workspace);
@@ -375,17 +374,17 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, &dm05::kv8::attn_kernel, tq, tkp, tvp, tks, tvs, ap) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, &dm05::kv8::attn_kernel, tq, tkp, tvp, tks, tvs, to, ap) != cudaSuccess)
         return DM05_ERR_CUDA;
     if (pl.splits == 1) return DM05_OK;
     dm05::kv8::MergeParams mp = {};
     mp.part = ap.part;
-    mp.out = ap.out;
+    mp.out = static_cast<__nv_bfloat16 *>(out);
     mp.lse = lse;
     mp.rows = units * GS;
     mp.GS = GS;
     mp.splits = pl.splits;
-    return launch(dm05::kv8::merge_kernel, dim3(static_cast<unsigned>((mp.rows + 3) / 4)), 128, 0, stream, mp);
+    return launch(dm05::kv8::merge_kernel, dim3(static_cast<unsigned>((mp.rows + 3) / 4)), 256, 0, stream, mp);
 }
 
 int dm05_prefix_attn_mass(const void *q, const void *k_prefix, const int32_t *prefix_valid_len,

@@ -202,9 +202,8 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 failed = !warp_wait(&bars[L::kBarQFull], 0);
                 uint8_t *chunk = smem + c4 * p.N * 128 + row * 128;
                 uint32_t *qmax = reinterpret_cast<uint32_t *>(sums) + row;  // [4][128]
-                uint4 v[8];
                 if (!failed) {
-                    if (row < p.GS) qmax[c4 * 128] = kv8::read_chunk(chunk, row & 7, v);
+                    if (row < p.GS) qmax[c4 * 128] = kv8::chunk_max(chunk, row & 7);
                     failed = !row_sync();
                 }
                 if (!failed) {
@@ -213,7 +212,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                         const float s = kv8::row_scale(bits);
                         // a row with a non-finite element becomes NaN
                         scale = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
-                        kv8::split_chunk(chunk, row & 7, cache::pow2_inverse(s), v);
+                        kv8::split_chunk(chunk, row & 7, cache::pow2_inverse(s));
                     }
                     ptx::fence_proxy_async_smem();
                     failed = !row_sync();  // qmax is read: the sums may be written

@@ -84,10 +84,10 @@ def attention(q, k, v, ks, vs, vis, v_step=None):
 
     Bound on out, per element: the output's bf16 rounding (2^-8 |o|); each
     weight held in two e4m3 terms of an fp16 value (2^-4 * 2^-4 + 2^-11) or,
-    for suffix rows, in bf16 (2^-8); the two-term form's smallest step 2^-9
-    in units in which the row's largest weight is at least 2^6, so 2^-16 of the
-    largest (weight x scale) times each code; the logit error through p' = p
-    dz, once in the sum and once in the normaliser; and fp32 sums."""
+    for suffix rows, in bf16 (2^-8); the two-term form's smallest step 2^-9,
+    an error of at most 2^-10 in units in which the row's largest weight is at
+    least 2^4, so 2^-14 of the largest (weight x scale) times each code; the
+    logit error through p' = p dz, once in the sum and once in the normaliser; and fp32 sums."""
     B, Hq, S, _ = q.shape
     H = k.shape[1]
     G = Hq // H
@@ -113,7 +113,7 @@ def attention(q, k, v, ks, vs, vis, v_step=None):
             small = (p * step).amax(-1)[..., None] * (vals / step[:, None]).abs().sum(0)
             out[b, sl], lse[b, sl] = o, total
             tol[b, sl] = (2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -11 + 2 * dz + 2 * sums)[..., None] * mags
-                          + 2.0 ** -16 * small + 1e-30)
+                          + 2.0 ** -14 * small + 1e-30)
             tol_lse[b, sl] = dz + sums + 2.0 ** -21 * (1 + total.abs())
     return out, lse, tol, tol_lse
 
