@@ -17,9 +17,10 @@
 // e4m3 terms of their scaled values as in the 8-bit attention, the scales of
 // key and query applied in the exponent.
 //
-// Warp roles: warp 16 loads, warp 17 issues the MMAs, warps 0-15 take the
-// logits (four warps per 32 keys, each the 16-column groups c, c + 4).  Four
-// logit buffers of 128 columns fill the tensor memory, so the MMAs run ahead.
+// Warp roles: warp 16 loads, warp 17 issues the MMAs, warps 0-15 are two
+// groups that take the tiles in turn (two warps per 32 keys), so that one
+// group's waits run beside the other's exponentials.  Four logit buffers of
+// 128 columns fill the tensor memory, so the MMAs run ahead.
 #pragma once
 
 #include "kv8_attn_kernel.cuh"
@@ -48,13 +49,15 @@ struct Smem {
     static constexpr int kBarSFull = kBarEmpty + kSlots;
     static constexpr int kBarSFree = kBarSFull + kBufs;
     static constexpr int kBarRow = kBarSFree + kBufs;
-    static constexpr int kBarFinal = kBarRow + 4;
+    static constexpr int kBarPair = kBarRow + 4;  // per group and lane quarter: its two warps
+    static constexpr int kBarFinal = kBarPair + 8;
     static constexpr int kNumBars = kBarFinal + 1;
     static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
-    // per query row {scale, -lse log2(e)}, then partial sums [2 parities][4][128]
+    // per query row {scale, -lse log2(e)}, then partial sums [2 parities][2 groups][128]
+    // (before: the rows' largest magnitudes, [4][128])
     static constexpr int kRowOff = (kTmemSlotOff + 16 + 15) / 16 * 16;
     static constexpr int kSumOff = kRowOff + 128 * 8;
-    static constexpr int kEnd = kSumOff + 8 * 128 * 4;
+    static constexpr int kEnd = kSumOff + 4 * 128 * 4;
     static constexpr int kAllocBytes = kEnd + 1024;
     static_assert(kAllocBytes <= 232448, "shared memory of a CTA");
 };
@@ -95,9 +98,10 @@ __global__ void __launch_bounds__(kThreadsM, 1)
         }
         for (int i = 0; i < kBufs; ++i) {
             ptx::mbar_init(&bars[L::kBarSFull + i], 1);
-            ptx::mbar_init(&bars[L::kBarSFree + i], kSoftWarps * 32);
+            ptx::mbar_init(&bars[L::kBarSFree + i], kSoftWarps / 2 * 32);
         }
         for (int i = 0; i < 4; ++i) ptx::mbar_init(&bars[L::kBarRow + i], 128);
+        for (int i = 0; i < 8; ++i) ptx::mbar_init(&bars[L::kBarPair + i], 64);
         ptx::mbar_init(&bars[L::kBarFinal], 1);
         ptx::fence_mbar_init();
     }
@@ -228,57 +232,79 @@ __global__ void __launch_bounds__(kThreadsM, 1)
             ptx::mbar_arrive(&bars[L::kBarQReady]);
             if (!failed) failed = !warp_wait(&bars[L::kBarQReady], 0);
         }
+        // The two groups of eight warps take the tiles in turn; a group's two
+        // warps of 32 keys take the 16-column groups hf, hf + 2, ...
+        const int hf = c4 & 1, grp = c4 >> 1;
         const int groups = p.N >> 4;
         const size_t unit_key0 = static_cast<size_t>(unit) * p.P;
-        for (int t = 0; t < T && !failed; ++t) {
+        uint64_t *pair_bar = &bars[L::kBarPair + grp * 4 + q4];
+        // what a tile needs of global memory, requested one of the group's tiles ahead
+        float before_next = 0.0f, ks_next = 1.0f;
+        uint32_t see_next = 0u;
+        auto load_next = [&](int t) {
+            const int j = (t0 + t) * kTile + row;
+            if (t >= T) return;
+            if (KV8 && j < vl) ks_next = __ldg(p.k_scale + static_cast<size_t>(unit) * p.nblk + (j >> p.shift));
+            if (hf == 0) {
+                see_next = j < vl ? 1u : 0u;
+                if (j < vl && p.mask != nullptr) see_next = __ldg(p.mask + static_cast<size_t>(b) * p.P + j);
+                if (j < p.P && p.mass_in != nullptr) before_next = p.mass_in[unit_key0 + j];
+            }
+        };
+        load_next(grp);
+        for (int t = grp; t < T && !failed; t += 2) {
             const int sb = t % kBufs;
             const int j = (t0 + t) * kTile + row;
-            // what the last step needs of global memory, requested before the wait
-            float before = 0.0f, ks = 1.0f;
-            bool see = j < vl;
-            if (KV8 && see) ks = __ldg(p.k_scale + static_cast<size_t>(unit) * p.nblk + (j >> p.shift));
-            if (c4 == 0 && j < p.P) {
-                if (p.mass_in != nullptr) before = p.mass_in[unit_key0 + j];
-                if (see && p.mask != nullptr) see = __ldg(p.mask + static_cast<size_t>(b) * p.P + j) != 0;
-            }
+            const float before = before_next, ks = ks_next;
+            const uint32_t see = see_next;
+            load_next(t + 2);
             if (!warp_wait(&bars[L::kBarSFull + sb], (t / kBufs) & 1)) {
                 failed = true;
                 break;
             }
             ptx::tc_fence_after_sync();
-            uint32_t raw[2][16];
             const uint32_t col = tmem + lane_base + sb * 128;
-            const bool one = c4 < groups, two = c4 + 4 < groups;
-            if (one) ptx::tmem_ld16(col + c4 * 16, raw[0]);
-            if (two) ptx::tmem_ld16(col + c4 * 16 + 64, raw[1]);
-            ptx::tmem_ld_wait();
-            ptx::tc_fence_before_sync();
-            ptx::mbar_arrive(&bars[L::kBarSFree + sb]);
+            const uint64_t ks2 = ptx::f32x2(ks, ks);
             uint64_t acc[2] = {ptx::f32x2(0.0f, 0.0f), ptx::f32x2(0.0f, 0.0f)};
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (g == 0 ? !one : !two) break;
-                const float4 *rc = reinterpret_cast<const float4 *>(rows + (c4 + 4 * g) * 16);
-                const uint64_t ks2 = ptx::f32x2(ks, ks);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t raw[2][16];
+                const int g0 = hf + 4 * h;
+                const bool one = g0 < groups, two = g0 + 2 < groups;
+                if (one) ptx::tmem_ld16(col + g0 * 16, raw[0]);
+                if (two) ptx::tmem_ld16(col + g0 * 16 + 32, raw[1]);
+                ptx::tmem_ld_wait();
+                if (h == 1) {
+                    ptx::tc_fence_before_sync();
+                    ptx::mbar_arrive(&bars[L::kBarSFree + sb]);
+                }
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 r = rc[e >> 1];  // {scale, -lse} of two query rows
-                    uint64_t f = ptx::f32x2(r.x, r.z);
-                    if (KV8) f = ptx::mul_f32x2(f, ks2);
-                    const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
-                        ptx::f32x2(__uint_as_float(raw[g][e]), __uint_as_float(raw[g][e + 1])), f, ptx::f32x2(r.y, r.w)));
-                    acc[(e >> 1) & 1] = ptx::add_f32x2(acc[(e >> 1) & 1], ptx::f32x2(ptx::ex2(x.x), ptx::ex2(x.y)));
+                for (int g = 0; g < 2; ++g) {
+                    if (g == 0 ? !one : !two) break;
+                    const float4 *rc = reinterpret_cast<const float4 *>(rows + (g0 + 2 * g) * 16);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 r = rc[e >> 1];  // {scale, -lse} of two query rows
+                        uint64_t f = ptx::f32x2(r.x, r.z);
+                        if (KV8) f = ptx::mul_f32x2(f, ks2);
+                        const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
+                            ptx::f32x2(__uint_as_float(raw[g][e]), __uint_as_float(raw[g][e + 1])), f, ptx::f32x2(r.y, r.w)));
+                        acc[(e >> 1) & 1] = ptx::add_f32x2(acc[(e >> 1) & 1], ptx::f32x2(ptx::ex2(x.x), ptx::ex2(x.y)));
+                    }
                 }
             }
             const float2 s2 = ptx::unpack_f32x2(ptx::add_f32x2(acc[0], acc[1]));
-            float *xs = sums + (t & 1) * 4 * 128 + row;
-            if (c4 != 0) xs[c4 * 128] = s2.x + s2.y;
-            if (!row_sync()) {
+            // the halves meet in the first one's warp; two tiles of a group apart,
+            // both are past the buffer's last use
+            const int turn = t >> 1;
+            float *xs = sums + ((turn & 1) * 2 + grp) * 128 + row;
+            if (hf == 1) *xs = s2.x + s2.y;
+            ptx::mbar_arrive(pair_bar);
+            if (!warp_wait(pair_bar, turn & 1)) {
                 failed = true;
                 break;
             }
-            if (c4 == 0 && j < p.P)
-                p.mass[unit_key0 + j] = see ? before + (((s2.x + s2.y) + xs[128]) + (xs[256] + xs[384])) : before;
+            if (hf == 0 && j < p.P) p.mass[unit_key0 + j] = see != 0u ? before + ((s2.x + s2.y) + *xs) : before;
         }
         // positions past the tiles in range keep what they had
         const int first = t_in * kTile;
