@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const int c = w * 32 + lane;
-                see_next[w] = t >= ns && t < T && c < rows_of(t) ? (mask_row != nullptr ? __ldg(mask_row + row0_of(t) + c) : 1u) : 0u;
+                see_next[w] = t >= ns && t < T && c < rows_of(t) ? (mask_row != nullptr ? ptx::load(mask_row + row0_of(t) + c) : 1u) : 0u;
             }
         };
         load_next(0);
@@ -615,13 +615,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     const int c = hf * 64 + w * 32 + lane;
-                    if (c < n) mask_next[w] = __ldg(mask_row + r0 + c);
+                    if (c < n) mask_next[w] = ptx::load(mask_row + r0 + c);
                 }
             }
             const int c = hf * 64 + lane * 16;
             if (lane < 4 && c < n) {
-                ks_next = __ldg(ksc + ((r0 + c) >> p.shift));
-                vs_next = __ldg(vsc + ((r0 + c) >> p.shift));
+                ks_next = ptx::load(ksc + ((r0 + c) >> p.shift));
+                vs_next = ptx::load(vsc + ((r0 + c) >> p.shift));
             }
         };
         load_next(grp);

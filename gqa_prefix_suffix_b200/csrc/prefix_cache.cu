@@ -251,8 +251,13 @@ int launch_select(const float *mass, const int32_t *valid_len, const uint8_t *ma
     sp.n_keep = n_keep;
     sp.n_first = n_first;
     sp.n_last = n_last;
-    return launch(dm05::cache::select_kernel, dim3(static_cast<unsigned>(B * Hkv)), dm05::cache::kSelectThreads, 0,
-                  stream, sp);
+    const dim3 grid(static_cast<unsigned>(B * Hkv));
+    constexpr int kT = dm05::cache::kSelectThreads;
+    if (P <= kT) return launch(dm05::cache::select_kernel<1>, grid, kT, 0, stream, sp);
+    if (P <= 2 * kT) return launch(dm05::cache::select_kernel<2>, grid, kT, 0, stream, sp);
+    if (P <= 4 * kT) return launch(dm05::cache::select_kernel<4>, grid, kT, 0, stream, sp);
+    if (P <= 8 * kT) return launch(dm05::cache::select_kernel<8>, grid, kT, 0, stream, sp);
+    return launch(dm05::cache::select_kernel<0>, grid, kT, 0, stream, sp);
 }
 
 }  // namespace
@@ -423,7 +428,6 @@ int dm05_prefix_evict(const void *k, const void *v, const float *mass, const int
     gp.k_out = static_cast<uint8_t *>(k_out);
     gp.v_out = static_cast<uint8_t *>(v_out);
     gp.pos = positions;
-    gp.valid = valid_out;
     gp.Hkv = Hkv;
     gp.P = P;
     gp.Pout = P_out;
@@ -461,14 +465,13 @@ int dm05_prefix_evict_kv8(const void *k8, const void *v8, const float *k_scale, 
     gp.k_scale_out = k_scale_out;
     gp.v_scale_out = v_scale_out;
     gp.pos = positions;
-    gp.valid = valid_out;
     gp.Hkv = Hkv;
     gp.P = P;
     gp.Pout = P_out;
     gp.nblk = blocks_of(P, shift);
     gp.nblk_out = blocks_of(P_out, shift);
     gp.shift = shift;
-    const dim3 grid(static_cast<unsigned>((n_keep + block - 1) >> shift), static_cast<unsigned>(B * Hkv), 2);
+    const dim3 grid(static_cast<unsigned>((n_keep + block - 1) >> shift), static_cast<unsigned>(B * Hkv));
     switch (block) {
     case 16: return launch(dm05::cache::gather_codes_kernel<16>, grid, 256, 0, stream, gp);
     case 32: return launch(dm05::cache::gather_codes_kernel<32>, grid, 256, 0, stream, gp);

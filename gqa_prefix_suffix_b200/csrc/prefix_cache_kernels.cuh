@@ -20,6 +20,18 @@
 #include "suffix_attn_kernel.cuh"
 
 namespace dm05 {
+
+namespace ptx {
+// A plain global load.  What the kernel launched right before may have written
+// is not read through the non-coherent path: with programmatic dependent
+// launch this kernel was already running then.
+template <class T>
+__device__ __forceinline__ T load(const T *p)
+{
+    return *p;
+}
+}  // namespace ptx
+
 namespace cache {
 
 constexpr int kRowBytes8 = kHeadDim;         // one 8-bit row
@@ -31,7 +43,7 @@ constexpr uint32_t kCodeNan = 0x7fu;
 __device__ __forceinline__ int clamped_len(const int32_t *valid_len, int b, int P, uint32_t *err, bool report)
 {
     if (valid_len == nullptr) return P;
-    const int raw = __ldg(valid_len + b);
+    const int raw = ptx::load(valid_len + b);
     const int vl = min(max(raw, 0), P);
     if (raw != vl && report) atomicOr(err, kEwClamped);
     return vl;
@@ -119,8 +131,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p)
         const int r = i * 16 + r0;
         if (r < rows) {
             const uint4 *a = reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * kHeadDim);
-            v[i][0] = __ldg(a);
-            v[i][1] = __ldg(a + 1);
+            v[i][0] = ptx::load(a);
+            v[i][1] = ptx::load(a + 1);
         }
     }
     // bf16 magnitudes order like their bit patterns; 0x7f80 and above are
@@ -191,8 +203,6 @@ struct SelectParams {
     int Hkv, P, Pout, n_keep, n_first, n_last;
 };
 
-constexpr int kSelectThreads = 512;
-
 // Sort key of a position: 0 hidden, 1 NaN, then the weights in ascending
 // order (-0 counts as +0), the largest for a protected position.
 __device__ __forceinline__ uint32_t select_key(const SelectParams &p, const float *mass, const uint8_t *mask, int vl,
@@ -206,94 +216,225 @@ __device__ __forceinline__ uint32_t select_key(const SelectParams &p, const floa
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Inclusive scan of one int per thread over the CTA; returns the exclusive
-// prefix and the total.  `slots` holds kSelectThreads / 32 words.
-__device__ __forceinline__ int block_scan(int v, int *slots, int *total)
+// Adds one to the bin of every participating lane's digit, one atomic per
+// distinct digit of the warp (weights of one head share their exponent, so
+// single adds would queue on a few bins).
+__device__ __forceinline__ void count_digit(int *hist, uint32_t digit, bool active)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = v;
+    const uint32_t who = __ballot_sync(0xffffffffu, active);
+    if (active) {
+        const uint32_t peers = __match_any_sync(who, digit);
+        if ((threadIdx.x & 31) == __ffs(static_cast<int>(peers)) - 1) atomicAdd(&hist[digit], __popc(peers));
+    }
+    __syncwarp();
+}
+
+// The digit whose bin, counted from the largest digit down, holds the
+// `want`-th key: {digit, the key's rank within the bin, the bin's count}.
+// One warp.
+__device__ __forceinline__ void pick_digit(const int *hist, int want, int *pick)
+{
+    const int lane = threadIdx.x & 31;
+    // eight runs of 32 bins, lane l holding the (l + 1)-th largest of each
+    int bin[8], chosen = 0, above = 0, run = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bin[e] = hist[255 - e * 32 - lane];
+    bool found = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int n = __reduce_add_sync(0xffffffffu, bin[e]);
+        if (!found && above + n >= want) {
+            found = true;
+            chosen = bin[e];
+            run = e;
+        }
+        if (!found) above += n;
+    }
+    int incl = chosen;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += t;
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
     }
-    __syncthreads();
-    if (lane == 31) slots[warp] = s;
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
-        const int t = slots[w];
-        if (w < warp) before += t;
-        all += t;
+    const int before = above + incl - chosen;
+    if (before < want && before + chosen >= want) {
+        pick[0] = 255 - run * 32 - lane;
+        pick[1] = want - before;
+        pick[2] = chosen;
     }
-    *total = all;
-    return before + s - v;
+}
+
+// Exclusive scan of table[0, n) by one warp; returns the total (that warp).
+__device__ __forceinline__ int warp_scan_table(int *table, int n)
+{
+    const int lane = threadIdx.x & 31;
+    int run = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int v = i0 + lane < n ? table[i0 + lane] : 0;
+        int s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += t;
+        }
+        if (i0 + lane < n) table[i0 + lane] = run + s - v;
+        run += __shfl_sync(0xffffffffu, s, 31);
+    }
+    return run;
 }
 
 // One CTA per (sample, KV head): the key of the n_keep-th wanted position by
-// a radix selection (four 8-bit digits, from the top), then one pass that
-// writes the kept positions in ascending order, the lowest ones first among
-// equals.
+// a radix selection (four 8-bit digits, from the top), then the kept
+// positions in ascending order, the lowest ones first among equals.
+//
+// KPT > 0: P <= KPT * 1024 and every thread keeps its keys in registers (the
+// weights are read once).  KPT == 0: any P; the keys are formed again in
+// every pass, and the positions are written 1024 at a time.
+// Latency bounds it: at P = 1024, 128 heads, XX us; at P = 2048, 4 heads, XX us.
+constexpr int kSelectThreads = 1024;
+
+template <int KPT>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p)
 {
-    __shared__ int hist[256];
-    __shared__ int slots[kSelectThreads / 32];
-    __shared__ int pick[2];
+    constexpr int kKeys = KPT > 0 ? KPT : 1;
+    __shared__ int hist[4][256];
+    __shared__ int table[kKeys * 32 + 1];
+    __shared__ int seen, pick[4][3];
     const int unit = blockIdx.x, b = unit / p.Hkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < 4 * 256; i += kSelectThreads) (&hist[0][0])[i] = 0;
+    if (threadIdx.x == 0) seen = 0;
     ptx::griddep_launch_dependents();
+    __syncthreads();
     ptx::griddep_wait();
     const int vl = clamped_len(p.valid_len, b, p.P, p.err, threadIdx.x == 0 && unit % p.Hkv == 0);
     const float *mass = p.mass + static_cast<size_t>(unit) * p.P;
     const uint8_t *mask = p.mask ? p.mask + static_cast<size_t>(b) * p.P : nullptr;
-    int seen = 0;
-    for (int j = threadIdx.x; j < vl; j += kSelectThreads) seen += mask == nullptr || mask[j] != 0;
-    int count = 0;
-    block_scan(seen, slots, &count);
-    const int keep = min(p.n_keep, count);
+    const int rounds = KPT > 0 ? KPT : (vl + kSelectThreads - 1) / kSelectThreads;
+    uint32_t keys[kKeys];
+    auto key_of = [&](int i) -> uint32_t {
+        const int j = i * kSelectThreads + threadIdx.x;
+        return j < vl ? select_key(p, mass, mask, vl, j) : 0u;
+    };
+    int visible = 0;
+    if (KPT > 0) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const int j = i * kSelectThreads + threadIdx.x;
+            keys[i] = j < vl ? select_key(p, mass, mask, vl, j) : 0u;
+            visible += keys[i] != 0u;
+            count_digit(hist[0], keys[i] >> 24, keys[i] != 0u);
+        }
+    } else {
+        for (int i = 0; i < rounds; ++i) {
+            const uint32_t k = key_of(i);
+            visible += k != 0u;
+            count_digit(hist[0], k >> 24, k != 0u);
+        }
+    }
+    visible = __reduce_add_sync(0xffffffffu, visible);
+    if (lane == 0 && visible != 0) atomicAdd(&seen, visible);
+    __syncthreads();
+    const int keep = min(p.n_keep, seen);
     if (threadIdx.x == 0 && unit % p.Hkv == 0) p.valid_out[b] = keep;
     int32_t *pos = p.pos + static_cast<size_t>(unit) * p.Pout;
     float *mass_out = p.mass_out + static_cast<size_t>(unit) * p.Pout;
-    uint32_t prefix = 0u, known = 0u;
-    int want = keep;  // how many of the keys that match the prefix are kept
     if (keep > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-            __syncthreads();
-            for (int j = threadIdx.x; j < vl; j += kSelectThreads) {
-                const uint32_t k = select_key(p, mass, mask, vl, j);
-                if (k != 0u && (k & known) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+        if (warp == 0) pick_digit(hist[0], keep, pick[0]);
+        __syncthreads();
+        uint32_t prefix = static_cast<uint32_t>(pick[0][0]) << 24, known = 0xff000000u;
+#pragma unroll
+        for (int pass = 1; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            if (KPT > 0) {
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i)
+                    count_digit(hist[pass], (keys[i] >> shift) & 255u, keys[i] != 0u && (keys[i] & known) == prefix);
+            } else {
+                for (int i = 0; i < rounds; ++i) {
+                    const uint32_t k = key_of(i);
+                    count_digit(hist[pass], (k >> shift) & 255u, k != 0u && (k & known) == prefix);
+                }
             }
             __syncthreads();
-            // thread t holds digit 255 - t: the number of larger digits' keys
-            const int mine = threadIdx.x < 256 ? hist[255 - threadIdx.x] : 0;
-            int total = 0;
-            const int above = block_scan(mine, slots, &total);
-            if (threadIdx.x < 256 && above < want && above + mine >= want) {
-                pick[0] = 255 - static_cast<int>(threadIdx.x);
-                pick[1] = want - above;
-            }
+            if (warp == 0) pick_digit(hist[pass], pick[pass - 1][1], pick[pass]);
             __syncthreads();
-            prefix |= static_cast<uint32_t>(pick[0]) << shift;
+            prefix |= static_cast<uint32_t>(pick[pass][0]) << shift;
             known |= 255u << shift;
-            want = pick[1];
         }
-    }
-    // prefix is the key of the last kept position, want how many of its equals are kept
-    int base = 0, ties = 0;
-    for (int j0 = 0; keep > 0 && j0 < vl; j0 += kSelectThreads) {
-        const int j = j0 + threadIdx.x;
-        const uint32_t k = j < vl ? select_key(p, mass, mask, vl, j) : 0u;
-        const bool tie = k != 0u && k == prefix;
-        int n_tie = 0, n_kept = 0;
-        const int tie_at = ties + block_scan(tie ? 1 : 0, slots, &n_tie);
-        const bool kept = k > prefix || (tie && tie_at < want);
-        const int at = base + block_scan(kept ? 1 : 0, slots, &n_kept);
-        if (kept) {
-            pos[at] = j;
-            mass_out[at] = mass[j];
+        // prefix: the key of the last kept position; `want` of its equals are kept
+        const int want = pick[3][1];
+        const bool all_equal = want == pick[3][2];
+        if (KPT > 0) {
+            uint32_t kept[kKeys];
+            if (!all_equal) {
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i) {
+                    const uint32_t t = __ballot_sync(0xffffffffu, keys[i] == prefix);
+                    if (lane == 0) table[i * 32 + warp] = __popc(t);
+                }
+                __syncthreads();
+                if (warp == 0) warp_scan_table(table, kKeys * 32);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+                bool tie = keys[i] == prefix;
+                if (!all_equal) {
+                    const uint32_t t = __ballot_sync(0xffffffffu, tie);
+                    tie = tie && table[i * 32 + warp] + __popc(t & ((1u << lane) - 1u)) < want;
+                }
+                kept[i] = __ballot_sync(0xffffffffu, keys[i] > prefix || tie);
+            }
+            if (!all_equal) __syncthreads();  // the tie table has been read
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+                if (lane == 0) table[i * 32 + warp] = __popc(kept[i]);
+            __syncthreads();
+            if (warp == 0) warp_scan_table(table, kKeys * 32);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+                if (kept[i] >> lane & 1u) {
+                    const int at = table[i * 32 + warp] + __popc(kept[i] & ((1u << lane) - 1u));
+                    const int j = i * kSelectThreads + threadIdx.x;
+                    pos[at] = j;
+                    mass_out[at] = mass[j];
+                }
+            }
+        } else {
+            int base = 0, ties = 0;
+            for (int i = 0; i < rounds; ++i) {
+                const uint32_t k = key_of(i);
+                const uint32_t t = __ballot_sync(0xffffffffu, k == prefix);
+                __syncthreads();  // the table's last use
+                if (lane == 0) table[warp] = __popc(t);
+                __syncthreads();
+                if (warp == 0) {
+                    const int n = warp_scan_table(table, 32);
+                    if (lane == 0) table[32] = n;
+                }
+                __syncthreads();
+                const bool tie = k == prefix && ties + table[warp] + __popc(t & ((1u << lane) - 1u)) < want;
+                ties += table[32];
+                const uint32_t m = __ballot_sync(0xffffffffu, k > prefix || tie);
+                __syncthreads();
+                if (lane == 0) table[warp] = __popc(m);
+                __syncthreads();
+                if (warp == 0) {
+                    const int n = warp_scan_table(table, 32);
+                    if (lane == 0) table[32] = n;
+                }
+                __syncthreads();
+                if (m >> lane & 1u) {
+                    const int at = base + table[warp] + __popc(m & ((1u << lane) - 1u));
+                    const int j = i * kSelectThreads + threadIdx.x;
+                    pos[at] = j;
+                    mass_out[at] = mass[j];
+                }
+                base += table[32];
+            }
         }
-        ties += n_tie;
-        base += n_kept;
     }
     for (int i = keep + threadIdx.x; i < p.Pout; i += kSelectThreads) {
         pos[i] = -1;
@@ -306,8 +447,7 @@ struct GatherParams {
     uint8_t *k_out, *v_out;             // [units, Pout] rows
     const float *k_scale, *v_scale;     // 8-bit: [units, nblk]
     float *k_scale_out, *v_scale_out;   // 8-bit: [units, nblk_out]
-    const int32_t *pos;      // [units, Pout]
-    const int32_t *valid;    // [B]: kept rows
+    const int32_t *pos;      // [units, Pout], -1 behind the kept rows
     int Hkv, P, Pout, nblk, nblk_out, shift;  // shift: log2 of the block
 };
 
@@ -315,26 +455,26 @@ struct GatherParams {
 __global__ void __launch_bounds__(256) gather_rows_kernel(const GatherParams p)
 {
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
     const int unit = blockIdx.y;
     const int lane = threadIdx.x & 31;
-    const int n = __ldg(p.valid + unit / p.Hkv);
     const int i0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4;
-    if (i0 >= n) return;
-    const int32_t *pos = p.pos + static_cast<size_t>(unit) * p.Pout;
     const size_t in0 = static_cast<size_t>(unit) * p.P, out0 = static_cast<size_t>(unit) * p.Pout;
+    ptx::griddep_wait();
+    int j[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) j[r] = i0 + r < p.Pout ? ptx::load(p.pos + out0 + i0 + r) : -1;
     uint4 v[4][2];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        if (i0 + r < n) {
-            const size_t off = (in0 + static_cast<size_t>(__ldg(pos + i0 + r))) * 512 + lane * 16;
-            v[r][0] = *reinterpret_cast<const uint4 *>(p.k + off);
-            v[r][1] = *reinterpret_cast<const uint4 *>(p.v + off);
+        if (j[r] >= 0) {
+            const size_t off = (in0 + static_cast<size_t>(j[r])) * 512 + lane * 16;
+            v[r][0] = ptx::load(reinterpret_cast<const uint4 *>(p.k + off));
+            v[r][1] = ptx::load(reinterpret_cast<const uint4 *>(p.v + off));
         }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        if (i0 + r < n) {
+        if (j[r] >= 0) {
             const size_t off = (out0 + i0 + r) * 512 + lane * 16;
             *reinterpret_cast<uint4 *>(p.k_out + off) = v[r][0];
             *reinterpret_cast<uint4 *>(p.v_out + off) = v[r][1];
@@ -342,68 +482,85 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const GatherParams p)
     }
 }
 
-// 8-bit rows: one CTA per (block of new rows, unit, K or V).  The kept rows
-// come from blocks with scales of their own; their largest value sets the
-// new block's scale by the quantiser's rule and every code is rounded to it.
+// 8-bit rows: one CTA per (block of new rows, unit), K and V together.  The
+// kept rows come from blocks with scales of their own; their largest value
+// sets the new block's scale by the quantiser's rule and every code is
+// rounded to it.
 template <int BLOCK>
 __global__ void __launch_bounds__(256) gather_codes_kernel(const GatherParams p)
 {
-    __shared__ uint32_t slots[8];
+    __shared__ uint32_t slots[2][8];
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int unit = blockIdx.y, which = blockIdx.z, nb = blockIdx.x;
-    const int n = __ldg(p.valid + unit / p.Hkv);
-    const int rows = min(BLOCK, n - nb * BLOCK);
-    if (rows <= 0) return;
+    const int unit = blockIdx.y, nb = blockIdx.x;
     constexpr int kPasses = BLOCK / 16;
     const int r0 = threadIdx.x >> 4, col = (threadIdx.x & 15) * 16;
-    const int32_t *pos = p.pos + static_cast<size_t>(unit) * p.Pout + nb * BLOCK;
-    const float *scale = (which ? p.v_scale : p.k_scale) + static_cast<size_t>(unit) * p.nblk;
-    uint4 v[kPasses];
-    float s[kPasses];
+    const size_t out0 = static_cast<size_t>(unit) * p.Pout + static_cast<size_t>(nb) * BLOCK;
+    ptx::griddep_wait();
+    int j[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+        j[i] = nb * BLOCK + i * 16 + r0 < p.Pout ? ptx::load(p.pos + out0 + i * 16 + r0) : -1;
+    uint4 v[2][kPasses];
+    float s[2][kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const int r = i * 16 + r0;
-        v[i] = make_uint4(0u, 0u, 0u, 0u);
-        s[i] = 0.0f;
-        if (r < rows) {
-            const int j = __ldg(pos + r);
-            v[i] = *reinterpret_cast<const uint4 *>(
-                (which ? p.v : p.k) + (static_cast<size_t>(unit) * p.P + j) * kRowBytes8 + col);
-            s[i] = __ldg(scale + (j >> p.shift));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            v[w][i] = make_uint4(0u, 0u, 0u, 0u);
+            s[w][i] = 0.0f;
+            if (j[i] >= 0) {
+                v[w][i] = ptx::load(reinterpret_cast<const uint4 *>(
+                    (w ? p.v : p.k) + (static_cast<size_t>(unit) * p.P + j[i]) * kRowBytes8 + col));
+                s[w][i] = ptx::load((w ? p.v_scale : p.k_scale) + static_cast<size_t>(unit) * p.nblk + (j[i] >> p.shift));
+            }
         }
     }
     // magnitudes of e4m3 codes order like their bits (NaN codes set no scale)
-    float amax = 0.0f;
+    float amax[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t top = 0u;
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t a = w[e] & 0x7f7f7f7fu;
-            top = __vmaxu4(top, a & ~__vcmpeq4(a, 0x7f7f7f7fu));
+        for (int i = 0; i < kPasses; ++i) {
+            const uint32_t c[4] = {v[w][i].x, v[w][i].y, v[w][i].z, v[w][i].w};
+            uint32_t top = 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a = c[e] & 0x7f7f7f7fu;
+                top = __vmaxu4(top, a & ~__vcmpeq4(a, 0x7f7f7f7fu));
+            }
+            top = __vmaxu4(top, top >> 16);
+            top = __vmaxu4(top, top >> 8) & 0xffu;
+            amax[w] = fmaxf(amax[w], decode4(top).x * s[w][i]);
         }
-        top = __vmaxu4(top, top >> 16);
-        top = __vmaxu4(top, top >> 8) & 0xffu;
-        amax = fmaxf(amax, decode4(top).x * s[i]);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax[w]));
+        if ((threadIdx.x & 31) == 0) slots[w][threadIdx.x >> 5] = m;
     }
-    amax = __uint_as_float(block_max_u32(__float_as_uint(amax), slots));
-    const float t = pow2_scale(amax), inv = pow2_inverse(t);
-    if (threadIdx.x == 0) (which ? p.v_scale_out : p.k_scale_out)[static_cast<size_t>(unit) * p.nblk_out + nb] = t;
-    uint8_t *dst = (which ? p.v_out : p.k_out) + (static_cast<size_t>(unit) * p.Pout + nb * BLOCK) * kRowBytes8 + col;
+    __syncthreads();
+    const bool any = nb * BLOCK < p.Pout && ptx::load(p.pos + out0) >= 0;  // the block has a kept row
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const int r = i * 16 + r0;
-        if (r >= rows) break;
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[4];
+    for (int w = 0; w < 2; ++w) {
+        uint32_t m = slots[w][0];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 x = decode4(w[e]);
-            o[e] = encode4(x.x * s[i] * inv, x.y * s[i] * inv, x.z * s[i] * inv, x.w * s[i] * inv);
+        for (int i = 1; i < 8; ++i) m = max(m, slots[w][i]);
+        const float t = pow2_scale(__uint_as_float(m)), inv = pow2_inverse(t);
+        if (threadIdx.x == 0 && any)
+            (w ? p.v_scale_out : p.k_scale_out)[static_cast<size_t>(unit) * p.nblk_out + nb] = t;
+        uint8_t *dst = (w ? p.v_out : p.k_out) + out0 * kRowBytes8 + col;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            if (j[i] < 0) continue;
+            const uint32_t c[4] = {v[w][i].x, v[w][i].y, v[w][i].z, v[w][i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 x = decode4(c[e]);
+                o[e] = encode4(x.x * s[w][i] * inv, x.y * s[w][i] * inv, x.z * s[w][i] * inv, x.w * s[w][i] * inv);
+            }
+            *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(i * 16 + r0) * kRowBytes8) =
+                make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(r) * kRowBytes8) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 

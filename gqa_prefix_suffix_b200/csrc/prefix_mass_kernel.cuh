@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
             if (c4 == 0) {
                 // rows that do not exist, and rows that saw no key (-inf), add 2^-inf
                 float l = INFINITY;
-                if (row < p.GS) l = __ldg(p.lse + static_cast<size_t>(unit) * p.GS + row);
+                if (row < p.GS) l = ptx::load(p.lse + static_cast<size_t>(unit) * p.GS + row);
                 if (l == -INFINITY) l = INFINITY;
                 rows[row] = make_float2(scale, -l * 1.4426950408889634f);
             }
@@ -244,10 +244,10 @@ __global__ void __launch_bounds__(kThreadsM, 1)
         auto load_next = [&](int t) {
             const int j = (t0 + t) * kTile + row;
             if (t >= T) return;
-            if (KV8 && j < vl) ks_next = __ldg(p.k_scale + static_cast<size_t>(unit) * p.nblk + (j >> p.shift));
+            if (KV8 && j < vl) ks_next = ptx::load(p.k_scale + static_cast<size_t>(unit) * p.nblk + (j >> p.shift));
             if (hf == 0) {
                 see_next = j < vl ? 1u : 0u;
-                if (j < vl && p.mask != nullptr) see_next = __ldg(p.mask + static_cast<size_t>(b) * p.P + j);
+                if (j < vl && p.mask != nullptr) see_next = ptx::load(p.mask + static_cast<size_t>(b) * p.P + j);
                 if (j < p.P && p.mass_in != nullptr) before_next = p.mass_in[unit_key0 + j];
             }
         };

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     int vl = p.P;
     if (p.valid_len != nullptr) {
-        const int raw = __ldg(p.valid_len + b);
+        const int raw = p.valid_len[b];  // a plain load: the kernel before may have written it
         vl = min(max(raw, 0), p.P);
         if (raw != vl && rank == 0 && threadIdx.x == 0) atomicOr(p.err, kEwClamped);
     }
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int w = 0; w < NH / 32; ++w) {
                 const int c = hf * NH + w * 32 + lane;
-                if (c < tn.n_valid) m[w] = __ldg(mask_row + tn.row0 + c);
+                if (c < tn.n_valid) m[w] = mask_row[tn.row0 + c];
             }
         };
         load_mask(0, mask_next);
