@@ -473,10 +473,10 @@ int dm05_prefix_evict_kv8(const void *k8, const void *v8, const float *k_scale, 
     gp.shift = shift;
     const dim3 grid(static_cast<unsigned>((n_keep + block - 1) >> shift), static_cast<unsigned>(B * Hkv));
     switch (block) {
-    case 16: return launch(dm05::cache::gather_codes_kernel<16>, grid, 256, 0, stream, gp);
-    case 32: return launch(dm05::cache::gather_codes_kernel<32>, grid, 256, 0, stream, gp);
-    case 64: return launch(dm05::cache::gather_codes_kernel<64>, grid, 256, 0, stream, gp);
-    default: return launch(dm05::cache::gather_codes_kernel<128>, grid, 256, 0, stream, gp);
+    case 16: return launch(dm05::cache::gather_codes_kernel<16>, grid, 512, 0, stream, gp);
+    case 32: return launch(dm05::cache::gather_codes_kernel<32>, grid, 512, 0, stream, gp);
+    case 64: return launch(dm05::cache::gather_codes_kernel<64>, grid, 512, 0, stream, gp);
+    default: return launch(dm05::cache::gather_codes_kernel<128>, grid, 512, 0, stream, gp);
     }
 }
 

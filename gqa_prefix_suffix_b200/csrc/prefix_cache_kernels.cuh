@@ -75,6 +75,16 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
     return lo | (hi << 16);
 }
 
+// Two codes and their values in fp16 (which holds every e4m3 value).
+__device__ __forceinline__ __half2 decode2(uint32_t codes)
+{
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3));
+}
+__device__ __forceinline__ uint32_t encode2(__half2 x)
+{
+    return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+}
+
 // the four values of four codes
 __device__ __forceinline__ float4 decode4(uint32_t w)
 {
@@ -203,14 +213,13 @@ struct SelectParams {
     int Hkv, P, Pout, n_keep, n_first, n_last;
 };
 
-// Sort key of a position: 0 hidden, 1 NaN, then the weights in ascending
-// order (-0 counts as +0), the largest for a protected position.
-__device__ __forceinline__ uint32_t select_key(const SelectParams &p, const float *mass, const uint8_t *mask, int vl,
-                                               int j)
+// Sort key of position j with this weight: 0 hidden, 1 NaN, then the weights
+// in ascending order (-0 counts as +0), the largest for a protected position.
+__device__ __forceinline__ uint32_t select_key(const SelectParams &p, int vl, int j, float weight, bool shown)
 {
-    if (j >= vl || (mask != nullptr && mask[j] == 0)) return 0u;
+    if (j >= vl || !shown) return 0u;
     if (j < p.n_first || j >= vl - p.n_last) return 0xffffffffu;
-    const float m = mass[j] + 0.0f;
+    const float m = weight + 0.0f;
     if (m != m) return 1u;
     const uint32_t u = __float_as_uint(m);
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
@@ -307,21 +316,32 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     ptx::griddep_launch_dependents();
     __syncthreads();
     ptx::griddep_wait();
-    const int vl = clamped_len(p.valid_len, b, p.P, p.err, threadIdx.x == 0 && unit % p.Hkv == 0);
     const float *mass = p.mass + static_cast<size_t>(unit) * p.P;
     const uint8_t *mask = p.mask ? p.mask + static_cast<size_t>(b) * p.P : nullptr;
+    float weight[kKeys];
+    bool shown[kKeys];
+    if (KPT > 0) {
+        // requested before the valid length is known
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const int j = i * kSelectThreads + threadIdx.x;
+            weight[i] = j < p.P ? mass[j] : 0.0f;
+            shown[i] = j < p.P && (mask == nullptr || mask[j] != 0);
+        }
+    }
+    const int vl = clamped_len(p.valid_len, b, p.P, p.err, threadIdx.x == 0 && unit % p.Hkv == 0);
     const int rounds = KPT > 0 ? KPT : (vl + kSelectThreads - 1) / kSelectThreads;
     uint32_t keys[kKeys];
     auto key_of = [&](int i) -> uint32_t {
         const int j = i * kSelectThreads + threadIdx.x;
-        return j < vl ? select_key(p, mass, mask, vl, j) : 0u;
+        return j < vl ? select_key(p, vl, j, mass[j], mask == nullptr || mask[j] != 0) : 0u;
     };
     int visible = 0;
     if (KPT > 0) {
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
             const int j = i * kSelectThreads + threadIdx.x;
-            keys[i] = j < vl ? select_key(p, mass, mask, vl, j) : 0u;
+            keys[i] = select_key(p, vl, j, weight[i], shown[i]);
             visible += keys[i] != 0u;
             count_digit(hist[0], keys[i] >> 24, keys[i] != 0u);
         }
@@ -399,7 +419,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
                     const int at = table[i * 32 + warp] + __popc(kept[i] & ((1u << lane) - 1u));
                     const int j = i * kSelectThreads + threadIdx.x;
                     pos[at] = j;
-                    mass_out[at] = mass[j];
+                    mass_out[at] = weight[i];
                 }
             }
         } else {
@@ -482,85 +502,82 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const GatherParams p)
     }
 }
 
-// 8-bit rows: one CTA per (block of new rows, unit), K and V together.  The
-// kept rows come from blocks with scales of their own; their largest value
-// sets the new block's scale by the quantiser's rule and every code is
-// rounded to it.
+// 8-bit rows: one CTA per (block of new rows, unit), half its threads on K,
+// half on V.  The kept rows come from blocks with scales of their own; their
+// largest value sets the new block's scale by the quantiser's rule and every
+// code is rounded to it.
 template <int BLOCK>
-__global__ void __launch_bounds__(256) gather_codes_kernel(const GatherParams p)
+__global__ void __launch_bounds__(512) gather_codes_kernel(const GatherParams p)
 {
-    __shared__ uint32_t slots[2][8];
+    __shared__ uint32_t slots[16];
     ptx::griddep_launch_dependents();
     const int unit = blockIdx.y, nb = blockIdx.x;
-    constexpr int kPasses = BLOCK / 16;
-    const int r0 = threadIdx.x >> 4, col = (threadIdx.x & 15) * 16;
+    const bool is_v = threadIdx.x >= 256;
+    const int tid = threadIdx.x & 255;
+    constexpr int kPasses = BLOCK / 16;  // 16 rows a pass, 16 codes a thread
+    const int r0 = tid >> 4, col = (tid & 15) * 16;
     const size_t out0 = static_cast<size_t>(unit) * p.Pout + static_cast<size_t>(nb) * BLOCK;
+    const uint8_t *src = (is_v ? p.v : p.k) + static_cast<size_t>(unit) * p.P * kRowBytes8 + col;
+    const float *scale = (is_v ? p.v_scale : p.k_scale) + static_cast<size_t>(unit) * p.nblk;
     ptx::griddep_wait();
     int j[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
         j[i] = nb * BLOCK + i * 16 + r0 < p.Pout ? ptx::load(p.pos + out0 + i * 16 + r0) : -1;
-    uint4 v[2][kPasses];
-    float s[2][kPasses];
+    uint4 v[kPasses];
+    float s[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            v[w][i] = make_uint4(0u, 0u, 0u, 0u);
-            s[w][i] = 0.0f;
-            if (j[i] >= 0) {
-                v[w][i] = ptx::load(reinterpret_cast<const uint4 *>(
-                    (w ? p.v : p.k) + (static_cast<size_t>(unit) * p.P + j[i]) * kRowBytes8 + col));
-                s[w][i] = ptx::load((w ? p.v_scale : p.k_scale) + static_cast<size_t>(unit) * p.nblk + (j[i] >> p.shift));
-            }
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        s[i] = 0.0f;
+        if (j[i] >= 0) {
+            v[i] = ptx::load(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(j[i]) * kRowBytes8));
+            s[i] = ptx::load(scale + (j[i] >> p.shift));
         }
     }
-    // magnitudes of e4m3 codes order like their bits (NaN codes set no scale)
-    float amax[2] = {0.0f, 0.0f};
+    // largest magnitude of a thread's codes in fp16 (exact; NaN codes set no scale)
+    float amax = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int i = 0; i < kPasses; ++i) {
+        const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        __half2 top = __float2half2_rn(0.0f);
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const uint32_t c[4] = {v[w][i].x, v[w][i].y, v[w][i].z, v[w][i].w};
-            uint32_t top = 0u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t a = c[e] & 0x7f7f7f7fu;
-                top = __vmaxu4(top, a & ~__vcmpeq4(a, 0x7f7f7f7fu));
-            }
-            top = __vmaxu4(top, top >> 16);
-            top = __vmaxu4(top, top >> 8) & 0xffu;
-            amax[w] = fmaxf(amax[w], decode4(top).x * s[w][i]);
-        }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax[w]));
-        if ((threadIdx.x & 31) == 0) slots[w][threadIdx.x >> 5] = m;
+        for (int e = 0; e < 4; ++e)
+            top = __hmax2(__hmax2(top, __habs2(decode2(c[e] & 0xffffu))), __habs2(decode2(c[e] >> 16)));
+        amax = fmaxf(amax, fmaxf(__low2float(top), __high2float(top)) * s[i]);
     }
+    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+    if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = m;
     __syncthreads();
-    const bool any = nb * BLOCK < p.Pout && ptx::load(p.pos + out0) >= 0;  // the block has a kept row
+    m = 0u;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        uint32_t m = slots[w][0];
+    for (int i = 0; i < 8; ++i) m = max(m, slots[(is_v ? 8 : 0) + i]);
+    const float t = pow2_scale(__uint_as_float(m)), inv = pow2_inverse(t);
+    if (tid == 0 && j[0] >= 0)  // the block has a kept row
+        (is_v ? p.v_scale_out : p.k_scale_out)[static_cast<size_t>(unit) * p.nblk_out + nb] = t;
+    uint8_t *dst = (is_v ? p.v_out : p.k_out) + out0 * kRowBytes8 + col;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) m = max(m, slots[w][i]);
-        const float t = pow2_scale(__uint_as_float(m)), inv = pow2_inverse(t);
-        if (threadIdx.x == 0 && any)
-            (w ? p.v_scale_out : p.k_scale_out)[static_cast<size_t>(unit) * p.nblk_out + nb] = t;
-        uint8_t *dst = (w ? p.v_out : p.k_out) + out0 * kRowBytes8 + col;
+    for (int i = 0; i < kPasses; ++i) {
+        if (j[i] < 0) continue;
+        const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t o[4];
+        // With powers of two the quotient of the scales multiplies exactly, in
+        // fp16 too: what it pushes below fp16's range rounds to the code 0.
+        const float ratio = s[i] * inv;
+        if ((__float_as_uint(ratio) & 0x7fffffu) == 0u && ratio >= 0x1p-24f && ratio <= 0x1p15f) {
+            const __half2 f = __float2half2_rn(ratio);
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            if (j[i] < 0) continue;
-            const uint32_t c[4] = {v[w][i].x, v[w][i].y, v[w][i].z, v[w][i].w};
-            uint32_t o[4];
+            for (int e = 0; e < 4; ++e)
+                o[e] = encode2(__hmul2(decode2(c[e] & 0xffffu), f)) | encode2(__hmul2(decode2(c[e] >> 16), f)) << 16;
+        } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float4 x = decode4(c[e]);
-                o[e] = encode4(x.x * s[w][i] * inv, x.y * s[w][i] * inv, x.z * s[w][i] * inv, x.w * s[w][i] * inv);
+                o[e] = encode4(x.x * s[i] * inv, x.y * s[i] * inv, x.z * s[i] * inv, x.w * s[i] * inv);
             }
-            *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(i * 16 + r0) * kRowBytes8) =
-                make_uint4(o[0], o[1], o[2], o[3]);
         }
+        *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(i * 16 + r0) * kRowBytes8) =
+            make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
