@@ -2,18 +2,23 @@
 
 Argument marshalling only: every step of the attention runs in the CUDA
 library.  If the library is missing the import of the entry points fails
-loudly; there is no other implementation behind these names.
+loudly; there is no other implementation behind these names.  The torch forms
+of the prefix-cache operators marshal in a compiled module (torch_front.cpp),
+since their smallest calls are shorter than checks in Python.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import NamedTuple, Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdm05_suffix_attn.so")
+FRONT_PATH = os.path.join(_HERE, "_torch_front.so")
 
 DM05_OK = 0
 DM05_ERR_NULL = -1
@@ -311,7 +316,6 @@ def dm05_suffix_attn_plan(B, Hq, Hkv, P, S, D):
 
 
 def dm05_set_split_override(splits_per_head: int) -> int:
-    _kv8_workspace_bytes.clear()
     return lib().dm05_set_split_override(splits_per_head)
 
 
@@ -547,84 +551,43 @@ class EvictedPrefixKv8(NamedTuple):
     valid_len: "torch.Tensor"
 
 
-def _need(name, t, dtype, shape, index):
-    """A dense tensor of this type and shape on CUDA device `index`, or ValueError."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != index or index < 0 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {list(shape)}"
-                         + (f" on cuda:{index}" if index >= 0 else ""))
+_front = None
 
 
-def _need_prefix(valid_len, mask, B, P, index):
+def _load_front():
+    """The compiled torch front end (csrc/torch_front.cpp), bound to the
+    loaded library; raises if it has not been built."""
+    global _front
+    L = lib()
+    import torch  # noqa: F401  (the module's symbols come from it)
+    with _lock:
+        if _front is None:
+            if not os.path.exists(FRONT_PATH):
+                raise RuntimeError(f"{FRONT_PATH} is missing: build it with `python -m gqa_prefix_suffix_b200.build`")
+            loader = importlib.machinery.ExtensionFileLoader("_torch_front", FRONT_PATH)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_torch_front", loader))
+            loader.exec_module(m)
+            m.bind(Dm05Error, *[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+                "dm05_kv8_quantize", "dm05_suffix_attn_kv8", "dm05_suffix_attn_kv8_plan", "dm05_prefix_attn_mass",
+                "dm05_prefix_attn_mass_kv8", "dm05_prefix_evict", "dm05_prefix_evict_kv8")])
+            _front = m
+    return _front
+
+
+@contextlib.contextmanager
+def _stream_of(t, stream):
+    """`stream` current on the device of t, for what is allocated as for what is launched."""
     import torch
-    if valid_len is not None:
-        _need("prefix_valid_len", valid_len, torch.int32, (B,), index)
-    if mask is not None:
-        _need("prefix_mask", mask, torch.uint8, (B, P), index)
-
-
-def _need_cache(name, cache, index):
-    """Checks an 8-bit cache; returns its (B, Hkv, P, D)."""
-    import torch
-    k, v, ks, vs, block = cache
-    if k.dim() != 4:
-        raise ValueError(f"{name}.k must be [B,Hkv,P,D]")
-    shape = k.shape
-    B, Hkv, P, D = shape
-    if block not in (16, 32, 64, 128):
-        raise ValueError(f"{name}.block must be 16, 32, 64 or 128")
-    scales = (B, Hkv, -(-P // block))
-    _need(f"{name}.k", k, torch.float8_e4m3fn, shape, index)
-    _need(f"{name}.v", v, torch.float8_e4m3fn, shape, index)
-    _need(f"{name}.k_scale", ks, torch.float32, scales, index)
-    _need(f"{name}.v_scale", vs, torch.float32, scales, index)
-    return B, Hkv, P, D
-
-
-def _current_stream_handle(index):
-    """Handle of the current stream of CUDA device `index`."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object (3 us)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
-
-
-def _on(index, stream, call):
-    """call(stream handle) with the tensors' device current and `stream` the
-    stream that newly allocated tensors belong to."""
-    import torch
-    if stream is None and torch.cuda.current_device() == index:
-        return call(_current_stream_handle(index))
-    with torch.cuda.device(index):
-        if stream is None:
-            return call(_current_stream_handle(index))
-        if not hasattr(stream, "cuda_stream"):
-            h = int(stream)
-            stream = torch.cuda.ExternalStream(h, device=index) if h else torch.cuda.default_stream(index)
-        if stream.device.index != index:
-            raise ValueError(f"stream must be on cuda:{index} like the tensors")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _check(rc, what):
-    if rc != DM05_OK:
-        raise Dm05Error(rc, what)
-
-
-def _codes(shape, index):
-    import torch
-    return torch.zeros(shape, dtype=torch.uint8, device=index).view(torch.float8_e4m3fn)
-
-
-def _empty_cache(B, Hkv, P, D, block, index):
-    """Zero codes and unit scales."""
-    import torch
-    shape, scales = (B, Hkv, P, D), (B, Hkv, -(-P // block))
-    ones = [torch.ones(scales, dtype=torch.float32, device=index) for _ in range(2)]
-    return Kv8Cache(_codes(shape, index), _codes(shape, index), ones[0], ones[1], block)
+    if not t.is_cuda:
+        yield  # refused by the call
+        return
+    if not hasattr(stream, "cuda_stream"):
+        h = int(stream)
+        stream = torch.cuda.ExternalStream(h, device=t.device) if h else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream must be on {t.device} like the tensors")
+    with torch.cuda.stream(stream):
+        yield
 
 
 def kv8_quantize(k, v, block: int = 64, valid_len=None, first: int = 0, out: Optional[Kv8Cache] = None, stream=None):
@@ -634,43 +597,13 @@ def kv8_quantize(k, v, block: int = 64, valid_len=None, first: int = 0, out: Opt
     prefix that is quantised in pieces); a fresh cache has zero codes and unit
     scales elsewhere.  With `out` given, its block is used and everything else
     in it is left as it was."""
-    import torch
-    if k.dim() != 4:
-        raise ValueError("k must be [B,Hkv,P,D]")
-    shape = k.shape
-    B, Hkv, P, D = shape
-    dev = k.get_device()
-    _need("k", k, torch.bfloat16, shape, dev)
-    _need("v", v, torch.bfloat16, shape, dev)
-    if valid_len is not None:
-        _need("valid_len", valid_len, torch.int32, (B,), dev)
-    if out is None:
-        if block not in (16, 32, 64, 128):
-            raise ValueError("block must be 16, 32, 64 or 128")
-    elif _need_cache("out", out, dev) != (B, Hkv, P, D):
-        raise ValueError("out must be a cache of k's sizes")
-
-    def call(s):
-        c = _empty_cache(B, Hkv, P, D, block, dev) if out is None else out
-        _check(dm05_kv8_quantize(k.data_ptr(), v.data_ptr(), _ptr(valid_len), c.k.data_ptr(), c.v.data_ptr(),
-                                 c.k_scale.data_ptr(), c.v_scale.data_ptr(), B, Hkv, P, D, c.block, first, s),
-               "dm05_kv8_quantize")
-        return c
-    return _on(dev, stream, call)
-
-
-_kv8_workspace_bytes: dict = {}  # sizes and device -> bytes; a split override changes plans and clears it
-
-
-def _kv8_workspace(key):
-    need = _kv8_workspace_bytes.get(key)
-    if need is None:
-        rc, _, _, need = dm05_suffix_attn_kv8_plan(*key[:6])
-        _check(rc, "dm05_suffix_attn_kv8")
-        if len(_kv8_workspace_bytes) > 4096:
-            _kv8_workspace_bytes.clear()
-        _kv8_workspace_bytes[key] = need
-    return need
+    call = (_front or _load_front()).kv8_quantize
+    if stream is None:
+        r = call(k, v, block, valid_len, first, out)
+    else:
+        with _stream_of(k, stream):
+            r = call(k, v, block, valid_len, first, out)
+    return out if out is not None else Kv8Cache(*r, block)
 
 
 def suffix_attn_kv8(q, cache: Kv8Cache, k_suffix, v_suffix, prefix_valid_len=None, prefix_mask=None, out=None,
@@ -680,82 +613,11 @@ def suffix_attn_kv8(q, cache: Kv8Cache, k_suffix, v_suffix, prefix_valid_len=Non
     As suffix_attn, with the prefix in a Kv8Cache.  workspace: a contiguous
     uint8 CUDA tensor of at least dm05_suffix_attn_kv8_plan's bytes that no
     call running at the same time uses; allocated for the call when not given."""
-    import torch
-    if q.dim() != 4:
-        raise ValueError("q must be [B,Hq,S,D]")
-    shape = q.shape
-    B, Hq, S, D = shape
-    dev = q.get_device()
-    bf = torch.bfloat16
-    _need("q", q, bf, shape, dev)
-    Bc, Hkv, P, Dc = _need_cache("cache", cache, dev)
-    if Bc != B or Dc != D:
-        raise ValueError("cache must have q's batch and head size")
-    suffix = (B, Hkv, S, D)
-    _need("k_suffix", k_suffix, bf, suffix, dev)
-    _need("v_suffix", v_suffix, bf, suffix, dev)
-    _need_prefix(prefix_valid_len, prefix_mask, B, P, dev)
-    if out is not None:
-        _need("out", out, bf, shape, dev)
-    if lse is not None:
-        _need("lse", lse, torch.float32, (B, Hq, S), dev)
-    if workspace is not None:
-        _need("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
-
-    def call(s):
-        o = torch.empty(shape, dtype=bf, device=dev) if out is None else out
-        ls = torch.empty((B, Hq, S), dtype=torch.float32, device=dev) if lse is None and want_lse else lse
-        key = (B, Hq, Hkv, P, S, D, dev)
-        for attempt in range(2):
-            ws = workspace
-            if ws is None:
-                need = _kv8_workspace(key)
-                ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-            rc = dm05_suffix_attn_kv8(q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-                                      cache.v_scale.data_ptr(), cache.block, _ptr(prefix_valid_len), _ptr(prefix_mask),
-                                      k_suffix.data_ptr(), v_suffix.data_ptr(), o.data_ptr(), _ptr(ls), _ptr(ws),
-                                      0 if ws is None else ws.numel(), B, Hq, Hkv, P, S, D, s)
-            if rc != DM05_ERR_WORKSPACE or workspace is not None or _kv8_workspace_bytes.pop(key, None) is None:
-                break  # else a plan was forced past this module: ask for its workspace again
-        _check(rc, "dm05_suffix_attn_kv8")
-        return o, ls
-    return _on(dev, stream, call)
-
-
-def _mass(q, k, k_scale, block, lse, valid_len, mask, mass_in, mass, stream):
-    import torch
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q must be [B,Hq,S,D] and the keys [B,Hkv,P,D]")
-    B, Hq, S, D = q.shape
-    Hkv, P = k.shape[1], k.shape[2]
-    dev = q.get_device()
-    _need("q", q, torch.bfloat16, (B, Hq, S, D), dev)
-    if k_scale is None:
-        _need("k_prefix", k, torch.bfloat16, (B, Hkv, P, D), dev)
-    else:
-        if block not in (16, 32, 64, 128):
-            raise ValueError("block must be 16, 32, 64 or 128")
-        _need("k8", k, torch.float8_e4m3fn, (B, Hkv, P, D), dev)
-        _need("k_scale", k_scale, torch.float32, (B, Hkv, -(-P // block)), dev)
-    _need("lse", lse, torch.float32, (B, Hq, S), dev)
-    _need_prefix(valid_len, mask, B, P, dev)
-    if mass_in is not None:
-        _need("mass_in", mass_in, torch.float32, (B, Hkv, P), dev)
-    if mass is not None:
-        _need("mass", mass, torch.float32, (B, Hkv, P), dev)
-
-    def call(s):
-        m = torch.empty((B, Hkv, P), dtype=torch.float32, device=dev) if mass is None else mass
-        if k_scale is None:
-            rc = dm05_prefix_attn_mass(q.data_ptr(), k.data_ptr(), _ptr(valid_len), _ptr(mask), lse.data_ptr(),
-                                       _ptr(mass_in), m.data_ptr(), B, Hq, Hkv, P, S, D, s)
-        else:
-            rc = dm05_prefix_attn_mass_kv8(q.data_ptr(), k.data_ptr(), k_scale.data_ptr(), block, _ptr(valid_len),
-                                           _ptr(mask), lse.data_ptr(), _ptr(mass_in), m.data_ptr(), B, Hq, Hkv, P, S,
-                                           D, s)
-        _check(rc, "dm05_prefix_attn_mass")
-        return m
-    return _on(dev, stream, call)
+    call = (_front or _load_front()).suffix_attn_kv8
+    if stream is None:
+        return call(q, cache, k_suffix, v_suffix, prefix_valid_len, prefix_mask, out, lse, want_lse, workspace)
+    with _stream_of(q, stream):
+        return call(q, cache, k_suffix, v_suffix, prefix_valid_len, prefix_mask, out, lse, want_lse, workspace)
 
 
 def prefix_attn_mass(q, k_prefix, lse, prefix_valid_len=None, prefix_mask=None, mass_in=None, mass=None, stream=None):
@@ -763,7 +625,11 @@ def prefix_attn_mass(q, k_prefix, lse, prefix_valid_len=None, prefix_mask=None, 
     suffix_attn call with this q, lse and masks, summed over the queries of
     each KV head and added to mass_in; returns fp32 [B,Hkv,P] (`mass`, which
     may be mass_in itself, when given)."""
-    return _mass(q, k_prefix, None, 0, lse, prefix_valid_len, prefix_mask, mass_in, mass, stream)
+    call = (_front or _load_front()).prefix_attn_mass
+    if stream is None:
+        return call(q, k_prefix, None, 0, lse, prefix_valid_len, prefix_mask, mass_in, mass)
+    with _stream_of(q, stream):
+        return call(q, k_prefix, None, 0, lse, prefix_valid_len, prefix_mask, mass_in, mass)
 
 
 def prefix_attn_mass_kv8(q, k8, k_scale, block, lse, prefix_valid_len=None, prefix_mask=None, mass_in=None, mass=None,
@@ -771,30 +637,11 @@ def prefix_attn_mass_kv8(q, k8, k_scale, block, lse, prefix_valid_len=None, pref
     """prefix_attn_mass over the keys of an 8-bit cache (its k, k_scale and block)."""
     if k_scale is None:
         raise ValueError("k_scale must be given")
-    return _mass(q, k8, k_scale, block, lse, prefix_valid_len, prefix_mask, mass_in, mass, stream)
-
-
-def _need_evicted(mass, B, Hkv, P, P_out, valid_len_in, mask, mass_out, positions, valid_len, index):
-    import torch
-    _need("mass", mass, torch.float32, (B, Hkv, P), index)
-    _need_prefix(valid_len_in, mask, B, P, index)
-    if mass_out is not None:
-        _need("mass_out", mass_out, torch.float32, (B, Hkv, P_out), index)
-    if positions is not None:
-        _need("positions", positions, torch.int32, (B, Hkv, P_out), index)
-    if valid_len is not None:
-        _need("valid_len", valid_len, torch.int32, (B,), index)
-
-
-def _evict_outputs(B, Hkv, P_out, mass_out, positions, valid_len, index):
-    import torch
-    if mass_out is None:
-        mass_out = torch.empty((B, Hkv, P_out), dtype=torch.float32, device=index)
-    if positions is None:
-        positions = torch.empty((B, Hkv, P_out), dtype=torch.int32, device=index)
-    if valid_len is None:
-        valid_len = torch.empty((B,), dtype=torch.int32, device=index)
-    return mass_out, positions, valid_len
+    call = (_front or _load_front()).prefix_attn_mass
+    if stream is None:
+        return call(q, k8, k_scale, block, lse, prefix_valid_len, prefix_mask, mass_in, mass)
+    with _stream_of(q, stream):
+        return call(q, k8, k_scale, block, lse, prefix_valid_len, prefix_mask, mass_in, mass)
 
 
 def prefix_evict(k, v, mass, n_keep: int, n_first: int = 0, n_last: int = 0, prefix_valid_len=None, prefix_mask=None,
@@ -805,34 +652,13 @@ def prefix_evict(k, v, mass, n_keep: int, n_first: int = 0, n_last: int = 0, pre
     in a cache of `bucket` rows (n_keep, or k_out's, when not given).  Fresh
     outputs hold zeros behind the kept rows; given ones keep what they held
     there."""
-    import torch
-    if k.dim() != 4:
-        raise ValueError("k must be [B,Hkv,P,D]")
-    B, Hkv, P, D = k.shape
-    dev = k.get_device()
-    bf = torch.bfloat16
-    if (k_out is None) != (v_out is None):
-        raise ValueError("k_out and v_out must be given together")
-    if k_out is not None and k_out.dim() == 4 and bucket is None:
-        bucket = k_out.shape[2]
-    bucket = n_keep if bucket is None else bucket
-    _need("k", k, bf, (B, Hkv, P, D), dev)
-    _need("v", v, bf, (B, Hkv, P, D), dev)
-    if k_out is not None:
-        _need("k_out", k_out, bf, (B, Hkv, bucket, D), dev)
-        _need("v_out", v_out, bf, (B, Hkv, bucket, D), dev)
-    _need_evicted(mass, B, Hkv, P, bucket, prefix_valid_len, prefix_mask, mass_out, positions, valid_len, dev)
-
-    def call(s):
-        ko, vo = k_out, v_out
-        if ko is None:
-            ko, vo = [torch.zeros((B, Hkv, max(bucket, 0), D), dtype=bf, device=dev) for _ in range(2)]
-        mo, po, vl = _evict_outputs(B, Hkv, max(bucket, 0), mass_out, positions, valid_len, dev)
-        _check(dm05_prefix_evict(k.data_ptr(), v.data_ptr(), mass.data_ptr(), _ptr(prefix_valid_len),
-                                 _ptr(prefix_mask), ko.data_ptr(), vo.data_ptr(), mo.data_ptr(), po.data_ptr(),
-                                 vl.data_ptr(), B, Hkv, P, bucket, D, n_keep, n_first, n_last, s), "dm05_prefix_evict")
-        return EvictedPrefix(ko, vo, mo, po, vl)
-    return _on(dev, stream, call)
+    call = (_front or _load_front()).prefix_evict
+    args = (k, v, mass, n_keep, n_first, n_last, prefix_valid_len, prefix_mask, bucket, k_out, v_out, mass_out, positions,
+            valid_len)
+    if stream is None:
+        return EvictedPrefix(*call(*args))
+    with _stream_of(k, stream):
+        return EvictedPrefix(*call(*args))
 
 
 def prefix_evict_kv8(cache: Kv8Cache, mass, n_keep: int, n_first: int = 0, n_last: int = 0, prefix_valid_len=None,
@@ -841,22 +667,12 @@ def prefix_evict_kv8(cache: Kv8Cache, mass, n_keep: int, n_first: int = 0, n_las
     """prefix_evict on an 8-bit cache: the kept rows form blocks of the same
     size with scales of their own (a fresh `out` has zero codes and unit
     scales behind them)."""
-    dev = cache.k.get_device()
-    B, Hkv, P, D = _need_cache("cache", cache, dev)
-    if out is not None and bucket is None and out.k.dim() == 4:
-        bucket = out.k.shape[2]
-    bucket = n_keep if bucket is None else bucket
-    if out is not None and (_need_cache("out", out, dev) != (B, Hkv, bucket, D) or out.block != cache.block):
-        raise ValueError(f"out must be a cache of {bucket} rows with cache's other sizes and block")
-    _need_evicted(mass, B, Hkv, P, bucket, prefix_valid_len, prefix_mask, mass_out, positions, valid_len, dev)
-
-    def call(s):
-        c = _empty_cache(B, Hkv, max(bucket, 0), D, cache.block, dev) if out is None else out
-        mo, po, vl = _evict_outputs(B, Hkv, max(bucket, 0), mass_out, positions, valid_len, dev)
-        _check(dm05_prefix_evict_kv8(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-                                     cache.v_scale.data_ptr(), cache.block, mass.data_ptr(), _ptr(prefix_valid_len),
-                                     _ptr(prefix_mask), c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(),
-                                     c.v_scale.data_ptr(), mo.data_ptr(), po.data_ptr(), vl.data_ptr(), B, Hkv, P,
-                                     bucket, D, n_keep, n_first, n_last, s), "dm05_prefix_evict_kv8")
-        return EvictedPrefixKv8(c, mo, po, vl)
-    return _on(dev, stream, call)
+    call = (_front or _load_front()).prefix_evict_kv8
+    args = (cache, mass, n_keep, n_first, n_last, prefix_valid_len, prefix_mask, bucket, out, mass_out, positions,
+            valid_len)
+    if stream is None:
+        c, m, p, n = call(*args)
+    else:
+        with _stream_of(cache.k, stream):
+            c, m, p, n = call(*args)
+    return EvictedPrefixKv8(out if out is not None else Kv8Cache(*c, cache.block), m, p, n)

@@ -1,4 +1,6 @@
-"""Builds the C-ABI shared library libdm05_suffix_attn.so in-tree (sm_100a)."""
+"""Builds the C-ABI shared library libdm05_suffix_attn.so in-tree (sm_100a), and
+the Python module _torch_front.so, the torch front end of the prefix-cache
+operators (host code)."""
 from __future__ import annotations
 
 import os
@@ -25,13 +27,19 @@ NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", 
               "-Xcompiler", "-fPIC", "-shared"]
 
 
+FRONT = os.path.join(HERE, "_torch_front.so")
+FRONT_SOURCE = os.path.join(HERE, "csrc", "torch_front.cpp")
+
+
 def nvcc() -> str:
     cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile when the library is missing or older than a source file."""
+    """Compile when the library is missing or older than a source file (the
+    front end with it)."""
+    build_front(force)
     if not force and os.path.exists(LIB):
         t = os.path.getmtime(LIB)
         if all(os.path.getmtime(d) <= t for d in deps()):
@@ -44,6 +52,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build_front(force: bool = False) -> str:
+    """Compile the torch front end when it is missing or older than its sources."""
+    sources = [FRONT_SOURCE, os.path.join(ROOT, "include", "dm05_suffix_attn.h")]
+    if not force and os.path.exists(FRONT):
+        t = os.path.getmtime(FRONT)
+        if all(os.path.getmtime(d) <= t for d in sources):
+            return FRONT
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
+    tmp = FRONT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-I{d}" for d in include], FRONT_SOURCE, "-o", tmp, "-L" + os.path.join(home, "lib"), "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, FRONT)
+    return FRONT
 
 
 if __name__ == "__main__":

@@ -226,8 +226,8 @@ __device__ __forceinline__ uint32_t select_key(const SelectParams &p, int vl, in
 }
 
 // Adds one to the bin of every participating lane's digit, one atomic per
-// distinct digit of the warp (weights of one head share their exponent, so
-// single adds would queue on a few bins).
+// distinct digit of the warp: for the first digit, where weights of one head
+// share their exponent and single adds would queue on a few bins.
 __device__ __forceinline__ void count_digit(int *hist, uint32_t digit, bool active)
 {
     const uint32_t who = __ballot_sync(0xffffffffu, active);
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
             if (KPT > 0) {
 #pragma unroll
                 for (int i = 0; i < kKeys; ++i)
-                    count_digit(hist[pass], (keys[i] >> shift) & 255u, keys[i] != 0u && (keys[i] & known) == prefix);
+                    if (keys[i] != 0u && (keys[i] & known) == prefix) atomicAdd(&hist[pass][(keys[i] >> shift) & 255u], 1);
             } else {
                 for (int i = 0; i < rounds; ++i) {
                     const uint32_t k = key_of(i);
