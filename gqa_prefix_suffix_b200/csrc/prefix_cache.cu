@@ -201,7 +201,7 @@ int mass_call(bool kv8, const void *q, const void *k, const float *k_scale, int 
     mp.N = N;
     mp.nblk = blocks_of(P, shift);
     mp.shift = shift;
-    mp.scale_log2 = static_cast<float>(kLog2e / std::sqrt(static_cast<double>(D)));
+    mp.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
     const int splits = mass_splits(units, (P + dm05::mass::kTile - 1) / dm05::mass::kTile, dev.num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(units), 1);

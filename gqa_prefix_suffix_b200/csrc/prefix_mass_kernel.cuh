@@ -19,8 +19,11 @@
 //
 // Warp roles: warp 16 loads, warp 17 issues the MMAs, warps 0-15 are two
 // groups that take the tiles in turn (two warps per 32 keys), so that one
-// group's waits run beside the other's exponentials.  Four logit buffers of
-// 128 columns fill the tensor memory, so the MMAs run ahead.
+// group's waits run beside the other's exponentials.  The 256 products
+// of a logit are summed in two halves, joined in fp32 registers: the tensor
+// cores' running sum loses a little with every step (2e-6 of the weight of
+// a key of large logit in one chain, 0.8e-6 in two).  Two buffers of two halves
+// of 128 columns fill the tensor memory.
 #pragma once
 
 #include "kv8_attn_kernel.cuh"
@@ -33,7 +36,7 @@ constexpr int kSoftWarps = 16;
 constexpr int kLoadWarp = 16;
 constexpr int kIssueWarp = 17;
 constexpr int kThreadsM = 576;
-constexpr int kBufs = 4;       // logit buffers of 128 columns
+constexpr int kBufs = 2;       // logit buffers of two halves of 128 columns
 
 template <bool KV8>
 struct Smem {
@@ -53,7 +56,7 @@ struct Smem {
     static constexpr int kBarFinal = kBarPair + 8;
     static constexpr int kNumBars = kBarFinal + 1;
     static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
-    // per query row {scale, -lse log2(e)}, then partial sums [2 parities][2 groups][128]
+    // per query row {scale, -lse}, then partial sums [2 parities][2 groups][128]
     // (before: the rows' largest magnitudes, [4][128])
     static constexpr int kRowOff = (kTmemSlotOff + 16 + 15) / 16 * 16;
     static constexpr int kSumOff = kRowOff + 128 * 8;
@@ -72,7 +75,7 @@ struct Params {
     uint32_t *err;
     int Hkv, P, GS, N;       // N: GS rounded up to 16, the MMA's N
     int nblk, shift;
-    float scale_log2;
+    float scale;             // 1 / sqrt(D)
 };
 
 template <bool KV8>
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 const uint64_t kd = kdesc + static_cast<uint64_t>((s * L::kSlotBytes) >> 4);
-                const uint32_t d = tmem + sb * 128;
+                const uint32_t d = tmem + sb * 256;
 #pragma unroll
                 for (int kk = 0; kk < 16; ++kk) {
                     if (KV8) {
@@ -174,11 +177,11 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                         const int j = kk >> 1;
                         const uint32_t qo = ((j >> 1) * qpitch + (j & 1) * 64 + (kk & 1) * 32) >> 4;
                         const uint32_t ko = ((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4;
-                        ptx::mma_f8_ss(d, kd + ko, qdesc + qo, idesc, kk > 0 ? 1u : 0u);
+                        ptx::mma_f8_ss(d + (kk >> 3) * 128, kd + ko, qdesc + qo, idesc, (kk & 7) > 0 ? 1u : 0u);
                     } else {
                         const uint32_t qo = ((kk >> 2) * qpitch + (kk & 3) * 32) >> 4;
                         const uint32_t ko = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-                        ptx::mma_bf16_ss(d, kd + ko, qdesc + qo, idesc, kk > 0 ? 1u : 0u);
+                        ptx::mma_bf16_ss(d + (kk >> 3) * 128, kd + ko, qdesc + qo, idesc, (kk & 7) > 0 ? 1u : 0u);
                     }
                 }
                 ptx::mma_commit(&bars[L::kBarEmpty + s]);
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
         };
         if (T > 0) {
             // ---- query rows: their constants, and the two terms for an 8-bit cache
-            float scale = p.scale_log2;
+            float factor = p.scale;
             if (KV8) {
                 failed = !warp_wait(&bars[L::kBarQFull], 0);
                 uint8_t *chunk = smem + c4 * p.N * 128 + row * 128;
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                         const uint32_t bits = max(max(qmax[0], qmax[128]), max(qmax[256], qmax[384]));
                         const float s = kv8::row_scale(bits);
                         // a row with a non-finite element becomes NaN
-                        scale = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
+                        factor = bits < 0x7f80u ? s * p.scale : __int_as_float(0x7fffffff);
                         kv8::split_chunk(chunk, row & 7, cache::pow2_inverse(s));
                     }
                     ptx::fence_proxy_async_smem();
@@ -223,11 +226,11 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 }
             }
             if (c4 == 0) {
-                // rows that do not exist, and rows that saw no key (-inf), add 2^-inf
+                // rows that do not exist, and rows that saw no key (-inf), add e^-inf
                 float l = INFINITY;
                 if (row < p.GS) l = ptx::load(p.lse + static_cast<size_t>(unit) * p.GS + row);
                 if (l == -INFINITY) l = INFINITY;
-                rows[row] = make_float2(scale, -l * 1.4426950408889634f);
+                rows[row] = make_float2(factor, -l);
             }
             ptx::mbar_arrive(&bars[L::kBarQReady]);
             if (!failed) failed = !warp_wait(&bars[L::kBarQReady], 0);
@@ -263,35 +266,40 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 break;
             }
             ptx::tc_fence_after_sync();
-            const uint32_t col = tmem + lane_base + sb * 128;
-            const uint64_t ks2 = ptx::f32x2(ks, ks);
+            const uint32_t col = tmem + lane_base + sb * 256;
+            const uint64_t ks2 = ptx::f32x2(ks, ks), log2e = ptx::f32x2(1.4426950408889634f, 1.4426950408889634f);
             uint64_t acc[2] = {ptx::f32x2(0.0f, 0.0f), ptx::f32x2(0.0f, 0.0f)};
+            const int last = groups - 1 - ((groups - 1 - hf) & 1);  // this warp's last column group
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t raw[2][16];
-                const int g0 = hf + 4 * h;
-                const bool one = g0 < groups, two = g0 + 2 < groups;
-                if (one) ptx::tmem_ld16(col + g0 * 16, raw[0]);
-                if (two) ptx::tmem_ld16(col + g0 * 16 + 32, raw[1]);
+            for (int h = 0; h < 4; ++h) {
+                const int g = hf + 2 * h;
+                if (g >= groups) break;
+                uint32_t raw[2][16];  // the two halves of the 256 products
+                ptx::tmem_ld16(col + g * 16, raw[0]);
+                ptx::tmem_ld16(col + 128 + g * 16, raw[1]);
                 ptx::tmem_ld_wait();
-                if (h == 1) {
+                if (g == last) {
                     ptx::tc_fence_before_sync();
                     ptx::mbar_arrive(&bars[L::kBarSFree + sb]);
                 }
+                const float4 *rc = reinterpret_cast<const float4 *>(rows + g * 16);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (g == 0 ? !one : !two) break;
-                    const float4 *rc = reinterpret_cast<const float4 *>(rows + (g0 + 2 * g) * 16);
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float4 r = rc[e >> 1];  // {scale, -lse} of two query rows
-                        uint64_t f = ptx::f32x2(r.x, r.z);
-                        if (KV8) f = ptx::mul_f32x2(f, ks2);
-                        const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
-                            ptx::f32x2(__uint_as_float(raw[g][e]), __uint_as_float(raw[g][e + 1])), f, ptx::f32x2(r.y, r.w)));
-                        acc[(e >> 1) & 1] = ptx::add_f32x2(acc[(e >> 1) & 1], ptx::f32x2(ptx::ex2(x.x), ptx::ex2(x.y)));
-                    }
+                for (int e = 0; e < 16; e += 2) {
+                    const float4 r = rc[e >> 1];  // {scale, -lse} of two query rows
+                    uint64_t f = ptx::f32x2(r.x, r.z);
+                    if (KV8) f = ptx::mul_f32x2(f, ks2);
+                    const uint64_t dot = ptx::add_f32x2(ptx::f32x2(__uint_as_float(raw[0][e]), __uint_as_float(raw[0][e + 1])),
+                                                        ptx::f32x2(__uint_as_float(raw[1][e]), __uint_as_float(raw[1][e + 1])));
+                    // z - lse is formed in natural units, where 1 / sqrt(D) is a power of
+                    // two and the difference of near equals exact, and only then taken
+                    // to base 2 (the other way round costs 2^-24 of the lse)
+                    const float2 x = ptx::unpack_f32x2(ptx::mul_f32x2(ptx::fma_f32x2(dot, f, ptx::f32x2(r.y, r.w)), log2e));
+                    acc[(e >> 1) & 1] = ptx::add_f32x2(acc[(e >> 1) & 1], ptx::f32x2(ptx::ex2(x.x), ptx::ex2(x.y)));
                 }
+            }
+            if (hf >= groups) {  // no column group for this warp (N = 16)
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(&bars[L::kBarSFree + sb]);
             }
             const float2 s2 = ptx::unpack_f32x2(ptx::add_f32x2(acc[0], acc[1]));
             // the halves meet in the first one's warp; two tiles of a group apart,
