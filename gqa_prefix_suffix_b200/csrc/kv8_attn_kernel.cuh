@@ -38,12 +38,12 @@
 // copies it to tensor memory (into the second S buffer, which is not in use
 // yet), and the softmax warps rewrite it in place as the two e4m3 terms.
 //
-// A unit's tiles may be split over any number of CTAs: each writes its
+// A unit's tiles may be split over any number of CTAs (and its query rows
+// over blocks, so that a CTA writes fewer partial rows): each writes its
 // unnormalised O with {m, l} per row, and merge_kernel, launched behind it,
 // joins them.  (A cluster merge inside the kernel, as the bf16 kernel has,
-// limits a unit to 16 CTAs and the grid to what clusters leave resident: 15.3
-// instead of XX us at B = 1, P = 1024, S = 50 and 68 instead of XX us at B = 2,
-// P = 30016.)
+// limits a unit to 16 CTAs and the grid to what clusters leave resident: 68
+// instead of 42 us at B = 2, P = 30016.)
 #pragma once
 
 #include "prefix_cache_kernels.cuh"
@@ -187,8 +187,9 @@ struct Params {
     uint32_t *err;
     uint8_t *part;                   // splits > 1: partial rows [units][splits][GS], kPartRow bytes each
     int Hkv, P, S, GS;               // GS: query rows of a unit
-    int qrows;                       // GS rounded up to 8: rows of a Q chunk in shared memory
-    int splits;                      // CTAs per unit
+    int qrows;                       // query rows of a block, a multiple of 8: rows of a Q chunk in shared memory
+    int row_blocks;                  // blocks of a unit
+    int splits;                      // CTAs per unit and block
     int nblk, shift;
     float scale_log2;
 };
@@ -227,39 +228,43 @@ __device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3
         : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
 }
 
-// A query row is cut into four chunks of 64 bf16 (128 swizzled bytes each;
-// sw: the row's swizzle).  A thread takes one chunk of a row: its largest
-// magnitude as bf16 bits (magnitudes order like their bits).
-__device__ __forceinline__ uint32_t chunk_max(const uint8_t *chunk, uint32_t sw)
+// Rewrites n query rows (four chunks of 64 bf16 a row, qpitch bytes apart,
+// each 128 swizzled bytes) as two e4m3 terms of the row scaled by a power of
+// two to a largest element in (224, 448].  The 64 bytes of 32 bf16 values
+// become their 32 first terms, then their 32 second ones, so a thread rewrites
+// only what it has read.  Warp w of 16 takes rows [8 w, 8 w + 8), a lane one
+// chunk of one row (conflict-free).  factor[row] becomes the row's scale times
+// `unit`, or NaN for a row with an infinity (NaN elements stay NaN codes).
+__device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, int warp, float unit, float *factor)
 {
-    uint32_t top = 0u;
+    const int lane = threadIdx.x & 31;
+    const int row = warp * 8 + (lane & 7);
+    if (warp * 8 >= n) return;
+    const bool mine = row < n;
+    uint8_t *chunk = q + (lane >> 3) * qpitch + row * 128;
+    auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + ((u ^ (lane & 7)) << 4)); };
+    __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
+    if (mine) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(chunk + ((u ^ sw) << 4));
-        top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
-        top = __vmaxu2(top, v.w & 0x7fff7fffu);
+        for (int u = 0; u < 8; ++u) {
+            const uint4 v = *unit16(u);
+            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(h[e]));
+        }
     }
-    return max(top & 0xffffu, top >> 16);
-}
-
-// Power-of-two scale of a query row whose largest element has these bf16
-// bits, so that the scaled row's largest element lies in (224, 448].
-__device__ __forceinline__ float row_scale(uint32_t bits)
-{
-    return bits < 0x7f80u ? cache::pow2_scale(__uint_as_float(bits << 16)) : 1.0f;
-}
-
-// Rewrites the chunk as two e4m3 terms of its scaled values: the 64 bytes of
-// 32 bf16 values become their 32 first terms, then their 32 second ones, so
-// a thread rewrites only what it has read.
-__device__ __forceinline__ void split_chunk(uint8_t *chunk, uint32_t sw, float inv)
-{
+    float amax = fmaxf(__low2float(top), __high2float(top));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+    const float s = amax < INFINITY ? cache::pow2_scale(amax) : 1.0f;
+    if (!mine) return;
+    if (lane < 8) factor[row] = amax < INFINITY ? s * unit : __int_as_float(0x7fffffff);
+    const float inv = cache::pow2_inverse(s);
 #pragma unroll 1
     for (int g = 0; g < 2; ++g) {
-        auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + (((g * 4 + u) ^ sw) << 4)); };
         uint4 v[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = *unit16(u);
+        for (int u = 0; u < 4; ++u) v[u] = *unit16(g * 4 + u);
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -268,10 +273,10 @@ __device__ __forceinline__ void split_chunk(uint8_t *chunk, uint32_t sw, float i
             two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
                       __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
         }
-        *unit16(0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *unit16(1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-        *unit16(2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *unit16(3) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+        *unit16(g * 4) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *unit16(g * 4 + 1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+        *unit16(g * 4 + 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *unit16(g * 4 + 3) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
     }
 }
 
@@ -288,7 +293,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemSlotOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int C = p.splits;
-    const int unit = blockIdx.x / C, rank = blockIdx.x - unit * C;
+    const int cl = blockIdx.x / C, rank = blockIdx.x - cl * C;
+    const int unit = cl / p.row_blocks, q0 = (cl - unit * p.row_blocks) * p.qrows;
+    const int nr = min(p.qrows, p.GS - q0);  // query rows [q0, q0 + nr) of the unit
     const int b = unit / p.Hkv;
     const int qpitch = p.qrows * 128;  // bytes of a 64-column chunk of Q
 
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         pol = ptx::policy_evict_first();
         // rows of the MMA past qrows read whatever lies behind: rows of their own
         ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(4 * qpitch));
-        ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, 0, 0, unit);
+        ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, q0, 0, unit);
         if (first) {
             ptx::mbar_arrive_expect_tx(&bars[L::kBarKFull], kSlotBytes);
             ptx::tma_load_4d_hint(k_slot(0), &tm_ks, &bars[L::kBarKFull], 0, 0, 0, unit, pol);
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     }
 
     const int vl = cache::clamped_len(p.valid_len, b, p.P, p.err,
-                                      threadIdx.x == 0 && rank == 0 && unit % p.Hkv == 0);
+                                      threadIdx.x == 0 && rank == 0 && q0 == 0 && unit % p.Hkv == 0);
     const int TS = (p.S + kSufTile - 1) / kSufTile;
     const int t_all = TS + (vl + kTile - 1) / kTile;
     const int t_begin = static_cast<int>((static_cast<long long>(t_all) * rank) / C);
@@ -577,26 +584,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
         };
         float sqs = 0.0f;  // this row's query scale * log2(e) / sqrt(D)
         if (T > 0) {
-            // ---- Q as two e4m3 terms: this thread's 64 values of its row
             failed = !warp_wait(&bars[L::kBarQFull], 0);
             if (!failed && ns > 0) failed = !warp_wait(&bars[L::kBarQFree], 0);
-            uint8_t *chunk = smem + c4 * qpitch + row * 128;
-            uint32_t *qmax = reinterpret_cast<uint32_t *>(xl) + row;  // [4][128]
-            const bool mine = row < p.GS;
             if (!failed) {
-                if (mine) qmax[c4 * kMRows] = chunk_max(chunk, row & 7);
-                failed = !row_sync();
-            }
-            if (!failed) {
-                if (mine) {
-                    const uint32_t bits = max(max(qmax[0], qmax[kMRows]), max(qmax[2 * kMRows], qmax[3 * kMRows]));
-                    const float s = row_scale(bits);
-                    // a row with a non-finite element becomes NaN
-                    sqs = bits < 0x7f80u ? s * p.scale_log2 : __int_as_float(0x7fffffff);
-                    split_chunk(chunk, row & 7, cache::pow2_inverse(s));
-                }
+                split_query_rows(smem, qpitch, nr, warp, p.scale_log2, xl);
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(&bars[L::kBarQConv]);
+                failed = !warp_wait(&bars[L::kBarQConv], 0);
+                if (row < nr) sqs = xl[row];
             }
         }
         float m_l = -INFINITY;  // what this thread's sum refers to
@@ -717,7 +712,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 }
                 if (partial) ptx::tmem_st_wait();
             }
-            if (row >= p.GS) hmax = -INFINITY;  // not a query row: never a reason to rescale
+            if (row >= nr) hmax = -INFINITY;  // not a query row: never a reason to rescale
             xmax[hf * kMRows + row] = hmax;
             if (!pair_sync()) {
                 failed = true;
@@ -841,7 +836,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         xl[c4 * kMRows + row] = l;
         if (!failed && !row_sync()) failed = true;
         const float l_row = (xl[row] + xl[kMRows + row]) + (xl[2 * kMRows + row] + xl[3 * kMRows + row]);
-        const bool row_valid = row < p.GS;
+        const bool row_valid = row < nr;
         const float inv_l = 1.0f / l_row;
         // The rows leave through shared memory in one copy: bf16 rows in the
         // layout of a Q tile, partial rows as they lie in the workspace.
@@ -882,17 +877,17 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 *reinterpret_cast<float4 *>(smem + row * kPartRow + kHeadDim * 4) =
                     make_float4(m_end, have_o && !failed ? l_row : 0.0f, 0.0f, 0.0f);
             else if (p.lse != nullptr && !failed)
-                p.lse[static_cast<size_t>(unit) * p.GS + row] = (m_end + ptx::lg2(l_row)) * 0.69314718055994531f;
+                p.lse[static_cast<size_t>(unit) * p.GS + q0 + row] = (m_end + ptx::lg2(l_row)) * 0.69314718055994531f;
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(&bars[L::kBarOut]);
         if (threadIdx.x == 0 && !failed) {
             if (ptx::mbar_wait(&bars[L::kBarOut], 0, kWaitLimitNs)) {
                 if (C == 1)
-                    ptx::tma_store_4d(&tm_out, smem, 0, 0, 0, unit);
+                    ptx::tma_store_4d(&tm_out, smem, 0, q0, 0, unit);
                 else
-                    ptx::bulk_store_s2g(p.part + (static_cast<size_t>(unit) * C + rank) * p.GS * kPartRow,
-                                        ptx::smem_addr(smem), static_cast<uint32_t>(p.GS * kPartRow));
+                    ptx::bulk_store_s2g(p.part + ((static_cast<size_t>(unit) * C + rank) * p.GS + q0) * kPartRow,
+                                        ptx::smem_addr(smem), static_cast<uint32_t>(nr * kPartRow));
                 ptx::bulk_commit();
                 ptx::bulk_wait_all();
                 ptx::fence_proxy_async_global();

@@ -95,15 +95,21 @@ int set_attributes(const Device &dev, bool mass) noexcept
 }
 
 struct Kv8Plan {
-    int splits = 1;    // CTAs per (sample, KV head)
-    size_t bytes = 0;  // partial results
+    int splits = 1;      // CTAs per (sample, KV head) and block of query rows
+    int row_blocks = 1;  // blocks of the GS query rows
+    int qrows = 8;       // rows of a block (a multiple of 8)
+    size_t bytes = 0;    // partial results
 };
 
 // The fewest CTAs per (sample, KV head) that make the longest run of tiles as
-// short as one wave allows; unsplit while that is as short.
+// short as one wave allows; unsplit while that is as short.  A split unit's
+// query rows are cut into blocks while SMs are left (at least 32 rows each):
+// every CTA then splits, stages and writes fewer rows, which at B = 1, P =
+// 1024, S = 50 is half its time, for K and V tiles read from L2 once more.
 Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
 {
     const long long units = static_cast<long long>(B) * Hkv;
+    const int GS = Hq / Hkv * S;
     const int tiles = (P + dm05::kv8::kTile - 1) / dm05::kv8::kTile + (S + dm05::kv8::kSufTile - 1) / dm05::kv8::kSufTile;
     const int most = static_cast<int>(std::min<long long>(
         std::min(tiles, dm05::kv8::kMaxSplits8), std::max<long long>(1, dev.num_sms / units)));
@@ -114,7 +120,12 @@ Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
         const int run = (tiles + most - 1) / most;
         pl.splits = (tiles + run - 1) / run;
     }
-    if (pl.splits > 1) pl.bytes = static_cast<size_t>(units) * pl.splits * (Hq / Hkv) * S * dm05::kv8::kPartRow;
+    int blocks = 1;
+    if (pl.splits > 1)
+        blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(GS / 32, dev.num_sms / (units * pl.splits))));
+    pl.qrows = ((GS + blocks - 1) / blocks + 7) / 8 * 8;
+    pl.row_blocks = (GS + pl.qrows - 1) / pl.qrows;
+    if (pl.splits > 1) pl.bytes = static_cast<size_t>(units) * pl.splits * GS * dm05::kv8::kPartRow;
     return pl;
 }
 
@@ -338,9 +349,11 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
         if (workspace == nullptr || workspace_bytes < pl.bytes) return DM05_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return DM05_ERR_ALIGN;
     }
-    const int GS = Hq / Hkv * S, units = B * Hkv, qrows = (GS + 7) / 8 * 8;
+    const int GS = Hq / Hkv * S, units = B * Hkv;
+    const long long grid = static_cast<long long>(units) * pl.row_blocks * pl.splits;
+    if (grid > 0x7fffffffLL) return DM05_ERR_SHAPE;
     CUtensorMap tq, tkp, tvp, tks, tvs, to;
-    if (encode_rows16(&tq, q, GS, units, qrows) != DM05_OK || encode_rows16(&to, out, GS, units, qrows) != DM05_OK ||
+    if (encode_rows16(&tq, q, GS, units, pl.qrows) != DM05_OK || encode_rows16(&to, out, GS, units, pl.qrows) != DM05_OK ||
         encode_rows16(&tks, k_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK ||
         encode_rows16(&tvs, v_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK)
         return DM05_ERR_CUDA;
@@ -364,13 +377,14 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     ap.P = P;
     ap.S = S;
     ap.GS = GS;
-    ap.qrows = qrows;
+    ap.qrows = pl.qrows;
+    ap.row_blocks = pl.row_blocks;
     ap.splits = pl.splits;
     ap.nblk = blocks_of(P, shift);
     ap.shift = shift;
     ap.scale_log2 = static_cast<float>(kLog2e / std::sqrt(static_cast<double>(D)));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * pl.splits), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(dm05::kv8::kThreads8, 1, 1);
     cfg.dynamicSmemBytes = dm05::kv8::Smem::kAllocBytes;
     cfg.stream = stream;

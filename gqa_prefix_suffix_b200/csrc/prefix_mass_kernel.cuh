@@ -51,15 +51,12 @@ struct Smem {
     static constexpr int kBarEmpty = kBarFull + kSlots;
     static constexpr int kBarSFull = kBarEmpty + kSlots;
     static constexpr int kBarSFree = kBarSFull + kBufs;
-    static constexpr int kBarRow = kBarSFree + kBufs;
-    static constexpr int kBarPair = kBarRow + 4;  // per group and lane quarter: its two warps
+    static constexpr int kBarPair = kBarSFree + kBufs;  // per group and lane quarter: its two warps
     static constexpr int kBarFinal = kBarPair + 8;
     static constexpr int kNumBars = kBarFinal + 1;
     static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
-    // per query row {scale, -lse}, then partial sums [2 parities][2 groups][128]
-    // (before: the rows' largest magnitudes, [4][128])
-    static constexpr int kRowOff = (kTmemSlotOff + 16 + 15) / 16 * 16;
-    static constexpr int kSumOff = kRowOff + 128 * 8;
+    static constexpr int kRowOff = (kTmemSlotOff + 16 + 15) / 16 * 16;  // per query row: factors [128], -lse [128]
+    static constexpr int kSumOff = kRowOff + 2 * 128 * 4;               // partial sums [2 parities][2 groups][128]
     static constexpr int kEnd = kSumOff + 4 * 128 * 4;
     static constexpr int kAllocBytes = kEnd + 1024;
     static_assert(kAllocBytes <= 232448, "shared memory of a CTA");
@@ -87,7 +84,8 @@ __global__ void __launch_bounds__(kThreadsM, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemSlotOff);
-    float2 *rows = reinterpret_cast<float2 *>(smem + L::kRowOff);
+    float *factors = reinterpret_cast<float *>(smem + L::kRowOff);  // per query row: its scale / sqrt(D)
+    float *lses = factors + 128;                                    // and -lse
     float *sums = reinterpret_cast<float *>(smem + L::kSumOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = blockIdx.y, b = unit / p.Hkv;
@@ -103,7 +101,6 @@ __global__ void __launch_bounds__(kThreadsM, 1)
             ptx::mbar_init(&bars[L::kBarSFull + i], 1);
             ptx::mbar_init(&bars[L::kBarSFree + i], kSoftWarps / 2 * 32);
         }
-        for (int i = 0; i < 4; ++i) ptx::mbar_init(&bars[L::kBarRow + i], 128);
         for (int i = 0; i < 8; ++i) ptx::mbar_init(&bars[L::kBarPair + i], 64);
         ptx::mbar_init(&bars[L::kBarFinal], 1);
         ptx::fence_mbar_init();
@@ -196,41 +193,20 @@ __global__ void __launch_bounds__(kThreadsM, 1)
         const int q4 = warp & 3, c4 = warp >> 2;
         const int row = q4 * 32 + lane;  // a key of the tile; a query row while those are prepared
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
-        uint64_t *row_bar = &bars[L::kBarRow + q4];
-        int row_phase = 0;
-        auto row_sync = [&]() -> bool {  // the four warps of these 32 rows
-            ptx::mbar_arrive(row_bar);
-            return warp_wait(row_bar, row_phase++ & 1);
-        };
         if (T > 0) {
             // ---- query rows: their constants, and the two terms for an 8-bit cache
-            float factor = p.scale;
             if (KV8) {
                 failed = !warp_wait(&bars[L::kBarQFull], 0);
-                uint8_t *chunk = smem + c4 * p.N * 128 + row * 128;
-                uint32_t *qmax = reinterpret_cast<uint32_t *>(sums) + row;  // [4][128]
-                if (!failed) {
-                    if (row < p.GS) qmax[c4 * 128] = kv8::chunk_max(chunk, row & 7);
-                    failed = !row_sync();
-                }
-                if (!failed) {
-                    if (row < p.GS) {
-                        const uint32_t bits = max(max(qmax[0], qmax[128]), max(qmax[256], qmax[384]));
-                        const float s = kv8::row_scale(bits);
-                        // a row with a non-finite element becomes NaN
-                        factor = bits < 0x7f80u ? s * p.scale : __int_as_float(0x7fffffff);
-                        kv8::split_chunk(chunk, row & 7, cache::pow2_inverse(s));
-                    }
-                    ptx::fence_proxy_async_smem();
-                    failed = !row_sync();  // qmax is read: the sums may be written
-                }
+                if (!failed) kv8::split_query_rows(smem, p.N * 128, p.GS, warp, p.scale, factors);
+                ptx::fence_proxy_async_smem();
+            } else if (c4 == 0) {
+                factors[row] = p.scale;
             }
-            if (c4 == 0) {
+            if (c4 == 1) {
                 // rows that do not exist, and rows that saw no key (-inf), add e^-inf
                 float l = INFINITY;
                 if (row < p.GS) l = ptx::load(p.lse + static_cast<size_t>(unit) * p.GS + row);
-                if (l == -INFINITY) l = INFINITY;
-                rows[row] = make_float2(factor, -l);
+                lses[row] = l == -INFINITY ? -INFINITY : -l;
             }
             ptx::mbar_arrive(&bars[L::kBarQReady]);
             if (!failed) failed = !warp_wait(&bars[L::kBarQReady], 0);
@@ -282,19 +258,26 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                     ptx::tc_fence_before_sync();
                     ptx::mbar_arrive(&bars[L::kBarSFree + sb]);
                 }
-                const float4 *rc = reinterpret_cast<const float4 *>(rows + g * 16);
+                const float4 *fc = reinterpret_cast<const float4 *>(factors + g * 16);
+                const float4 *lc = reinterpret_cast<const float4 *>(lses + g * 16);
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 r = rc[e >> 1];  // {scale, -lse} of two query rows
-                    uint64_t f = ptx::f32x2(r.x, r.z);
-                    if (KV8) f = ptx::mul_f32x2(f, ks2);
-                    const uint64_t dot = ptx::add_f32x2(ptx::f32x2(__uint_as_float(raw[0][e]), __uint_as_float(raw[0][e + 1])),
-                                                        ptx::f32x2(__uint_as_float(raw[1][e]), __uint_as_float(raw[1][e + 1])));
-                    // z - lse is formed in natural units, where 1 / sqrt(D) is a power of
-                    // two and the difference of near equals exact, and only then taken
-                    // to base 2 (the other way round costs 2^-24 of the lse)
-                    const float2 x = ptx::unpack_f32x2(ptx::mul_f32x2(ptx::fma_f32x2(dot, f, ptx::f32x2(r.y, r.w)), log2e));
-                    acc[(e >> 1) & 1] = ptx::add_f32x2(acc[(e >> 1) & 1], ptx::f32x2(ptx::ex2(x.x), ptx::ex2(x.y)));
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 f4 = fc[e >> 2], l4 = lc[e >> 2];
+#pragma unroll
+                    for (int d = 0; d < 4; d += 2) {
+                        uint64_t f = d == 0 ? ptx::f32x2(f4.x, f4.y) : ptx::f32x2(f4.z, f4.w);
+                        const uint64_t l = d == 0 ? ptx::f32x2(l4.x, l4.y) : ptx::f32x2(l4.z, l4.w);
+                        if (KV8) f = ptx::mul_f32x2(f, ks2);
+                        const int i = e + d;
+                        const uint64_t dot =
+                            ptx::add_f32x2(ptx::f32x2(__uint_as_float(raw[0][i]), __uint_as_float(raw[0][i + 1])),
+                                           ptx::f32x2(__uint_as_float(raw[1][i]), __uint_as_float(raw[1][i + 1])));
+                        // z - lse is formed in natural units, where 1 / sqrt(D) is a power of
+                        // two and the difference of near equals exact, and only then taken
+                        // to base 2 (the other way round costs 2^-24 of the lse)
+                        const float2 x = ptx::unpack_f32x2(ptx::mul_f32x2(ptx::fma_f32x2(dot, f, l), log2e));
+                        acc[d >> 1] = ptx::add_f32x2(acc[d >> 1], ptx::f32x2(ptx::ex2(x.x), ptx::ex2(x.y)));
+                    }
                 }
             }
             if (hf >= groups) {  // no column group for this warp (N = 16)
