@@ -798,17 +798,17 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 ptx::tc_fence_after_sync();
                 const float factor = rescale ? ptx::ex2(m_old - m_used) : 1.0f;  // 0 when m_old is -inf
 #pragma unroll 1
-                for (int j = 0; j < kHeadDim / 64; ++j) {
-                    uint32_t o[2][16];
-                    const uint32_t oc = tmem + lane_base + kTmemO8 + hf * (kHeadDim / 2) + j * 32;
-                    ptx::tmem_ld16(oc, o[0]);
-                    ptx::tmem_ld16(oc + 16, o[1]);
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t o[4][16];
+                    const uint32_t oc = tmem + lane_base + kTmemO8 + hf * (kHeadDim / 2) + j * 64;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ptx::tmem_ld16(oc + e * 16, o[e]);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 64; ++e)
                         o[e >> 4][e & 15] = __float_as_uint(__uint_as_float(o[e >> 4][e & 15]) * factor);
-                    ptx::tmem_st16(oc, o[0]);
-                    ptx::tmem_st16(oc + 16, o[1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ptx::tmem_st16(oc + e * 16, o[e]);
                 }
             }
             ptx::tmem_st_wait();
