@@ -38,6 +38,13 @@
 // copies it to tensor memory (into the second S buffer, which is not in use
 // yet), and the softmax warps rewrite it in place as the two e4m3 terms.
 //
+// Few query rows (R = 4: at most 32, R = 2: at most 64) are laid R times over
+// the 128 rows of the MMA, and copy r of a row weighs only the r-th part of
+// every tile's keys (its other weights are zeros): the exponentials, which
+// every one of 128 rows would otherwise do for every key, are dealt to all
+// warps, at the price of joining R partial rows at the end.  (P = 30016, S =
+// 10: XX instead of 41 us.)
+//
 // A unit's tiles may be split over any number of CTAs (and its query rows
 // over blocks, so that a CTA writes fewer partial rows): each writes its
 // unnormalised O with {m, l} per row, and merge_kernel, launched behind it,
@@ -89,6 +96,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 
@@ -183,6 +197,7 @@ struct Params {
     const float *k_scale, *v_scale;  // [units, nblk]
     const int32_t *valid_len;
     const uint8_t *mask;
+    __nv_bfloat16 *out;
     float *lse;
     uint32_t *err;
     uint8_t *part;                   // splits > 1: partial rows [units][splits][GS], kPartRow bytes each
@@ -235,12 +250,14 @@ __device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3
 // only what it has read.  Warp w of 16 takes rows [8 w, 8 w + 8), a lane one
 // chunk of one row (conflict-free).  factor[row] becomes the row's scale times
 // `unit`, or NaN for a row with an infinity (NaN elements stay NaN codes).
+// With COPY < 128 the rows lie there 128 / COPY times, COPY rows apart.
+template <int COPY = 128>
 __device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, int warp, float unit, float *factor)
 {
     const int lane = threadIdx.x & 31;
     const int row = warp * 8 + (lane & 7);
-    if (warp * 8 >= n) return;
-    const bool mine = row < n;
+    if ((warp * 8) % COPY >= n) return;
+    const bool mine = row % COPY < n;
     uint8_t *chunk = q + (lane >> 3) * qpitch + row * 128;
     auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + ((u ^ (lane & 7)) << 4)); };
     __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
@@ -280,6 +297,7 @@ __device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, 
     }
 }
 
+template <int R>
 __global__ void __launch_bounds__(kThreads8, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
                 const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ks,
@@ -297,7 +315,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const int unit = cl / p.row_blocks, q0 = (cl - unit * p.row_blocks) * p.qrows;
     const int nr = min(p.qrows, p.GS - q0);  // query rows [q0, q0 + nr) of the unit
     const int b = unit / p.Hkv;
-    const int qpitch = p.qrows * 128;  // bytes of a 64-column chunk of Q
+    constexpr int kCopy = kMRows / R;  // MMA rows of a copy of the query rows
+    const int qpitch = R == 1 ? p.qrows * 128 : kMRows * 128;  // bytes of a 64-column chunk of Q
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(&bars[L::kBarQFull], 1);
@@ -352,8 +371,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
     if (warp == kLoadWarp && lane == 0) {
         pol = ptx::policy_evict_first();
         // rows of the MMA past qrows read whatever lies behind: rows of their own
-        ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(4 * qpitch));
-        ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, q0, 0, unit);
+        ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(R * 4 * p.qrows * 128));
+        if (R == 1) {
+            ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, q0, 0, unit);
+        } else {
+            for (int c = 0; c < 4; ++c)
+                for (int r = 0; r < R; ++r)
+                    ptx::tma_load_4d(smem + c * qpitch + r * kCopy * 128, &tm_q, &bars[L::kBarQFull], 0, q0, c, unit);
+        }
         if (first) {
             ptx::mbar_arrive_expect_tx(&bars[L::kBarKFull], kSlotBytes);
             ptx::tma_load_4d_hint(k_slot(0), &tm_ks, &bars[L::kBarKFull], 0, 0, 0, unit, pol);
@@ -562,8 +587,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
         // reductions run beside the other's exponentials.  Warp w of a group:
         // lane quarter w % 4 (32 query rows), half w / 4 of its tiles' columns.
         const int q4 = warp & 3, hf = (warp >> 2) & 1, grp = warp >> 3;
-        const int c4 = warp >> 2;  // column quarter of Q and of O
+        const int c4 = warp >> 2;  // column quarter of O
         const int row = q4 * 32 + lane;
+        const int copy = row / kCopy, qrow = row % kCopy;
+        const bool row_valid = qrow < nr;
+        constexpr int kCols = 64 / R, kGroups = kCols / 16, kWords = (kCols + 31) / 32;
+        const int col0 = copy * (kTile / R) + hf * kCols;  // this thread's columns of a prefix tile
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
         const float *ksc = p.k_scale + static_cast<size_t>(unit) * p.nblk;
         const float *vsc = p.v_scale + static_cast<size_t>(unit) * p.nblk;
@@ -587,34 +616,35 @@ __global__ void __launch_bounds__(kThreads8, 1)
             failed = !warp_wait(&bars[L::kBarQFull], 0);
             if (!failed && ns > 0) failed = !warp_wait(&bars[L::kBarQFree], 0);
             if (!failed) {
-                split_query_rows(smem, qpitch, nr, warp, p.scale_log2, xl);
+                split_query_rows<kCopy>(smem, qpitch, nr, warp, p.scale_log2, xl);
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(&bars[L::kBarQConv]);
                 failed = !warp_wait(&bars[L::kBarQConv], 0);
-                if (row < nr) sqs = xl[row];
+                if (row_valid) sqs = xl[row];
             }
         }
         float m_l = -INFINITY;  // what this thread's sum refers to
         float l = 0.0f;         // its sum of p, in units of 2^m_l
         // What tile t needs from global memory, one of the group's tiles ahead:
-        // the mask bytes of this lane's two columns, and (lanes 0-3) the scales
-        // of the half's four 16-column groups (a block never ends inside one).
-        uint32_t mask_next[2];
+        // the mask bytes of this lane's columns, and (the first lanes) the scales
+        // of the thread's 16-column groups (a block never ends inside one).
+        uint32_t mask_next[kWords];
         float ks_next, vs_next;
         auto load_next = [&](int t) {
-            mask_next[0] = mask_next[1] = 1u;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) mask_next[w] = 1u;
             ks_next = vs_next = 1.0f;
             if (t < ns || t >= T) return;
             const int r0 = row0_of(t), n = rows_of(t);
             if (mask_row != nullptr) {
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int c = hf * 64 + w * 32 + lane;
-                    if (c < n) mask_next[w] = ptx::load(mask_row + r0 + c);
+                for (int w = 0; w < kWords; ++w) {
+                    const int c = col0 + w * 32 + lane;
+                    if (w * 32 + lane < kCols && c < n) mask_next[w] = ptx::load(mask_row + r0 + c);
                 }
             }
-            const int c = hf * 64 + lane * 16;
-            if (lane < 4 && c < n) {
+            const int c = col0 + lane * 16;
+            if (lane < kGroups && c < n) {
                 ks_next = ptx::load(ksc + ((r0 + c) >> p.shift));
                 vs_next = ptx::load(vsc + ((r0 + c) >> p.shift));
             }
@@ -622,29 +652,31 @@ __global__ void __launch_bounds__(kThreads8, 1)
         load_next(grp);
         for (int t = grp; t < T && !failed; t += 2) {
             const int sb = buffer_of(t, ns), before = uses_before(t, ns);
-            const uint32_t mask_cur[2] = {mask_next[0], mask_next[1]};
+            uint32_t mask_cur[kWords];
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) mask_cur[w] = mask_next[w];
             float ks_cur = ks_next, vs_cur = vs_next;
             load_next(t + 2);
             const int n = rows_of(t);
-            uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
-            float ag[4], bg[4], ig[4];
+            float ag[kGroups], bg[kGroups], ig[kGroups];
             const bool partial = t >= ns && partial_at(t);
             if (t >= ns) {
                 if (partial) {
+                    uint32_t vis[kWords];
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const bool see = hf * 64 + w * 32 + lane < n && mask_cur[w] != 0u;
+                    for (int w = 0; w < kWords; ++w) {
+                        const bool see = w * 32 + lane < kCols && col0 + w * 32 + lane < n && mask_cur[w] != 0u;
                         vis[w] = __ballot_sync(0xffffffffu, see);
                         lim[w * 32 + lane] = see ? INFINITY : -INFINITY;
                     }
                     __syncwarp();
                     // a group without a visible key may have any scale: it gets 1
-                    const uint32_t mine = (lane & 2) ? vis[1] : vis[0];
+                    const uint32_t mine = (lane & 2) ? vis[kWords - 1] : vis[0];
                     if (((lane & 1) ? mine >> 16 : mine & 0xffffu) == 0u) ks_cur = vs_cur = 1.0f;
                 }
                 const float lv = ptx::lg2(vs_cur), iv = 1.0f / vs_cur;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < kGroups; ++g) {
                     ag[g] = __shfl_sync(0xffffffffu, ks_cur, g) * sqs;
                     bg[g] = __shfl_sync(0xffffffffu, lv, g);
                     ig[g] = __shfl_sync(0xffffffffu, iv, g);
@@ -662,57 +694,74 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 break;
             }
             ptx::tc_fence_after_sync();
-            const uint32_t scol = tmem + lane_base + kTmemS8 + sb * kTile + hf * (t < ns ? 32 : 64);
+            const uint32_t sbuf = tmem + lane_base + kTmemS8 + sb * kTile;
+            const uint32_t scol = sbuf + (t < ns ? hf * 32 : col0);
             uint32_t raw[2][16];
             float hmax = -INFINITY;
-            if (t < ns) {
-                ptx::tmem_ld16(scol, raw[0]);
-                ptx::tmem_ld16(scol + 16, raw[1]);
-                ptx::tmem_ld_wait();
+            // the group's largest exponent (rounding is monotone)
+            auto group_max = [&](const uint32_t (&x)[16], int g) {
+                float a = __uint_as_float(x[0]), c = __uint_as_float(x[1]);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    uint32_t &x = raw[c >> 4][c & 15];
-                    if (hf * 32 + c >= n) x = 0xff800000u;
-                    hmax = fmaxf(hmax, __uint_as_float(x));
+                for (int e = 2; e < 14; e += 4) {
+                    a = ptx::max3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    c = ptx::max3(c, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
                 }
-                hmax = fmaf(hmax, p.scale_log2, -kSuffixBits);
-            } else {
+                a = ptx::max3(a, __uint_as_float(x[14]), __uint_as_float(x[15]));
+                return fmaf(fmaxf(a, c), ag[g], bg[g]);
+            };
+            // min(x, -inf) is -inf for any x, NaN included
+            auto hide = [&](uint32_t (&x)[16], int c0) {
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(lim + c0 + c);
+                    x[c] = __float_as_uint(fminf(__uint_as_float(x[c]), f.x));
+                    x[c + 1] = __float_as_uint(fminf(__uint_as_float(x[c + 1]), f.y));
+                    x[c + 2] = __float_as_uint(fminf(__uint_as_float(x[c + 2]), f.z));
+                    x[c + 3] = __float_as_uint(fminf(__uint_as_float(x[c + 3]), f.w));
+                }
+            };
+            if (t < ns) {
+                // suffix keys are the first copy's
+                if (R == 1 || copy == 0) {
+                    ptx::tmem_ld16(scol, raw[0]);
+                    ptx::tmem_ld16(scol + 16, raw[1]);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        uint32_t &x = raw[c >> 4][c & 15];
+                        if (hf * 32 + c >= n) x = 0xff800000u;
+                        hmax = fmaxf(hmax, __uint_as_float(x));
+                    }
+                    hmax = fmaf(hmax, p.scale_log2, -kSuffixBits);
+                }
+            } else if (R == 1) {
+                // 64 columns, 32 at a time: read again below (registers); hidden
+                // ones are hidden in tensor memory too
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     ptx::tmem_ld16(scol + w * 32, raw[0]);
                     ptx::tmem_ld16(scol + w * 32 + 16, raw[1]);
                     ptx::tmem_ld_wait();
                     if (partial) {
-                        // min(x, -inf) is -inf for any x, NaN included
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(lim + w * 32 + c);
-                            const float fe[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t &x = raw[(c + e) >> 4][(c + e) & 15];
-                                x = __float_as_uint(fminf(__uint_as_float(x), fe[e]));
-                            }
-                        }
+                        hide(raw[0], w * 32);
+                        hide(raw[1], w * 32 + 16);
                         ptx::tmem_st16(scol + w * 32, raw[0]);
                         ptx::tmem_st16(scol + w * 32 + 16, raw[1]);
                     }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float a = __uint_as_float(raw[g][0]), c = __uint_as_float(raw[g][1]);
-#pragma unroll
-                        for (int e = 2; e < 14; e += 4) {
-                            a = ptx::max3(a, __uint_as_float(raw[g][e]), __uint_as_float(raw[g][e + 1]));
-                            c = ptx::max3(c, __uint_as_float(raw[g][e + 2]), __uint_as_float(raw[g][e + 3]));
-                        }
-                        a = ptx::max3(a, __uint_as_float(raw[g][14]), __uint_as_float(raw[g][15]));
-                        // rounding is monotone: this is the largest of the group's exponents
-                        hmax = fmaxf(hmax, fmaf(fmaxf(a, c), ag[w * 2 + g], bg[w * 2 + g]));
-                    }
+                    hmax = fmaxf(hmax, fmaxf(group_max(raw[0], (w * 2) % kGroups), group_max(raw[1], (w * 2 + 1) % kGroups)));
                 }
                 if (partial) ptx::tmem_st_wait();
+            } else {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) ptx::tmem_ld16(scol + g * 16, raw[g % 2]);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    if (partial) hide(raw[g % 2], g * 16);
+                    hmax = fmaxf(hmax, group_max(raw[g % 2], g));
+                }
             }
-            if (row >= nr) hmax = -INFINITY;  // not a query row: never a reason to rescale
+            if (!row_valid) hmax = -INFINITY;  // not a query row: never a reason to rescale
             xmax[hf * kMRows + row] = hmax;
             if (!pair_sync()) {
                 failed = true;
@@ -733,7 +782,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             // weights of this tile are 2^(z + log2 vs - m_used)
             const bool grow = t == 0 || tmax > m_old + kMaxBits;
             const float m_used = grow ? tmax - kTopBits : m_old;
-            const bool rescale = grow && t > 0;
+            const bool rescale = grow && m_old != -INFINITY;  // (before any weight O is zero)
             if (hf == 0) mref[(t & 1) * kMRows + row] = m_used;
             ptx::mbar_arrive(max_bar);
             if (m_l != m_used) {
@@ -741,51 +790,81 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 m_l = m_used;
             }
             const float msub = m_used == -INFINITY ? 0.0f : m_used;
-            if (t < ns) {
-                const uint64_t a2 = ptx::f32x2(p.scale_log2, p.scale_log2), c2 = ptx::f32x2(-msub, -msub);
+            // a group's weights: their sum without the scale, and two terms each
+            auto weigh = [&](const uint32_t (&x)[16], int g, uint32_t *hi, uint32_t *lo) {
+                const float cg = bg[g] - msub;
+                const uint64_t a2 = ptx::f32x2(ag[g], ag[g]), c2 = ptx::f32x2(cg, cg);
                 uint64_t l2 = ptx::f32x2(0.0f, 0.0f);
-                uint32_t pk[16];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
-                        ptx::f32x2(__uint_as_float(raw[c >> 4][c & 15]), __uint_as_float(raw[c >> 4][(c & 15) + 1])), a2, c2));
-                    const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
-                    pk[c >> 1] = pack_bf16x2(p0, p1);
-                    l2 = ptx::add_f32x2(l2, ptx::f32x2(p0, p1));
+                for (int e = 0; e < 16; e += 4) {
+                    const float2 u = ptx::unpack_f32x2(ptx::fma_f32x2(
+                        ptx::f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), a2, c2));
+                    const float2 v = ptx::unpack_f32x2(ptx::fma_f32x2(
+                        ptx::f32x2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), a2, c2));
+                    const float w0 = ptx::ex2(u.x), w1 = ptx::ex2(u.y), w2 = ptx::ex2(v.x), w3 = ptx::ex2(v.y);
+                    l2 = ptx::add_f32x2(l2, ptx::f32x2(w0, w1));
+                    l2 = ptx::add_f32x2(l2, ptx::f32x2(w2, w3));
+                    two_terms(w0, w1, w2, w3, hi[e >> 2], lo[e >> 2]);
                 }
                 const float2 lp = ptx::unpack_f32x2(l2);
-                l += lp.x + lp.y;
+                l = fmaf(lp.x + lp.y, ig[g], l);
+            };
+            if (t < ns) {
+                uint32_t pk[16];
+                if (R == 1 || copy == 0) {
+                    const uint64_t a2 = ptx::f32x2(p.scale_log2, p.scale_log2), c2 = ptx::f32x2(-msub, -msub);
+                    uint64_t l2 = ptx::f32x2(0.0f, 0.0f);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
+                            ptx::f32x2(__uint_as_float(raw[c >> 4][c & 15]), __uint_as_float(raw[c >> 4][(c & 15) + 1])), a2, c2));
+                        const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
+                        pk[c >> 1] = pack_bf16x2(p0, p1);
+                        l2 = ptx::add_f32x2(l2, ptx::f32x2(p0, p1));
+                    }
+                    const float2 lp = ptx::unpack_f32x2(l2);
+                    l += lp.x + lp.y;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) pk[c] = 0u;
+                }
                 ptx::tmem_st16(scol, pk);
-            } else {
+            } else if (R == 1) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     ptx::tmem_ld16(scol + w * 32, raw[0]);
                     ptx::tmem_ld16(scol + w * 32 + 16, raw[1]);
                     ptx::tmem_ld_wait();
                     uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float cg = bg[w * 2 + g] - msub;
-                        const uint64_t a2 = ptx::f32x2(ag[w * 2 + g], ag[w * 2 + g]), c2 = ptx::f32x2(cg, cg);
-                        uint64_t l2 = ptx::f32x2(0.0f, 0.0f);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
-                                ptx::f32x2(__uint_as_float(raw[g][e]), __uint_as_float(raw[g][e + 1])), a2, c2));
-                            const float2 y = ptx::unpack_f32x2(ptx::fma_f32x2(
-                                ptx::f32x2(__uint_as_float(raw[g][e + 2]), __uint_as_float(raw[g][e + 3])), a2, c2));
-                            const float w0 = ptx::ex2(x.x), w1 = ptx::ex2(x.y), w2 = ptx::ex2(y.x), w3 = ptx::ex2(y.y);
-                            l2 = ptx::add_f32x2(l2, ptx::f32x2(w0, w1));
-                            l2 = ptx::add_f32x2(l2, ptx::f32x2(w2, w3));
-                            two_terms(w0, w1, w2, w3, hi[g * 4 + (e >> 2)], lo[g * 4 + (e >> 2)]);
-                        }
-                        const float2 lp = ptx::unpack_f32x2(l2);
-                        l = fmaf(lp.x + lp.y, ig[w * 2 + g], l);  // the weights without their scale
-                    }
+                    weigh(raw[0], (w * 2) % kGroups, hi, lo);
+                    weigh(raw[1], (w * 2 + 1) % kGroups, hi + 4, lo + 4);
                     // in the first 16 columns of the half for its first 32 keys, then
                     // the next 16: where only this warp's own logits were
                     ptx::tmem_st8(scol + w * 16, hi);
                     ptx::tmem_st8(scol + w * 16 + 8, lo);
+                }
+            } else {
+                // Both halves hold their logits in registers by now.  A 32-key step
+                // kk has its weights in 16 columns of its own; the other copies'
+                // steps are zero in these rows.
+                const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                auto step = [&](int kk) { return sbuf + (kk >> 1) * 64 + (kk & 1) * 16; };
+                const int kk = col0 >> 5;
+                uint32_t hi[8], lo[8];
+                weigh(raw[0], 0, hi, lo);
+                if (R == 2) {
+                    weigh(raw[1], kGroups - 1, hi + 4, lo + 4);
+                    ptx::tmem_st8(step(kk), hi);
+                    ptx::tmem_st8(step(kk) + 8, lo);
+                    ptx::tmem_st8(step(kk ^ 2), zero);
+                    ptx::tmem_st8(step(kk ^ 2) + 8, zero);
+                } else {
+                    ptx::tmem_st4(step(kk) + hf * 4, hi);
+                    ptx::tmem_st4(step(kk) + 8 + hf * 4, lo);
+                    const int k1 = (kk + 1 + hf) & 3;
+                    ptx::tmem_st8(step(k1), zero);
+                    ptx::tmem_st8(step(k1) + 8, zero);
+                    ptx::tmem_st8(step((kk + 3) & 3) + hf * 8, zero);
                 }
             }
             if (__any_sync(0xffffffffu, rescale)) {
@@ -836,8 +915,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
         xl[c4 * kMRows + row] = l;
         if (!failed && !row_sync()) failed = true;
         const float l_row = (xl[row] + xl[kMRows + row]) + (xl[2 * kMRows + row] + xl[3 * kMRows + row]);
-        const bool row_valid = row < nr;
         const float inv_l = 1.0f / l_row;
+        const int srow = R == 1 ? row : copy * nr + qrow;  // staged row
         // The rows leave through shared memory in one copy: bf16 rows in the
         // layout of a Q tile, partial rows as they lie in the workspace.
         // (16-byte stores of 32 rows at a time took 5k cycles a CTA, one bulk
@@ -851,7 +930,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 ptx::tmem_ld16(oc + 16, o[1]);
                 ptx::tmem_ld_wait();
                 if (!row_valid) continue;
-                if (C == 1) {
+                if (R == 1 && C == 1) {
                     uint8_t *dst = smem + c4 * qpitch + row * 128;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -864,7 +943,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(smem + row * kPartRow + (c4 * (kHeadDim / 4) + j * 32) * 4);
+                    uint4 *dst = reinterpret_cast<uint4 *>(smem + srow * kPartRow + (c4 * (kHeadDim / 4) + j * 32) * 4);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e] = make_uint4(o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1], o[e >> 2][4 * (e & 3) + 2],
@@ -873,15 +952,54 @@ __global__ void __launch_bounds__(kThreads8, 1)
             }
         }
         if (c4 == 0 && row_valid) {
-            if (C > 1)
-                *reinterpret_cast<float4 *>(smem + row * kPartRow + kHeadDim * 4) =
+            if (R > 1 || C > 1)
+                *reinterpret_cast<float4 *>(smem + srow * kPartRow + kHeadDim * 4) =
                     make_float4(m_end, have_o && !failed ? l_row : 0.0f, 0.0f, 0.0f);
             else if (p.lse != nullptr && !failed)
                 p.lse[static_cast<size_t>(unit) * p.GS + q0 + row] = (m_end + ptx::lg2(l_row)) * 0.69314718055994531f;
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(&bars[L::kBarOut]);
-        if (threadIdx.x == 0 && !failed) {
+        if (R > 1) {
+            // the copies of a row joined as the splits are, 64 threads a row
+            if (!failed && !warp_wait(&bars[L::kBarOut], 0)) failed = true;
+            if (!failed) {
+                const int col4 = threadIdx.x & 63;
+                for (int r = threadIdx.x >> 6; r < nr; r += kSoftWarps / 2) {
+                    float2 st[R];
+                    float M = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < R; ++c) {
+                        st[c] = *reinterpret_cast<const float2 *>(smem + (c * nr + r) * kPartRow + kHeadDim * 4);
+                        if (st[c].y != 0.0f) M = fmaxf(M, st[c].x);
+                    }
+                    float total = 0.0f;
+                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int c = 0; c < R; ++c) {
+                        const float w = st[c].y != 0.0f ? ptx::ex2(st[c].x - M) : 0.0f;
+                        const float4 v = *reinterpret_cast<const float4 *>(smem + (c * nr + r) * kPartRow + col4 * 16);
+                        const bool use = w != 0.0f;
+                        total = fmaf(w, st[c].y, total);
+                        acc.x = fmaf(w, use ? v.x : 0.0f, acc.x);
+                        acc.y = fmaf(w, use ? v.y : 0.0f, acc.y);
+                        acc.z = fmaf(w, use ? v.z : 0.0f, acc.z);
+                        acc.w = fmaf(w, use ? v.w : 0.0f, acc.w);
+                    }
+                    if (C == 1) {
+                        const size_t o = static_cast<size_t>(unit) * p.GS + q0 + r;
+                        const float inv = 1.0f / total;
+                        *reinterpret_cast<uint2 *>(p.out + o * kHeadDim + col4 * 4) =
+                            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                        if (col4 == 0 && p.lse != nullptr) p.lse[o] = (M + ptx::lg2(total)) * 0.69314718055994531f;
+                    } else {
+                        uint8_t *dst = p.part + ((static_cast<size_t>(unit) * C + rank) * p.GS + q0 + r) * kPartRow;
+                        *reinterpret_cast<float4 *>(dst + col4 * 16) = acc;
+                        if (col4 == 0) *reinterpret_cast<float4 *>(dst + kHeadDim * 4) = make_float4(M, total, 0.0f, 0.0f);
+                    }
+                }
+            }
+        } else if (threadIdx.x == 0 && !failed) {
             if (ptx::mbar_wait(&bars[L::kBarOut], 0, kWaitLimitNs)) {
                 if (C == 1)
                     ptx::tma_store_4d(&tm_out, smem, 0, q0, 0, unit);

@@ -85,7 +85,9 @@ int set_attributes(const Device &dev, bool mass) noexcept
                  cudaFuncSetAttribute(&dm05::mass::mass_kernel<true>, kSmem, dm05::mass::Smem<true>::kAllocBytes) ==
                      cudaSuccess;
         else
-            ok = cudaFuncSetAttribute(&dm05::kv8::attn_kernel, kSmem, dm05::kv8::Smem::kAllocBytes) == cudaSuccess;
+            ok = cudaFuncSetAttribute(&dm05::kv8::attn_kernel<1>, kSmem, dm05::kv8::Smem::kAllocBytes) == cudaSuccess &&
+                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<2>, kSmem, dm05::kv8::Smem::kAllocBytes) == cudaSuccess &&
+                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<4>, kSmem, dm05::kv8::Smem::kAllocBytes) == cudaSuccess;
         if (!ok) return DM05_ERR_CUDA;
         ready = true;
         return DM05_OK;
@@ -98,6 +100,7 @@ struct Kv8Plan {
     int splits = 1;      // CTAs per (sample, KV head) and block of query rows
     int row_blocks = 1;  // blocks of the GS query rows
     int qrows = 8;       // rows of a block (a multiple of 8)
+    int copies = 1;      // how often a block's rows are laid over the MMA's 128
     size_t bytes = 0;    // partial results
 };
 
@@ -125,6 +128,7 @@ Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
         blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(GS / 32, dev.num_sms / (units * pl.splits))));
     pl.qrows = ((GS + blocks - 1) / blocks + 7) / 8 * 8;
     pl.row_blocks = (GS + pl.qrows - 1) / pl.qrows;
+    pl.copies = pl.qrows <= 32 ? 4 : pl.qrows <= 64 ? 2 : 1;
     if (pl.splits > 1) pl.bytes = static_cast<size_t>(units) * pl.splits * GS * dm05::kv8::kPartRow;
     return pl;
 }
@@ -137,13 +141,13 @@ int kv8_check(int B, int Hq, int Hkv, int P, int S, int D)
     return DM05_OK;
 }
 
-// bf16 [units][rows][256] in boxes of box_rows rows: four 64-column chunks
-// of 128 swizzled bytes
-int encode_rows16(CUtensorMap *map, const void *base, int rows, int units, int box_rows)
+// bf16 [units][rows][256] in boxes of box_rows rows: box_chunks 64-column
+// chunks of 128 swizzled bytes
+int encode_rows16(CUtensorMap *map, const void *base, int rows, int units, int box_rows, int box_chunks = 4)
 {
     const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), 4, static_cast<cuuint64_t>(units)};
     const cuuint64_t strides[3] = {512, 128, static_cast<cuuint64_t>(rows) * 512};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 4, 1};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_chunks), 1};
     return dm05::internal::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box);
 }
 
@@ -353,7 +357,7 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     const long long grid = static_cast<long long>(units) * pl.row_blocks * pl.splits;
     if (grid > 0x7fffffffLL) return DM05_ERR_SHAPE;
     CUtensorMap tq, tkp, tvp, tks, tvs, to;
-    if (encode_rows16(&tq, q, GS, units, pl.qrows) != DM05_OK || encode_rows16(&to, out, GS, units, pl.qrows) != DM05_OK ||
+    if (encode_rows16(&tq, q, GS, units, pl.qrows, pl.copies == 1 ? 4 : 1) != DM05_OK || encode_rows16(&to, out, GS, units, pl.qrows) != DM05_OK ||
         encode_rows16(&tks, k_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK ||
         encode_rows16(&tvs, v_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK)
         return DM05_ERR_CUDA;
@@ -370,6 +374,7 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     ap.v_scale = v_scale;
     ap.valid_len = prefix_valid_len;
     ap.mask = prefix_mask;
+    ap.out = static_cast<__nv_bfloat16 *>(out);
     ap.lse = lse;
     ap.err = dev.err;
     ap.part = static_cast<uint8_t *>(workspace);
@@ -393,8 +398,10 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, &dm05::kv8::attn_kernel, tq, tkp, tvp, tks, tvs, to, ap) != cudaSuccess)
-        return DM05_ERR_CUDA;
+    auto *kernel = pl.copies == 4   ? &dm05::kv8::attn_kernel<4>
+                   : pl.copies == 2 ? &dm05::kv8::attn_kernel<2>
+                                    : &dm05::kv8::attn_kernel<1>;
+    if (cudaLaunchKernelEx(&cfg, kernel, tq, tkp, tvp, tks, tvs, to, ap) != cudaSuccess) return DM05_ERR_CUDA;
     if (pl.splits == 1) return DM05_OK;
     dm05::kv8::MergeParams mp = {};
     mp.part = ap.part;
