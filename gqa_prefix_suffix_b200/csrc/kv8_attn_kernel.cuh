@@ -43,7 +43,7 @@
 // every tile's keys (its other weights are zeros): the exponentials, which
 // every one of 128 rows would otherwise do for every key, are dealt to all
 // warps, at the price of joining R partial rows at the end.  (P = 30016, S =
-// 10: XX instead of 41 us.)
+// 10: 38 instead of 42 us; with runs under four tiles the joining costs more.)
 //
 // A unit's tiles may be split over any number of CTAs (and its query rows
 // over blocks, so that a CTA writes fewer partial rows): each writes its
@@ -250,14 +250,14 @@ __device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3
 // only what it has read.  Warp w of 16 takes rows [8 w, 8 w + 8), a lane one
 // chunk of one row (conflict-free).  factor[row] becomes the row's scale times
 // `unit`, or NaN for a row with an infinity (NaN elements stay NaN codes).
-// With COPY < 128 the rows lie there 128 / COPY times, COPY rows apart.
+// With COPY < 128 the result is written 128 / COPY times, COPY rows apart.
 template <int COPY = 128>
 __device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, int warp, float unit, float *factor)
 {
     const int lane = threadIdx.x & 31;
     const int row = warp * 8 + (lane & 7);
-    if ((warp * 8) % COPY >= n) return;
-    const bool mine = row % COPY < n;
+    if (warp * 8 >= n) return;
+    const bool mine = row < n;
     uint8_t *chunk = q + (lane >> 3) * qpitch + row * 128;
     auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + ((u ^ (lane & 7)) << 4)); };
     __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
@@ -275,7 +275,10 @@ __device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, 
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
     const float s = amax < INFINITY ? cache::pow2_scale(amax) : 1.0f;
     if (!mine) return;
-    if (lane < 8) factor[row] = amax < INFINITY ? s * unit : __int_as_float(0x7fffffff);
+    if (lane < 8) {
+#pragma unroll
+        for (int c = 0; c < 128; c += COPY) factor[c + row] = amax < INFINITY ? s * unit : __int_as_float(0x7fffffff);
+    }
     const float inv = cache::pow2_inverse(s);
 #pragma unroll 1
     for (int g = 0; g < 2; ++g) {
@@ -290,10 +293,13 @@ __device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, 
             two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
                       __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
         }
-        *unit16(g * 4) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *unit16(g * 4 + 1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-        *unit16(g * 4 + 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *unit16(g * 4 + 3) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+#pragma unroll
+        for (int c = 0; c < 128; c += COPY) {
+            unit16(g * 4)[c * 8] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            unit16(g * 4 + 1)[c * 8] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+            unit16(g * 4 + 2)[c * 8] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            unit16(g * 4 + 3)[c * 8] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+        }
     }
 }
 
@@ -371,13 +377,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
     if (warp == kLoadWarp && lane == 0) {
         pol = ptx::policy_evict_first();
         // rows of the MMA past qrows read whatever lies behind: rows of their own
-        ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(R * 4 * p.qrows * 128));
+        ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(4 * p.qrows * 128));
         if (R == 1) {
             ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, q0, 0, unit);
         } else {
-            for (int c = 0; c < 4; ++c)
-                for (int r = 0; r < R; ++r)
-                    ptx::tma_load_4d(smem + c * qpitch + r * kCopy * 128, &tm_q, &bars[L::kBarQFull], 0, q0, c, unit);
+            for (int c = 0; c < 4; ++c) ptx::tma_load_4d(smem + c * qpitch, &tm_q, &bars[L::kBarQFull], 0, q0, c, unit);
         }
         if (first) {
             ptx::mbar_arrive_expect_tx(&bars[L::kBarKFull], kSlotBytes);
@@ -1035,11 +1039,12 @@ struct MergeParams {
 // Joins the partial rows of a split call, two warps a row: with
 // M = max_c m_c and w_c = 2^(m_c - M), out = sum_c w_c O_c / sum_c w_c l_c and
 // lse = (M + log2 sum_c w_c l_c) ln 2.  A partial without keys (l = 0) has no
-// weight, whatever its O holds.  Latency is all there is: the first eight
-// partials are requested before their weights are known.
+// weight, whatever its O holds.  Latency is all there is: the first AHEAD
+// partials are requested before their weights are known (8 for few of them:
+// 16 cost one token's call 0.3 us; 16 for more: 1.5 us less at 18 partials).
+template <int AHEAD>
 __global__ void __launch_bounds__(256) merge_kernel(const MergeParams p)
 {
-    constexpr int kAhead = 8;
     ptx::griddep_launch_dependents();
     const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 31, col4 = threadIdx.x & 63;
     if (r >= p.rows) return;
@@ -1047,9 +1052,9 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeParams p)
     const uint8_t *base = p.part + (static_cast<size_t>(unit) * p.splits * p.GS + row) * kPartRow;
     const size_t step = static_cast<size_t>(p.GS) * kPartRow;
     ptx::griddep_wait();
-    float4 o[kAhead];
+    float4 o[AHEAD];
 #pragma unroll
-    for (int c = 0; c < kAhead; ++c)
+    for (int c = 0; c < AHEAD; ++c)
         if (c < p.splits) o[c] = *reinterpret_cast<const float4 *>(base + c * step + col4 * 16);
     float m[2], l[2], M = -INFINITY;
 #pragma unroll
@@ -1081,10 +1086,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeParams p)
         acc.w = fmaf(wc, use ? v.w : 0.0f, acc.w);
     };
 #pragma unroll
-    for (int c = 0; c < kAhead; ++c)
+    for (int c = 0; c < AHEAD; ++c)
         if (c < p.splits) add(c, o[c]);
 #pragma unroll 4
-    for (int c = kAhead; c < p.splits; ++c) add(c, *reinterpret_cast<const float4 *>(base + c * step + col4 * 16));
+    for (int c = AHEAD; c < p.splits; ++c) add(c, *reinterpret_cast<const float4 *>(base + c * step + col4 * 16));
     const float inv = 1.0f / total;
     *reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(r) * kHeadDim + col4 * 4) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));

@@ -107,8 +107,9 @@ struct Kv8Plan {
 // The fewest CTAs per (sample, KV head) that make the longest run of tiles as
 // short as one wave allows; unsplit while that is as short.  A split unit's
 // query rows are cut into blocks while SMs are left (at least 32 rows each):
-// every CTA then splits, stages and writes fewer rows, which at B = 1, P =
-// 1024, S = 50 is half its time, for K and V tiles read from L2 once more.
+// every CTA then prepares, stages and writes fewer rows, for K and V tiles read
+// from L2 once more (B = 1, P = 1024, S = 50: 12.7 instead of 13.3 us).  Few
+// rows are copied over the MMA's when a CTA walks at least four tiles.
 Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
 {
     const long long units = static_cast<long long>(B) * Hkv;
@@ -120,15 +121,16 @@ Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
     if (dev.split_override > 0) {
         pl.splits = dev.split_override;
     } else {
-        const int run = (tiles + most - 1) / most;
-        pl.splits = (tiles + run - 1) / run;
+        const int longest = (tiles + most - 1) / most;
+        pl.splits = (tiles + longest - 1) / longest;
     }
     int blocks = 1;
     if (pl.splits > 1)
         blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(GS / 32, dev.num_sms / (units * pl.splits))));
     pl.qrows = ((GS + blocks - 1) / blocks + 7) / 8 * 8;
     pl.row_blocks = (GS + pl.qrows - 1) / pl.qrows;
-    pl.copies = pl.qrows <= 32 ? 4 : pl.qrows <= 64 ? 2 : 1;
+    const int run = (tiles + pl.splits - 1) / pl.splits;
+    pl.copies = run < 4 ? 1 : pl.qrows <= 32 ? 4 : pl.qrows <= 64 ? 2 : 1;
     if (pl.splits > 1) pl.bytes = static_cast<size_t>(units) * pl.splits * GS * dm05::kv8::kPartRow;
     return pl;
 }
@@ -410,7 +412,9 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     mp.rows = units * GS;
     mp.GS = GS;
     mp.splits = pl.splits;
-    return launch(dm05::kv8::merge_kernel, dim3(static_cast<unsigned>((mp.rows + 3) / 4)), 256, 0, stream, mp);
+    const dim3 blocks(static_cast<unsigned>((mp.rows + 3) / 4));
+    return pl.splits <= 8 ? launch(dm05::kv8::merge_kernel<8>, blocks, 256, 0, stream, mp)
+                          : launch(dm05::kv8::merge_kernel<16>, blocks, 256, 0, stream, mp);
 }
 
 int dm05_prefix_attn_mass(const void *q, const void *k_prefix, const int32_t *prefix_valid_len,
