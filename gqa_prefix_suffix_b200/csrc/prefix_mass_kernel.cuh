@@ -202,6 +202,9 @@ __global__ void __launch_bounds__(kThreadsM, 1)
             } else if (c4 == 0) {
                 factors[row] = p.scale;
             }
+            // the MMA's columns behind the last query row hold zeros; their factor
+            // must be a number too
+            if (KV8 && c4 == 0 && row >= p.GS) factors[row] = 0.0f;
             if (c4 == 1) {
                 // rows that do not exist, and rows that saw no key (-inf), add e^-inf
                 float l = INFINITY;

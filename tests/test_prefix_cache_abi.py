@@ -66,6 +66,13 @@ def test_attention_plan_refuses():
     assert bd.dm05_suffix_attn_kv8_plan(1, 6, 4, 1024, 50, 256)[0] == bd.DM05_ERR_SHAPE
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="for a machine without a GPU")
+def test_valid_calls_without_a_gpu_return_an_error():
+    assert bd.dm05_suffix_attn_kv8_plan(1, 8, 4, 1024, 50, 256)[0] == bd.DM05_ERR_CUDA
+    assert _call(bd.dm05_kv8_quantize, QUANT, QUANT_D, {}) == bd.DM05_ERR_CUDA
+    assert _call(bd.dm05_suffix_attn_kv8, ATTN, ATTN_D, {}) == bd.DM05_ERR_CUDA
+
+
 MASS = "q k valid_len mask lse mass_in mass B Hq Hkv P S D stream".split()
 MASS_D = dict(q=F, k=F, valid_len=None, mask=None, lse=F, mass_in=None, mass=F, B=1, Hq=8, Hkv=4, P=1024, S=50, D=256,
               stream=None)

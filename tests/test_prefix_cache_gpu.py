@@ -296,6 +296,125 @@ def test_attention_outputs_only_and_clamp_flag():
     assert torch.equal(none, empty)
 
 
+@pytest.mark.parametrize("S,splits", [(1, 1), (4, 2), (10, 1), (16, 2), (17, 1), (32, 1), (32, 2), (33, 1), (50, 2), (60, 2)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_attention_few_and_many_rows_on_long_runs(S, splits, masked):
+    """Query rows laid once, twice and four times over the MMA's rows, and in blocks: every CTA walks several tiles."""
+    g = gen(S * 8 + splits)
+    mask = (torch.rand(2, 900, generator=g) >= 0.2).to(torch.uint8) if masked else None
+    if masked:
+        mask[0, 128:300] = 0                               # a whole tile hidden
+        mask[1] = 0
+    try:
+        assert bd.dm05_set_split_override(splits) == 0
+        check_attention(g, 2, 8, 4, 900, S, 32, [900, 130], mask)
+        c = make_cache(g, 1, 2, 1030, 16, spread=0.0)      # growing logits, one head a group
+        c.k_scale.mul_(torch.linspace(0.25, 24.0, 65)[None, None])
+        check_attention(g, 1, 2, 2, 1030, S, 16, c=c)
+        c.k_scale.copy_(c.k_scale.flip(2).contiguous())
+        c.v_scale[:, :, ::3] = 2.0 ** -30
+        check_attention(g, 1, 2, 2, 1030, S, 16, [1021], c=c)
+    finally:
+        bd.dm05_set_split_override(0)
+
+
+@pytest.mark.parametrize("S", [9, 20, 50])
+def test_attention_rows_do_not_touch_each_other(S):
+    """A query row of NaN or infinity spoils its own output only."""
+    g = gen(S)
+    c = make_cache(g, 1, 4, 900, 16)
+    q = rand(g, 1, 8, S, 256).to(BF)
+    ks, vs = rand(g, 1, 4, S, 256).to(BF), rand(g, 1, 4, S, 256).to(BF)
+    bad = q.clone()
+    bad[0, 1, 3, 100], bad[0, 6, 7] = float("nan"), float("inf")
+    keep = torch.ones(8, S, dtype=torch.bool)
+    keep[1, 3] = keep[6, 7] = False
+    out, lse = bd.suffix_attn_kv8(bad.cuda(), on_gpu(c), ks.cuda(), vs.cuda())
+    k, v = (ref.dequant(x.to(F64), s.to(F64), 16) for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+    step = c.v_scale.to(F64).repeat_interleave(16, dim=2)[:, :, :900]
+    o, l, tol, tol_l = ref.attention(q.to(F64), k, v, ks.to(F64), vs.to(F64), torch.ones(1, 900, dtype=torch.bool), step)
+    assert (out[0].cpu().to(F64) - o[0]).abs()[keep].le(tol[0][keep]).all()
+    assert (lse[0].cpu().to(F64) - l[0]).abs()[keep].le(tol_l[0][keep]).all()
+    assert torch.isnan(out[0].cpu()[~keep].float()).all()
+
+
+def test_attention_workspace_of_the_caller():
+    g = gen(19)
+    c = on_gpu(make_cache(g, 1, 4, 1000, 64))
+    q, ks = rand(g, 1, 8, 50, 256).to(BF).cuda(), rand(g, 1, 4, 50, 256).to(BF).cuda()
+    rc, splits, rows, nbytes = bd.dm05_suffix_attn_kv8_plan(1, 8, 4, 1000, 50, 256)
+    assert rc == 0 and splits > 1 and rows == 128 and nbytes > 0
+    want = bd.suffix_attn_kv8(q, c, ks, ks)
+    ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = bd.suffix_attn_kv8(q, c, ks, ks, workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(bd.Dm05Error):
+        bd.suffix_attn_kv8(q, c, ks, ks, workspace=ws[:-16])
+
+
+def test_many_heads_of_one_row():
+    """B * Hkv at its limit, and a batch whose heads fill several waves."""
+    g = gen(20)
+    B = 65535
+    c = make_cache(g, B, 1, 1, 16)
+    q, ks, vs = (rand(g, B, 1, 1, 256).to(BF) for _ in range(3))
+    at = torch.tensor([0, 1, 147, 148, 32768, 65534])
+    out, lse = bd.suffix_attn_kv8(q.cuda(), on_gpu(c), ks.cuda(), vs.cuda())
+    m = bd.prefix_attn_mass_kv8(q.cuda(), c.k.cuda(), c.k_scale.cuda(), 16, lse)
+    k, v = (ref.dequant(x[at].to(F64), s[at].to(F64), 16) for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+    vis = torch.ones(len(at), 1, dtype=torch.bool)
+    o, l, tol, tol_l = ref.attention(q[at].to(F64), k, v, ks[at].to(F64), vs[at].to(F64), vis, c.v_scale[at].to(F64))
+    assert ((out.cpu()[at].to(F64) - o).abs() <= tol).all() and ((lse.cpu()[at].to(F64) - l).abs() <= tol_l).all()
+    want, tol = ref.mass(q[at].to(F64), k, lse.cpu()[at], vis, None)
+    assert ((m.cpu()[at].to(F64) - want).abs() <= tol).all()
+    e = bd.prefix_evict_kv8(on_gpu(c), m, 1)
+    assert torch.equal(e.mass, m) and (e.positions == 0).all() and (e.valid_len == 1).all()
+    assert same(e.cache.k.float() * e.cache.k_scale[..., None], c.k.float() * c.k_scale[..., None])
+    x = c.k.float().to(BF).cuda()
+    assert same(bd.kv8_quantize(x, x, 16).k.float()[65534], ref.quantize(
+        x[65534:].cpu().to(F64), None, 16, 0, torch.zeros(1, 1, 1, 256, dtype=F64), torch.ones(1, 1, 1, dtype=F64))[0][0])
+    check_attention(g, 40, 8, 4, 140, 10, 16)              # 160 heads: more than one wave
+
+
+def test_offsets_past_32_bits():
+    """Caches whose last rows lie past 2^31 codes and 2^32 bytes."""
+    g = gen(25)
+    B, H, P, S, n = 2, 4, 1_200_000, 10, 320               # P is a multiple of the block, the last n rows are seen
+    tail = rand(g, 2, 1, H, n, 256).to(BF)
+    k, v = (torch.zeros(B, H, P, 256, dtype=BF, device="cuda") for _ in range(2))
+    k[1, :, -n:], v[1, :, -n:] = tail[0, 0].cuda(), tail[1, 0].cuda()
+    mask = torch.zeros(B, P, dtype=torch.uint8, device="cuda")
+    mask[1, -n:] = 1
+    mask[0, :5] = 1
+    c = bd.kv8_quantize(k, v, 64)
+    small = bd.kv8_quantize(tail[0].cuda(), tail[1].cuda(), 64)
+    for a, b in zip(c[:4], small[:4]):
+        assert torch.equal(a[1:, :, -b.shape[2]:].view(torch.uint8), b.view(torch.uint8))
+    q, ks, vs = rand(g, B, 8, S, 256).to(BF), rand(g, B, H, S, 256).to(BF), rand(g, B, H, S, 256).to(BF)
+    out, lse = bd.suffix_attn_kv8(q.cuda(), c, ks.cuda(), vs.cuda(), prefix_mask=mask)
+    kd, vd = (ref.dequant(x.cpu().to(F64), s.cpu().to(F64), 64) for x, s in ((small.k, small.k_scale), (small.v, small.v_scale)))
+    vis = torch.ones(1, n, dtype=torch.bool)
+    d = lambda t: t[1:].cpu().to(F64)  # noqa: E731
+    o, l, tol, tol_l = ref.attention(d(q), kd, vd, d(ks), d(vs), vis,
+                                     small.v_scale.cpu().to(F64).repeat_interleave(64, dim=2))
+    assert ((d(out) - o).abs() <= tol).all() and ((d(lse) - l).abs() <= tol_l).all()
+    for m, keys in ((bd.prefix_attn_mass_kv8(q.cuda(), c.k, c.k_scale, 64, lse, prefix_mask=mask), kd),
+                    (bd.prefix_attn_mass(q.cuda(), k, lse, prefix_mask=mask), tail[0].to(F64))):
+        want, tol = ref.mass(d(q), keys, lse[1:].cpu(), vis, None)
+        assert ((d(m)[:, :, -n:] - want).abs() <= tol).all()
+        assert (m[1, :, :-n] == 0).all() and (m[0, :, 5:] == 0).all()
+    e = bd.prefix_evict(k, v, m, 100, prefix_mask=mask)
+    e8 = bd.prefix_evict_kv8(c, m, 100, prefix_mask=mask)
+    assert e.valid_len.tolist() == [5, 100] and torch.equal(e8.positions, e.positions)
+    for h in range(H):
+        order = ref.evict_order(m[1, h, -n:].tolist(), [True] * n, n, 100, 0, 0)
+        assert (e.positions[1, h].cpu() - (P - n)).tolist() == order
+        assert torch.equal(e.k[1, h].cpu(), tail[0, 0, h, order]) and torch.equal(e.v[1, h].cpu(), tail[1, 0, h, order])
+        assert same(e8.cache.v[1, h].float() * e8.cache.v_scale[1, h].repeat_interleave(64)[:100, None],
+                    ref.dequant(*ref.quantize(vd[:, h:h + 1, order], None, 64, 0, torch.zeros(1, 1, 100, 256, dtype=F64),
+                                              torch.ones(1, 1, 2, dtype=F64)), 64)[0, 0])
+
+
 # ------------------------------------------------------------------ mass
 
 def check_mass(g, B, Hq, H, P, S, block, valid=None, mask=None, before=None, lse=None, q=None, k=None):
@@ -449,6 +568,24 @@ def test_evict_ties_and_odd_weights(kind):
         m = 1.0 + torch.randint(0, 50, (2, 2, 700), generator=g).float() * 2.0 ** -23
     check_evict(g, 2, 2, 700, 400, 0, 390, 0, 0, [700, 655], m=m)
     check_evict(g, 2, 2, 700, 400, 0, 100, 2, 3, [700, 655], m=m)
+
+
+@pytest.mark.parametrize("P", [1023, 1024, 1025, 2048, 2049, 4096, 4097, 8192, 8193, 10000])
+@pytest.mark.parametrize("block", [0, 16])
+def test_evict_lengths(P, block):
+    g = gen(P)
+    m = torch.randint(0, 40, (2, 1, P), generator=g).float()   # many equal weights, some of them cut
+    check_evict(g, 2, 1, P, 700, block, 650, 3, 5, [P, P - 7], m=m)
+    mask = (torch.rand(2, P, generator=g) >= 0.5).to(torch.uint8)
+    check_evict(g, 2, 1, P, P, block, P, 0, 0, [P, 900], mask, m=torch.rand(2, 1, P, generator=g))
+
+
+@pytest.mark.parametrize("block", [0, 16, 128])
+@pytest.mark.parametrize("B,H", [(5, 7), (37, 4), (149, 1), (75, 4)])
+def test_evict_many_heads(B, H, block):
+    g = gen(B)
+    valid = torch.randint(0, 331, (B,), generator=g).tolist()
+    check_evict(g, B, H, 330, 200, block, 190, 2, 9, valid)
 
 
 def test_evict_long_prefix():
