@@ -235,6 +235,12 @@ int mass_call(bool kv8, const void *q, const void *k, const float *k_scale, int 
     return e == cudaSuccess ? DM05_OK : DM05_ERR_CUDA;
 }
 
+bool overlap(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 int evict_checks(const void *k, const void *v, const float *mass, const int32_t *valid_len, const void *k_out,
                  const void *v_out, const float *mass_out, const int32_t *positions, const int32_t *valid_out, int B,
                  int Hkv, int P, int P_out, int D, int n_keep, int n_first, int n_last)
@@ -250,9 +256,95 @@ int evict_checks(const void *k, const void *v, const float *mass, const int32_t 
     return DM05_OK;
 }
 
-int launch_select(const float *mass, const int32_t *valid_len, const uint8_t *mask, float *mass_out,
-                  int32_t *positions, int32_t *valid_out, uint32_t *err, int B, int Hkv, int P, int P_out, int n_keep,
-                  int n_first, int n_last, cudaStream_t stream)
+// An eviction in place would write rows that other CTAs have yet to read.
+bool evict_overlaps(int row_bytes, const void *k, const void *v, const float *mass, const void *k_out,
+                    const void *v_out, const float *mass_out, int units, int P, int P_out)
+{
+    const size_t rows = static_cast<size_t>(units) * P, rows_out = static_cast<size_t>(units) * P_out;
+    const size_t in = rows * row_bytes, out = rows_out * row_bytes;
+    return overlap(k, in, k_out, out) || overlap(k, in, v_out, out) || overlap(v, in, k_out, out) ||
+           overlap(v, in, v_out, out) || overlap(k_out, out, v_out, out) ||
+           overlap(mass, rows * 4, mass_out, rows_out * 4);
+}
+
+// CTAs per unit of the one-kernel eviction: what one wave holds, at most one
+// for each block (8-bit) or eight rows (bf16); 0 where the selection and a
+// gather of finer grain behind it are faster: many rows a CTA, more units than
+// SMs, or more positions than a CTA's registers hold.
+int evict_ctas(int units, int P, int n_keep, int block, int num_sms)
+{
+    if (units > num_sms || n_keep == 0 || P > 8 * dm05::cache::kSelectThreads) return 0;
+    const int rows = block > 0 ? block : 8, parts = (n_keep + rows - 1) / rows;
+    const int ctas = std::min(num_sms / units, parts);
+    return (parts + ctas - 1) / ctas * rows <= 256 ? ctas : 0;
+}
+
+template <int BLOCK>
+int launch_evict(const dm05::cache::EvictParams &ep, int ctas, int units, cudaStream_t stream)
+{
+    using namespace dm05::cache;
+    constexpr int kT = kSelectThreads;
+    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(units));
+    if (ep.s.P <= kT) return launch(evict_kernel<1, BLOCK>, grid, kT, 0, stream, ep);
+    if (ep.s.P <= 2 * kT) return launch(evict_kernel<2, BLOCK>, grid, kT, 0, stream, ep);
+    if (ep.s.P <= 4 * kT) return launch(evict_kernel<4, BLOCK>, grid, kT, 0, stream, ep);
+    return launch(evict_kernel<8, BLOCK>, grid, kT, 0, stream, ep);
+}
+
+int launch_select(const dm05::cache::SelectParams &sp, int units, cudaStream_t stream)
+{
+    using namespace dm05::cache;
+    const dim3 grid(1, static_cast<unsigned>(units));
+    constexpr int kT = kSelectThreads;
+    if (sp.P <= kT) return launch(select_kernel<1>, grid, kT, 0, stream, sp);
+    if (sp.P <= 2 * kT) return launch(select_kernel<2>, grid, kT, 0, stream, sp);
+    if (sp.P <= 4 * kT) return launch(select_kernel<4>, grid, kT, 0, stream, sp);
+    if (sp.P <= 8 * kT) return launch(select_kernel<8>, grid, kT, 0, stream, sp);
+    return launch(select_kernel<0>, grid, kT, 0, stream, sp);
+}
+
+template <int BLOCK>
+int launch_gather(const dm05::cache::GatherParams &gp, int units, int n_keep, cudaStream_t stream)
+{
+    constexpr int kRows = dm05::cache::Strip<BLOCK, 256>::kRows;
+    return launch(dm05::cache::gather_codes_kernel<BLOCK>,
+                  dim3(static_cast<unsigned>((n_keep + kRows - 1) / kRows), static_cast<unsigned>(units)), 512, 0, stream,
+                  gp);
+}
+
+// One kernel or two (microseconds, P = 1024, 512 rows kept, bf16 / blocks of
+// 64): 4 samples of 4 heads 7.2 / 6.6 in one, 8.4 / 7.9 in two; 18 samples
+// 16.4 / 12.5 and 17.3 / 13.2; 25 samples, with one CTA a unit 22.8 / 17.9
+// and 21.8 / 16.0.
+int run_evict(const dm05::cache::EvictParams &ep, int units, int n_keep, int block, int num_sms, cudaStream_t stream)
+{
+    using namespace dm05::cache;
+    const int ctas = evict_ctas(units, ep.s.P, n_keep, block, num_sms);
+    if (ctas > 0) {
+        switch (block) {
+        case 0: return launch_evict<0>(ep, ctas, units, stream);
+        case 16: return launch_evict<16>(ep, ctas, units, stream);
+        case 32: return launch_evict<32>(ep, ctas, units, stream);
+        case 64: return launch_evict<64>(ep, ctas, units, stream);
+        default: return launch_evict<128>(ep, ctas, units, stream);
+        }
+    }
+    const int rc = launch_select(ep.s, units, stream);
+    if (rc != DM05_OK || n_keep == 0) return rc;
+    if (block == 0)
+        return launch(gather_rows_kernel, dim3(static_cast<unsigned>((n_keep + 31) / 32), static_cast<unsigned>(units)),
+                      256, 0, stream, ep.g);
+    switch (block) {
+    case 16: return launch_gather<16>(ep.g, units, n_keep, stream);
+    case 32: return launch_gather<32>(ep.g, units, n_keep, stream);
+    case 64: return launch_gather<64>(ep.g, units, n_keep, stream);
+    default: return launch_gather<128>(ep.g, units, n_keep, stream);
+    }
+}
+
+dm05::cache::SelectParams select_params(const float *mass, const int32_t *valid_len, const uint8_t *mask,
+                                        float *mass_out, int32_t *positions, int32_t *valid_out, uint32_t *err,
+                                        int Hkv, int P, int P_out, int n_keep, int n_first, int n_last)
 {
     dm05::cache::SelectParams sp = {};
     sp.mass = mass;
@@ -268,13 +360,7 @@ int launch_select(const float *mass, const int32_t *valid_len, const uint8_t *ma
     sp.n_keep = n_keep;
     sp.n_first = n_first;
     sp.n_last = n_last;
-    const dim3 grid(static_cast<unsigned>(B * Hkv));
-    constexpr int kT = dm05::cache::kSelectThreads;
-    if (P <= kT) return launch(dm05::cache::select_kernel<1>, grid, kT, 0, stream, sp);
-    if (P <= 2 * kT) return launch(dm05::cache::select_kernel<2>, grid, kT, 0, stream, sp);
-    if (P <= 4 * kT) return launch(dm05::cache::select_kernel<4>, grid, kT, 0, stream, sp);
-    if (P <= 8 * kT) return launch(dm05::cache::select_kernel<8>, grid, kT, 0, stream, sp);
-    return launch(dm05::cache::select_kernel<0>, grid, kT, 0, stream, sp);
+    return sp;
 }
 
 }  // namespace
@@ -441,13 +527,14 @@ int dm05_prefix_evict(const void *k, const void *v, const float *mass, const int
     int rc = evict_checks(k, v, mass, valid_len, k_out, v_out, mass_out, positions, valid_out, B, Hkv, P, P_out, D,
                           n_keep, n_first, n_last);
     if (rc != DM05_OK) return rc;
+    if (evict_overlaps(512, k, v, mass, k_out, v_out, mass_out, B * Hkv, P, P_out)) return DM05_ERR_UNSUPPORTED;
     Device dev;
     rc = dm05::internal::device(stream, true, &dev);
     if (rc != DM05_OK) return rc;
-    rc = launch_select(mass, valid_len, mask, mass_out, positions, valid_out, dev.err, B, Hkv, P, P_out, n_keep,
-                       n_first, n_last, stream);
-    if (rc != DM05_OK || n_keep == 0) return rc;
-    dm05::cache::GatherParams gp = {};
+    dm05::cache::EvictParams ep = {};
+    ep.s = select_params(mass, valid_len, mask, mass_out, positions, valid_out, dev.err, Hkv, P, P_out, n_keep,
+                         n_first, n_last);
+    dm05::cache::GatherParams &gp = ep.g;
     gp.k = static_cast<const uint8_t *>(k);
     gp.v = static_cast<const uint8_t *>(v);
     gp.k_out = static_cast<uint8_t *>(k_out);
@@ -456,8 +543,8 @@ int dm05_prefix_evict(const void *k, const void *v, const float *mass, const int
     gp.Hkv = Hkv;
     gp.P = P;
     gp.Pout = P_out;
-    return launch(dm05::cache::gather_rows_kernel,
-                  dim3(static_cast<unsigned>((n_keep + 31) / 32), static_cast<unsigned>(B * Hkv)), 256, 0, stream, gp);
+    gp.n_keep = n_keep;
+    return run_evict(ep, B * Hkv, n_keep, 0, dev.num_sms, stream);
 }
 
 int dm05_prefix_evict_kv8(const void *k8, const void *v8, const float *k_scale, const float *v_scale, int block,
@@ -474,13 +561,14 @@ int dm05_prefix_evict_kv8(const void *k8, const void *v8, const float *k_scale, 
     if (shift < 0) return DM05_ERR_UNSUPPORTED;
     if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(k_scale_out, 4) || !aligned(v_scale_out, 4))
         return DM05_ERR_ALIGN;
+    if (evict_overlaps(256, k8, v8, mass, k8_out, v8_out, mass_out, B * Hkv, P, P_out)) return DM05_ERR_UNSUPPORTED;
     Device dev;
     rc = dm05::internal::device(stream, true, &dev);
     if (rc != DM05_OK) return rc;
-    rc = launch_select(mass, valid_len, mask, mass_out, positions, valid_out, dev.err, B, Hkv, P, P_out, n_keep,
-                       n_first, n_last, stream);
-    if (rc != DM05_OK || n_keep == 0) return rc;
-    dm05::cache::GatherParams gp = {};
+    dm05::cache::EvictParams ep = {};
+    ep.s = select_params(mass, valid_len, mask, mass_out, positions, valid_out, dev.err, Hkv, P, P_out, n_keep,
+                         n_first, n_last);
+    dm05::cache::GatherParams &gp = ep.g;
     gp.k = static_cast<const uint8_t *>(k8);
     gp.v = static_cast<const uint8_t *>(v8);
     gp.k_out = static_cast<uint8_t *>(k8_out);
@@ -493,16 +581,11 @@ int dm05_prefix_evict_kv8(const void *k8, const void *v8, const float *k_scale, 
     gp.Hkv = Hkv;
     gp.P = P;
     gp.Pout = P_out;
+    gp.n_keep = n_keep;
     gp.nblk = blocks_of(P, shift);
     gp.nblk_out = blocks_of(P_out, shift);
     gp.shift = shift;
-    const dim3 grid(static_cast<unsigned>((n_keep + block - 1) >> shift), static_cast<unsigned>(B * Hkv));
-    switch (block) {
-    case 16: return launch(dm05::cache::gather_codes_kernel<16>, grid, 512, 0, stream, gp);
-    case 32: return launch(dm05::cache::gather_codes_kernel<32>, grid, 512, 0, stream, gp);
-    case 64: return launch(dm05::cache::gather_codes_kernel<64>, grid, 512, 0, stream, gp);
-    default: return launch(dm05::cache::gather_codes_kernel<128>, grid, 512, 0, stream, gp);
-    }
+    return run_evict(ep, B * Hkv, n_keep, block, dev.num_sms, stream);
 }
 
 }  // extern "C"

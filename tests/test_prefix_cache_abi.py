@@ -121,6 +121,19 @@ def test_evict_refuses(kw, status):
     assert _call(bd.dm05_prefix_evict_kv8, EVICT8, EVICT8_D, kw) == status
 
 
+def test_evict_refuses_to_work_in_place():
+    G = 1 << 40
+    apart = dict(v=F + G, k_out=F + 2 * G, v_out=F + 3 * G, mass=F + 4 * G, mass_out=F + 5 * G, B=2)
+    for fn, order, d, row in ((bd.dm05_prefix_evict, EVICT, EVICT_D, 512), (bd.dm05_prefix_evict_kv8, EVICT8, EVICT8_D, 256)):
+        d = dict(d, **apart)
+        size = 2 * 4 * 1024 * row
+        for kw in (dict(k_out=F), dict(v_out=F), dict(k_out=F + size - 16), dict(k_out=F + G - 16), dict(v_out=F + G + 512),
+                   dict(v_out=F + 2 * G), dict(mass_out=F + 4 * G + 4)):
+            assert _call(fn, order, d, kw) == bd.DM05_ERR_UNSUPPORTED
+        if not torch.cuda.is_available():                  # one row behind the old cache is no overlap
+            assert _call(fn, order, d, dict(k_out=F + size)) == bd.DM05_ERR_CUDA
+
+
 def test_evict_kv8_refuses():
     for name in ("k_scale", "v_scale", "k_scale_out", "v_scale_out"):
         assert _call(bd.dm05_prefix_evict_kv8, EVICT8, EVICT8_D, {name: None}) == bd.DM05_ERR_NULL
