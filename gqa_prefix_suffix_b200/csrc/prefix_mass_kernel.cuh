@@ -118,7 +118,22 @@ __global__ void __launch_bounds__(kThreadsM, 1)
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    if (warp == kLoadWarp && lane == 0) {
+        // what will be read first is asked into L2 while the kernel before this
+        // one ends (caches and queries may still change until the wait below:
+        // L2 then holds the change).  The run is the one of a full prefix.
+        if (p.valid_len != nullptr) ptx::prefetch_l2(p.valid_len + b);
+        ptx::tma_prefetch_4d(&tm_q, 0, 0, 0, unit);
+        const long long all = (p.P + kTile - 1) / kTile;
+        const int ta = static_cast<int>(all * blockIdx.x / gridDim.x);
+        const int te = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
+        for (int t = ta; t < min(te, ta + 2); ++t) ptx::tma_prefetch_4d(&tm_k, 0, t * kTile, 0, unit);
+    }
     ptx::griddep_wait();
+    if (warp == kLoadWarp && lane == 0) {  // needs no valid length
+        ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(p.N) * 512u);
+        ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, 0, 0, unit);
+    }
 
     const int vl = cache::clamped_len(p.valid_len, b, p.P, p.err,
                                       threadIdx.x == 0 && blockIdx.x == 0 && unit % p.Hkv == 0);
@@ -130,10 +145,8 @@ __global__ void __launch_bounds__(kThreadsM, 1)
     bool failed = false;
 
     if (warp == kLoadWarp) {
-        if (lane == 0 && T > 0) {
+        if (lane == 0) {
             const uint64_t pol = ptx::policy_evict_first();
-            ptx::mbar_arrive_expect_tx(&bars[L::kBarQFull], static_cast<uint32_t>(p.N) * 512u);
-            ptx::tma_load_4d(smem, &tm_q, &bars[L::kBarQFull], 0, 0, 0, unit);
             int issued = 0;
             for (int t = 0; t < T; ++t) {
                 const int s = t % L::kSlots, n = t / L::kSlots;
