@@ -304,7 +304,7 @@ __device__ __forceinline__ int warp_scan_table(int *table, int n)
 // for each.  Returns keep, the number of kept positions.  All 1024 threads.
 //
 // Latency bounds it, a chain of counts, scans and barriers, so that it stops at
-// the first digit whose bin is kept whole (P = 2048, 512 of it kept: 6.3
+// the first digit whose bin is kept whole (1000 of 2048 kept: 6.3
 // instead of 6.9 us for the whole eviction).
 //
 // KPT > 0: P <= KPT * 1024 and every thread keeps its keys in registers (the
