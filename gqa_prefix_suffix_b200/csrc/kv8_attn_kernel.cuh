@@ -46,11 +46,12 @@
 // 10: 38 instead of 42 us; with runs under four tiles the joining costs more.)
 //
 // A unit's tiles may be split over any number of CTAs (and its query rows
-// over blocks, so that a CTA writes fewer partial rows): each writes its
-// unnormalised O with {m, l} per row, and merge_kernel, launched behind it,
-// joins them.  (A cluster merge inside the kernel, as the bf16 kernel has,
-// limits a unit to 16 CTAs and the grid to what clusters leave resident: 68
-// instead of 42 us at B = 2, P = 30016.)
+// over blocks, so that a CTA writes fewer partial rows).  Each has its
+// unnormalised O with {m, l} per row.  Few splits form a cluster whose CTAs read one another's
+// partial rows from shared memory (CL); else they are written to the
+// workspace and merge_kernel, launched behind, joins them.  (Clusters alone would limit a unit to
+// 16 CTAs and the grid to what clusters leave resident: 68 instead of 42 us
+// at B = 2, P = 30016.)
 #pragma once
 
 #include "prefix_cache_kernels.cuh"
@@ -303,13 +304,69 @@ __device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, 
     }
 }
 
-template <int R>
+// Joins the `splits` partials of one row, two warps a row (thread col4 of 64
+// owns four columns): with M = max_c m_c and w_c = 2^(m_c - M), out = sum_c w_c
+// O_c / sum_c w_c l_c and lse = (M + log2 sum_c w_c l_c) ln 2.  A partial without
+// keys (l = 0) has no weight, whatever its O holds.  part(c): the four
+// columns of partial c; state(c): its {m, l}.  Latency is all there is: the
+// first AHEAD partials are requested before their weights are known.
+template <int AHEAD, class Part, class State>
+__device__ __forceinline__ void join_partials(int splits, Part &&part, State &&state, __nv_bfloat16 *out, float *lse,
+                                              size_t r, int col4)
+{
+    const int lane = threadIdx.x & 31;
+    float4 o[AHEAD];
+#pragma unroll
+    for (int c = 0; c < AHEAD; ++c)
+        if (c < splits) o[c] = part(c);
+    float m[2], l[2], M = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        float2 st = make_float2(-INFINITY, 0.0f);
+        if (c < splits) st = state(c);
+        m[h] = st.x;
+        l[h] = st.y;
+        if (l[h] != 0.0f) M = fmaxf(M, m[h]);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+    float w[2], total = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        w[h] = l[h] != 0.0f ? ptx::ex2(m[h] - M) : 0.0f;
+        total = fmaf(w[h], l[h], total);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](int c, const float4 &v) {
+        const float wc = __shfl_sync(0xffffffffu, c < 32 ? w[0] : w[1], c & 31);
+        const bool use = wc != 0.0f;
+        acc.x = fmaf(wc, use ? v.x : 0.0f, acc.x);
+        acc.y = fmaf(wc, use ? v.y : 0.0f, acc.y);
+        acc.z = fmaf(wc, use ? v.z : 0.0f, acc.z);
+        acc.w = fmaf(wc, use ? v.w : 0.0f, acc.w);
+    };
+#pragma unroll
+    for (int c = 0; c < AHEAD; ++c)
+        if (c < splits) add(c, o[c]);
+#pragma unroll 4
+    for (int c = AHEAD; c < splits; ++c) add(c, part(c));
+    const float inv = 1.0f / total;
+    *reinterpret_cast<uint2 *>(out + r * kHeadDim + col4 * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (col4 == 0 && lse != nullptr) lse[r] = (M + ptx::lg2(total)) * 0.69314718055994531f;
+}
+
+template <int R, bool CL>
 __global__ void __launch_bounds__(kThreads8, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
                 const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ks,
                 const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ CUtensorMap tm_out,
                 const Params p)
 {
+    static_assert(!CL || R == 1, "copies are joined before partial rows leave");
     using L = Smem;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1003,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                 }
             }
-        } else if (threadIdx.x == 0 && !failed) {
+        } else if (!CL && threadIdx.x == 0 && !failed) {
             if (ptx::mbar_wait(&bars[L::kBarOut], 0, kWaitLimitNs)) {
                 if (C == 1)
                     ptx::tma_store_4d(&tm_out, smem, 0, q0, 0, unit);
@@ -1021,6 +1078,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
     if (failed) atomicOr(p.err, kEwTimeout);
     __syncwarp();
+    if (CL) {
+        // the partial rows staged by the cluster's CTAs, dealt out row by row
+        ptx::cluster_sync();
+        const int col4 = threadIdx.x & 63;
+        for (int r = rank + C * (threadIdx.x >> 6); r < nr; r += C * (kThreads8 / 64)) {
+            const uint32_t at = ptx::smem_addr(smem) + static_cast<uint32_t>(r * kPartRow);
+            join_partials<8>(
+                C, [&](int c) { return ptx::ld_dsmem_f32x4(ptx::mapa(at + static_cast<uint32_t>(col4) * 16u, c)); },
+                [&](int c) {
+                    const float4 v = ptx::ld_dsmem_f32x4(ptx::mapa(at + static_cast<uint32_t>(kHeadDim) * 4u, c));
+                    return make_float2(v.x, v.y);
+                },
+                p.out, p.lse, static_cast<size_t>(unit) * p.GS + q0 + r, col4);
+        }
+        ptx::cluster_sync();  // every peer has read this CTA's rows
+    }
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (warp == kIssueWarp) {
@@ -1036,64 +1109,22 @@ struct MergeParams {
     int rows, GS, splits;  // rows: units * GS
 };
 
-// Joins the partial rows of a split call, two warps a row: with
-// M = max_c m_c and w_c = 2^(m_c - M), out = sum_c w_c O_c / sum_c w_c l_c and
-// lse = (M + log2 sum_c w_c l_c) ln 2.  A partial without keys (l = 0) has no
-// weight, whatever its O holds.  Latency is all there is: the first AHEAD
-// partials are requested before their weights are known (8 for few of them:
-// 16 cost one token's call 0.3 us; 16 for more: 1.5 us less at 18 partials).
+// The partial rows of a split call joined behind it (AHEAD: 8 for few
+// partials, 16 cost one token's call 0.3 us; 16 for more: 1.5 us less at 18).
 template <int AHEAD>
 __global__ void __launch_bounds__(256) merge_kernel(const MergeParams p)
 {
     ptx::griddep_launch_dependents();
-    const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 31, col4 = threadIdx.x & 63;
+    const int r = blockIdx.x * 4 + (threadIdx.x >> 6), col4 = threadIdx.x & 63;
     if (r >= p.rows) return;
     const int unit = r / p.GS, row = r - unit * p.GS;
     const uint8_t *base = p.part + (static_cast<size_t>(unit) * p.splits * p.GS + row) * kPartRow;
     const size_t step = static_cast<size_t>(p.GS) * kPartRow;
     ptx::griddep_wait();
-    float4 o[AHEAD];
-#pragma unroll
-    for (int c = 0; c < AHEAD; ++c)
-        if (c < p.splits) o[c] = *reinterpret_cast<const float4 *>(base + c * step + col4 * 16);
-    float m[2], l[2], M = -INFINITY;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int c = lane + 32 * h;
-        float2 st = make_float2(-INFINITY, 0.0f);
-        if (c < p.splits) st = *reinterpret_cast<const float2 *>(base + c * step + kHeadDim * 4);
-        m[h] = st.x;
-        l[h] = st.y;
-        if (l[h] != 0.0f) M = fmaxf(M, m[h]);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-    float w[2], total = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        w[h] = l[h] != 0.0f ? ptx::ex2(m[h] - M) : 0.0f;
-        total = fmaf(w[h], l[h], total);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto add = [&](int c, const float4 &v) {
-        const float wc = __shfl_sync(0xffffffffu, c < 32 ? w[0] : w[1], c & 31);
-        const bool use = wc != 0.0f;
-        acc.x = fmaf(wc, use ? v.x : 0.0f, acc.x);
-        acc.y = fmaf(wc, use ? v.y : 0.0f, acc.y);
-        acc.z = fmaf(wc, use ? v.z : 0.0f, acc.z);
-        acc.w = fmaf(wc, use ? v.w : 0.0f, acc.w);
-    };
-#pragma unroll
-    for (int c = 0; c < AHEAD; ++c)
-        if (c < p.splits) add(c, o[c]);
-#pragma unroll 4
-    for (int c = AHEAD; c < p.splits; ++c) add(c, *reinterpret_cast<const float4 *>(base + c * step + col4 * 16));
-    const float inv = 1.0f / total;
-    *reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(r) * kHeadDim + col4 * 4) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (col4 == 0 && p.lse != nullptr) p.lse[r] = (M + ptx::lg2(total)) * 0.69314718055994531f;
+    join_partials<AHEAD>(
+        p.splits, [&](int c) { return *reinterpret_cast<const float4 *>(base + c * step + col4 * 16); },
+        [&](int c) { return *reinterpret_cast<const float2 *>(base + c * step + kHeadDim * 4); }, p.out, p.lse,
+        static_cast<size_t>(r), col4);
 }
 
 }  // namespace kv8

@@ -66,8 +66,12 @@ int launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, c
 
 constexpr int kMaxDevices = 64;
 std::mutex g_attr_mu;
-bool g_kv8_ready[kMaxDevices];
+constexpr int kMaxCluster = 16;  // the hardware's largest
 bool g_mass_ready[kMaxDevices];
+struct Kv8Device {
+    bool ready;
+    int active[kMaxCluster + 1];  // clusters of this many CTAs that run at once
+} g_kv8[kMaxDevices];
 
 // Kernel attributes of the attention or of the weight kernels, once per device.
 int set_attributes(const Device &dev, bool mass) noexcept
@@ -75,9 +79,10 @@ int set_attributes(const Device &dev, bool mass) noexcept
     if (dev.ordinal < 0 || dev.ordinal >= kMaxDevices) return DM05_ERR_CUDA;
     try {
         std::lock_guard<std::mutex> lk(g_attr_mu);
-        bool &ready = (mass ? g_mass_ready : g_kv8_ready)[dev.ordinal];
+        bool &ready = mass ? g_mass_ready[dev.ordinal] : g_kv8[dev.ordinal].ready;
         if (ready) return DM05_OK;
         constexpr cudaFuncAttribute kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        constexpr int kSmem8 = dm05::kv8::Smem::kAllocBytes;
         bool ok;
         if (mass)
             ok = cudaFuncSetAttribute(&dm05::mass::mass_kernel<false>, kSmem, dm05::mass::Smem<false>::kAllocBytes) ==
@@ -85,10 +90,31 @@ int set_attributes(const Device &dev, bool mass) noexcept
                  cudaFuncSetAttribute(&dm05::mass::mass_kernel<true>, kSmem, dm05::mass::Smem<true>::kAllocBytes) ==
                      cudaSuccess;
         else
-            ok = cudaFuncSetAttribute(&dm05::kv8::attn_kernel<1>, kSmem, dm05::kv8::Smem::kAllocBytes) == cudaSuccess &&
-                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<2>, kSmem, dm05::kv8::Smem::kAllocBytes) == cudaSuccess &&
-                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<4>, kSmem, dm05::kv8::Smem::kAllocBytes) == cudaSuccess;
+            ok = cudaFuncSetAttribute(&dm05::kv8::attn_kernel<1, false>, kSmem, kSmem8) == cudaSuccess &&
+                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<2, false>, kSmem, kSmem8) == cudaSuccess &&
+                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<4, false>, kSmem, kSmem8) == cudaSuccess &&
+                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<1, true>, kSmem, kSmem8) == cudaSuccess &&
+                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<1, true>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                      1) == cudaSuccess;
         if (!ok) return DM05_ERR_CUDA;
+        for (int c = 2; !mass && c <= kMaxCluster; ++c) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(c), 1, 1);
+            cfg.blockDim = dim3(dm05::kv8::kThreads8, 1, 1);
+            cfg.dynamicSmemBytes = kSmem8;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = static_cast<unsigned>(c);
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, &dm05::kv8::attn_kernel<1, true>, &cfg) != cudaSuccess) {
+                cudaGetLastError();  // a refused size: never used
+                n = 0;
+            }
+            g_kv8[dev.ordinal].active[c] = n;
+        }
         ready = true;
         return DM05_OK;
     } catch (...) {
@@ -96,12 +122,16 @@ int set_attributes(const Device &dev, bool mass) noexcept
     }
 }
 
+constexpr int kCopyRun = 4;        // tiles a CTA walks from which few query rows are copied
+constexpr int kClusterRows = 384;  // partial rows a cluster joins
+
 struct Kv8Plan {
     int splits = 1;      // CTAs per (sample, KV head) and block of query rows
     int row_blocks = 1;  // blocks of the GS query rows
     int qrows = 8;       // rows of a block (a multiple of 8)
     int copies = 1;      // how often a block's rows are laid over the MMA's 128
-    size_t bytes = 0;    // partial results
+    bool cluster = false;  // the splits of a unit are a cluster that joins their rows
+    size_t bytes = 0;    // partial results of the others
 };
 
 // The fewest CTAs per (sample, KV head) that make the longest run of tiles as
@@ -110,6 +140,14 @@ struct Kv8Plan {
 // every CTA then prepares, stages and writes fewer rows, for K and V tiles read
 // from L2 once more (B = 1, P = 1024, S = 50: 12.7 instead of 13.3 us).  Few
 // rows are copied over the MMA's when a CTA walks at least four tiles.
+//
+// Splits that fit a cluster join their rows inside it as long as all clusters
+// run at once (B = 1, P = 576, S = 1: 8.7 instead of 9.5 us with a second
+// kernel, P = 1024, S = 50: 12.0 instead of 12.5; B = 2, P = 1024, S = 32 in
+// clusters that do not: 21.0 instead of 12.3), for which the rows may be cut into
+// fewer blocks, and the partial rows of a cluster are few (B = 2, P = 576, S =
+// 50, 6 x 56 rows: 12.2 instead of 13.2; P = 1024, 9 x 104 rows: 16.3 instead of
+// 13.1).  Call after set_attributes(dev, false).
 Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
 {
     const long long units = static_cast<long long>(B) * Hkv;
@@ -124,14 +162,22 @@ Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
         const int longest = (tiles + most - 1) / most;
         pl.splits = (tiles + longest - 1) / longest;
     }
-    int blocks = 1;
-    if (pl.splits > 1)
-        blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(GS / 32, dev.num_sms / (units * pl.splits))));
-    pl.qrows = ((GS + blocks - 1) / blocks + 7) / 8 * 8;
-    pl.row_blocks = (GS + pl.qrows - 1) / pl.qrows;
     const int run = (tiles + pl.splits - 1) / pl.splits;
-    pl.copies = run < 4 ? 1 : pl.qrows <= 32 ? 4 : pl.qrows <= 64 ? 2 : 1;
-    if (pl.splits > 1) pl.bytes = static_cast<size_t>(units) * pl.splits * GS * dm05::kv8::kPartRow;
+    auto cut = [&](long long blocks) {
+        const int n = static_cast<int>(std::max<long long>(1, blocks));
+        pl.qrows = ((GS + n - 1) / n + 7) / 8 * 8;
+        pl.row_blocks = (GS + pl.qrows - 1) / pl.qrows;
+    };
+    cut(1);
+    if (pl.splits > 1) {
+        const long long blocks = std::min<long long>(GS / 32, dev.num_sms / (units * pl.splits));
+        const long long at_once = pl.splits <= kMaxCluster ? g_kv8[dev.ordinal].active[pl.splits] : 0;
+        cut(std::min(blocks, at_once / units));
+        pl.cluster = run < kCopyRun && units <= at_once && pl.qrows * pl.splits <= kClusterRows;
+        if (!pl.cluster) cut(blocks);
+    }
+    pl.copies = run < kCopyRun ? 1 : pl.qrows <= 32 ? 4 : pl.qrows <= 64 ? 2 : 1;
+    if (pl.splits > 1 && !pl.cluster) pl.bytes = static_cast<size_t>(units) * pl.splits * GS * dm05::kv8::kPartRow;
     return pl;
 }
 
@@ -410,7 +456,8 @@ int dm05_suffix_attn_kv8_plan(int B, int Hq, int Hkv, int P, int S, int D, int *
     int rc = kv8_check(B, Hq, Hkv, P, S, D);
     if (rc != DM05_OK) return rc;
     Device dev;
-    if ((rc = dm05::internal::device(nullptr, false, &dev)) != DM05_OK) return rc;
+    if ((rc = dm05::internal::device(nullptr, false, &dev)) != DM05_OK || (rc = set_attributes(dev, false)) != DM05_OK)
+        return rc;
     const Kv8Plan pl = kv8_plan(B, Hq, Hkv, P, S, dev);
     if (splits_per_head) *splits_per_head = pl.splits;
     if (tile_rows) *tile_rows = dm05::kv8::kTile;
@@ -481,16 +528,20 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     cfg.blockDim = dim3(dm05::kv8::kThreads8, 1, 1);
     cfg.dynamicSmemBytes = dm05::kv8::Smem::kAllocBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(pl.splits);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    auto *kernel = pl.copies == 4   ? &dm05::kv8::attn_kernel<4>
-                   : pl.copies == 2 ? &dm05::kv8::attn_kernel<2>
-                                    : &dm05::kv8::attn_kernel<1>;
+    cfg.numAttrs = pl.cluster ? 2 : 1;
+    auto *kernel = pl.cluster       ? &dm05::kv8::attn_kernel<1, true>
+                   : pl.copies == 4 ? &dm05::kv8::attn_kernel<4, false>
+                   : pl.copies == 2 ? &dm05::kv8::attn_kernel<2, false>
+                                    : &dm05::kv8::attn_kernel<1, false>;
     if (cudaLaunchKernelEx(&cfg, kernel, tq, tkp, tvp, tks, tvs, to, ap) != cudaSuccess) return DM05_ERR_CUDA;
-    if (pl.splits == 1) return DM05_OK;
+    if (pl.splits == 1 || pl.cluster) return DM05_OK;
     dm05::kv8::MergeParams mp = {};
     mp.part = ap.part;
     mp.out = static_cast<__nv_bfloat16 *>(out);

@@ -340,9 +340,9 @@ def test_attention_rows_do_not_touch_each_other(S):
 
 def test_attention_workspace_of_the_caller():
     g = gen(19)
-    c = on_gpu(make_cache(g, 1, 4, 1000, 64))
+    c = on_gpu(make_cache(g, 1, 4, 3000, 64))
     q, ks = rand(g, 1, 8, 50, 256).to(BF).cuda(), rand(g, 1, 4, 50, 256).to(BF).cuda()
-    rc, splits, rows, nbytes = bd.dm05_suffix_attn_kv8_plan(1, 8, 4, 1000, 50, 256)
+    rc, splits, rows, nbytes = bd.dm05_suffix_attn_kv8_plan(1, 8, 4, 3000, 50, 256)
     assert rc == 0 and splits > 1 and rows == 128 and nbytes > 0
     want = bd.suffix_attn_kv8(q, c, ks, ks)
     ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
@@ -350,6 +350,18 @@ def test_attention_workspace_of_the_caller():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     with pytest.raises(bd.Dm05Error):
         bd.suffix_attn_kv8(q, c, ks, ks, workspace=ws[:-16])
+
+
+@pytest.mark.parametrize("B,P,S", [(1, 576, 1), (1, 200, 50), (2, 576, 50), (1, 1024, 50), (1, 1900, 64), (3, 300, 7),
+                                   (2, 1024, 32), (4, 1024, 1), (1, 2500, 12)])
+def test_attention_splits_joined_in_the_kernel_and_behind_it(B, P, S):
+    """Clusters while they all run at once, a second kernel otherwise: with masks that leave splits without a key."""
+    g = gen(B * P + S)
+    check_attention(g, B, 8, 4, P, S, 16, [P] + [P // 3] * (B - 1))
+    mask = torch.zeros(B, P, dtype=torch.uint8)
+    mask[:, :3] = 1
+    mask[0, P // 2] = 1
+    check_attention(g, B, 8, 4, P, S, 16, [P] + [0] * (B - 1), mask)
 
 
 def test_many_heads_of_one_row():
