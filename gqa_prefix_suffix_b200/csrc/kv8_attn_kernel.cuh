@@ -247,61 +247,84 @@ __device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3
 // Rewrites n query rows (four chunks of 64 bf16 a row, qpitch bytes apart,
 // each 128 swizzled bytes) as two e4m3 terms of the row scaled by a power of
 // two to a largest element in (224, 448].  The 64 bytes of 32 bf16 values
-// become their 32 first terms, then their 32 second ones, so a thread rewrites
-// only what it has read.  Warp w of 16 takes rows [8 w, 8 w + 8), a lane one
-// chunk of one row (conflict-free).  factor[row] becomes the row's scale times
-// `unit`, or NaN for a row with an infinity (NaN elements stay NaN codes).
-// With COPY < 128 the result is written 128 / COPY times, COPY rows apart.
-template <int COPY = 128>
-__device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, int warp, float unit, float *factor)
+// become their 32 first terms, then their 32 second ones.  Warp w of 16 takes
+// RW rows, lanes 8 / RW parts of a row's chunk (conflict-free).  factor[row]
+// becomes the row's scale times `unit`, or NaN for a row with an infinity (NaN
+// elements stay NaN codes).  With COPY < 128 the result is written 128 / COPY
+// times, COPY rows apart.
+template <int COPY, int RW>
+__device__ __forceinline__ void split_rows(uint8_t *q, int qpitch, int n, int warp, float unit, float *factor)
 {
-    const int lane = threadIdx.x & 31;
-    const int row = warp * 8 + (lane & 7);
-    if (warp * 8 >= n) return;
+    constexpr int kParts = 8 / RW;    // lanes of a row's chunk
+    constexpr int kUnits = 8 / kParts;  // 16-byte units of a lane
+    const int lane = threadIdx.x & 31, part = lane & (kParts - 1);
+    const int row = warp * RW + ((lane & 7) / kParts);
+    if (warp * RW >= n) return;
     const bool mine = row < n;
     uint8_t *chunk = q + (lane >> 3) * qpitch + row * 128;
-    auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + ((u ^ (lane & 7)) << 4)); };
+    auto unit16 = [&](int u) { return reinterpret_cast<uint4 *>(chunk + ((u ^ (row & 7)) << 4)); };
     __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
     if (mine) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const uint4 v = *unit16(u);
+        for (int u = 0; u < kUnits; ++u) {
+            const uint4 v = *unit16(part * kUnits + u);
             const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(h[e]));
         }
     }
     float amax = fmaxf(__low2float(top), __high2float(top));
+#pragma unroll
+    for (int m = 1; m < kParts; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
     const float s = amax < INFINITY ? cache::pow2_scale(amax) : 1.0f;
-    if (!mine) return;
-    if (lane < 8) {
+    if (mine && lane < 8 && part == 0) {
 #pragma unroll
         for (int c = 0; c < 128; c += COPY) factor[c + row] = amax < INFINITY ? s * unit : __int_as_float(0x7fffffff);
     }
     const float inv = cache::pow2_inverse(s);
+    constexpr int kStep = kUnits < 4 ? kUnits : 4;  // units rewritten together
 #pragma unroll 1
-    for (int g = 0; g < 2; ++g) {
-        uint4 v[4];
+    for (int u0 = part * kUnits; u0 < (part + 1) * kUnits; u0 += kStep) {
+        uint4 v[kStep];
+        uint32_t hi[2 * kStep], lo[2 * kStep];
+        if (mine) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = *unit16(g * 4 + u);
-        uint32_t hi[8], lo[8];
+            for (int u = 0; u < kStep; ++u) v[u] = *unit16(u0 + u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint4 &src = v[e >> 1];
-            const uint32_t w0 = (e & 1) ? src.z : src.x, w1 = (e & 1) ? src.w : src.y;
-            two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
-                      __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
+            for (int e = 0; e < 2 * kStep; ++e) {
+                const uint4 &src = v[e >> 1];
+                const uint32_t w0 = (e & 1) ? src.z : src.x, w1 = (e & 1) ? src.w : src.y;
+                two_terms(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
+                          __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv, hi[e], lo[e]);
+            }
         }
+        // two lanes share four units: both have read before either writes
+        if (kStep < 4) __syncwarp();
+        if (mine) {
+            const int out = (u0 & 4) + (u0 & 3) / 2;  // unit of the first terms; the second ones' is two behind
 #pragma unroll
-        for (int c = 0; c < 128; c += COPY) {
-            unit16(g * 4)[c * 8] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            unit16(g * 4 + 1)[c * 8] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-            unit16(g * 4 + 2)[c * 8] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            unit16(g * 4 + 3)[c * 8] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+            for (int c = 0; c < 128; c += COPY)
+#pragma unroll
+                for (int e = 0; e < kStep / 2; ++e) {
+                    unit16(out + e)[c * 8] = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+                    unit16(out + 2 + e)[c * 8] = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+                }
         }
     }
+}
+
+// As few rows a warp as sixteen warps allow: the fewer, the shorter a lane's chain.
+template <int COPY = 128>
+__device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, int warp, float unit, float *factor)
+{
+    if (COPY <= 32 || n <= 32)
+        split_rows<COPY, 2>(q, qpitch, n, warp, unit, factor);
+    else if (COPY <= 64 || n <= 64)
+        split_rows<COPY, 4>(q, qpitch, n, warp, unit, factor);
+    else
+        split_rows<COPY, 8>(q, qpitch, n, warp, unit, factor);
 }
 
 // Joins the `splits` partials of one row, two warps a row (thread col4 of 64
