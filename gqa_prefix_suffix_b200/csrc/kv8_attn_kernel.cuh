@@ -38,12 +38,12 @@
 // copies it to tensor memory (into the second S buffer, which is not in use
 // yet), and the softmax warps rewrite it in place as the two e4m3 terms.
 //
-// Few query rows (R = 4: at most 32, R = 2: at most 64) are laid R times over
+// Few query rows of an unclustered run (R = 4: at most 32, R = 2: at most 64) are laid R times over
 // the 128 rows of the MMA, and copy r of a row weighs only the r-th part of
 // every tile's keys (its other weights are zeros): the exponentials, which
 // every one of 128 rows would otherwise do for every key, are dealt to all
 // warps, at the price of joining R partial rows at the end.  (P = 30016, S =
-// 10: 38 instead of 42 us; with runs under four tiles the joining costs more.)
+// 10: 37 instead of 42 us; with runs under four tiles the joining costs more.)
 //
 // A unit's tiles may be split over any number of CTAs (and its query rows
 // over blocks, so that a CTA writes fewer partial rows).  Each has its
@@ -687,10 +687,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
         uint64_t *row_bar = &bars[L::kBarRow + q4], *pair_bar = &bars[L::kBarPair + grp * 4 + q4];
         uint64_t *max_bar = &bars[L::kBarMax + q4];
         int row_phase = 0, pair_phase = 0;
-        auto row_sync = [&]() -> bool {  // the four warps of this lane quarter
-            ptx::mbar_arrive(row_bar);
-            return warp_wait(row_bar, row_phase++ & 1);
-        };
         auto pair_sync = [&]() -> bool {  // the two of this group
             ptx::mbar_arrive(pair_bar);
             return warp_wait(pair_bar, pair_phase++ & 1);
@@ -996,25 +992,36 @@ __global__ void __launch_bounds__(kThreads8, 1)
                      (first && (!warp_wait(&bars[L::kBarKFull], 0) || !warp_wait(&bars[L::kBarVFull], 0)));
         }
         const bool have_o = T > 0 && !failed;
+        // a row's four sums meet; only rows that leave normalised need the total before they are staged
         xl[c4 * kMRows + row] = l;
-        if (!failed && !row_sync()) failed = true;
-        const float l_row = (xl[row] + xl[kMRows + row]) + (xl[2 * kMRows + row] + xl[3 * kMRows + row]);
-        const float inv_l = 1.0f / l_row;
+        const bool direct = R == 1 && C == 1;
+        float l_row = 0.0f, inv_l = 0.0f;
+        auto total = [&]() {
+            if (!failed && !warp_wait(row_bar, row_phase++ & 1)) failed = true;
+            l_row = (xl[row] + xl[kMRows + row]) + (xl[2 * kMRows + row] + xl[3 * kMRows + row]);
+            inv_l = 1.0f / l_row;
+        };
+        ptx::mbar_arrive(row_bar);
+        if (direct) total();
         const int srow = R == 1 ? row : copy * nr + qrow;  // staged row
         // The rows leave through shared memory in one copy: bf16 rows in the
         // layout of a Q tile, partial rows as they lie in the workspace.
         // (16-byte stores of 32 rows at a time took 5k cycles a CTA, one bulk
         // store a row 3.7k.)
         if (have_o && !failed) {
-#pragma unroll 1
+            uint32_t all[2][2][16];
+#pragma unroll
             for (int j = 0; j < 2; ++j) {
-                uint32_t o[2][16];
                 const uint32_t oc = tmem + lane_base + kTmemO8 + c4 * (kHeadDim / 4) + j * 32;
-                ptx::tmem_ld16(oc, o[0]);
-                ptx::tmem_ld16(oc + 16, o[1]);
-                ptx::tmem_ld_wait();
-                if (!row_valid) continue;
-                if (R == 1 && C == 1) {
+                ptx::tmem_ld16(oc, all[j][0]);
+                ptx::tmem_ld16(oc + 16, all[j][1]);
+            }
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t (&o)[2][16] = all[j];
+                if (!row_valid) break;
+                if (direct) {
                     uint8_t *dst = smem + c4 * qpitch + row * 128;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -1035,8 +1042,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 }
             }
         }
+        if (!direct) total();
         if (c4 == 0 && row_valid) {
-            if (R > 1 || C > 1)
+            if (!direct)
                 *reinterpret_cast<float4 *>(smem + srow * kPartRow + kHeadDim * 4) =
                     make_float4(m_end, have_o && !failed ? l_row : 0.0f, 0.0f, 0.0f);
             else if (p.lse != nullptr && !failed)
@@ -1044,7 +1052,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(&bars[L::kBarOut]);
-        if (R > 1) {
+        if (CL) {
+            // joined below
+        } else if (R > 1) {
             // the copies of a row joined as the splits are, 64 threads a row
             if (!failed && !warp_wait(&bars[L::kBarOut], 0)) failed = true;
             if (!failed) {
@@ -1083,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                 }
             }
-        } else if (!CL && threadIdx.x == 0 && !failed) {
+        } else if (threadIdx.x == 0 && !failed) {
             if (ptx::mbar_wait(&bars[L::kBarOut], 0, kWaitLimitNs)) {
                 if (C == 1)
                     ptx::tma_store_4d(&tm_out, smem, 0, q0, 0, unit);

@@ -73,6 +73,13 @@ struct Kv8Device {
     int active[kMaxCluster + 1];  // clusters of this many CTAs that run at once
 } g_kv8[kMaxDevices];
 
+auto *kv8_kernel(int copies, bool cluster)
+{
+    using namespace dm05::kv8;
+    if (cluster) return &attn_kernel<1, true>;
+    return copies == 4 ? &attn_kernel<4, false> : copies == 2 ? &attn_kernel<2, false> : &attn_kernel<1, false>;
+}
+
 // Kernel attributes of the attention or of the weight kernels, once per device.
 int set_attributes(const Device &dev, bool mass) noexcept
 {
@@ -90,12 +97,12 @@ int set_attributes(const Device &dev, bool mass) noexcept
                  cudaFuncSetAttribute(&dm05::mass::mass_kernel<true>, kSmem, dm05::mass::Smem<true>::kAllocBytes) ==
                      cudaSuccess;
         else
-            ok = cudaFuncSetAttribute(&dm05::kv8::attn_kernel<1, false>, kSmem, kSmem8) == cudaSuccess &&
-                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<2, false>, kSmem, kSmem8) == cudaSuccess &&
-                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<4, false>, kSmem, kSmem8) == cudaSuccess &&
-                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<1, true>, kSmem, kSmem8) == cudaSuccess &&
-                 cudaFuncSetAttribute(&dm05::kv8::attn_kernel<1, true>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                      1) == cudaSuccess;
+            ok = cudaFuncSetAttribute(kv8_kernel(1, false), kSmem, kSmem8) == cudaSuccess &&
+                 cudaFuncSetAttribute(kv8_kernel(2, false), kSmem, kSmem8) == cudaSuccess &&
+                 cudaFuncSetAttribute(kv8_kernel(4, false), kSmem, kSmem8) == cudaSuccess &&
+                 cudaFuncSetAttribute(kv8_kernel(1, true), kSmem, kSmem8) == cudaSuccess &&
+                 cudaFuncSetAttribute(kv8_kernel(1, true), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                     cudaSuccess;
         if (!ok) return DM05_ERR_CUDA;
         for (int c = 2; !mass && c <= kMaxCluster; ++c) {
             cudaLaunchConfig_t cfg = {};
@@ -109,7 +116,7 @@ int set_attributes(const Device &dev, bool mass) noexcept
             cfg.attrs = at;
             cfg.numAttrs = 1;
             int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, &dm05::kv8::attn_kernel<1, true>, &cfg) != cudaSuccess) {
+            if (cudaOccupancyMaxActiveClusters(&n, kv8_kernel(1, true), &cfg) != cudaSuccess) {
                 cudaGetLastError();  // a refused size: never used
                 n = 0;
             }
@@ -536,11 +543,7 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = pl.cluster ? 2 : 1;
-    auto *kernel = pl.cluster       ? &dm05::kv8::attn_kernel<1, true>
-                   : pl.copies == 4 ? &dm05::kv8::attn_kernel<4, false>
-                   : pl.copies == 2 ? &dm05::kv8::attn_kernel<2, false>
-                                    : &dm05::kv8::attn_kernel<1, false>;
-    if (cudaLaunchKernelEx(&cfg, kernel, tq, tkp, tvp, tks, tvs, to, ap) != cudaSuccess) return DM05_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kv8_kernel(pl.copies, pl.cluster), tq, tkp, tvp, tks, tvs, to, ap) != cudaSuccess) return DM05_ERR_CUDA;
     if (pl.splits == 1 || pl.cluster) return DM05_OK;
     dm05::kv8::MergeParams mp = {};
     mp.part = ap.part;
