@@ -1,5 +1,10 @@
 """The prefix-cache compression operators on the GPU against their plain
 64-bit forms (prefix_cache_ref), whose docstrings derive the bounds."""
+import os
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -742,6 +747,54 @@ def test_two_captured_chains_replay_at_once():
     graphs[0].replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(outs[0], fresh))
+
+
+FIRST_IN_CAPTURE = """
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import test_prefix_cache_gpu as t
+a, big = t.chain_inputs(47), t.chain_inputs(48, B=2, P=3000, S=10)
+t.bd.kv8_quantize(a[1], a[2], 32)                          # only the error word exists before the capture
+torch.cuda.synchronize()
+g, out = torch.cuda.CUDAGraph(), []
+with torch.cuda.graph(g):
+    for x in (a, big):
+        out.append(t.flat(t.chain(*x)))
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+for x, got in zip((a, big), out):
+    assert all(torch.equal(p, q) for p, q in zip(got, t.flat(t.chain(*x))))
+assert t.bd.dm05_get_error_word(None) == (0, 0)
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE, here], cwd=os.path.dirname(here), capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+def test_calls_from_several_threads():
+    """Threads with streams of their own, the first calls of all at the same time."""
+    ins = [chain_inputs(50 + i, P=400 + 300 * i) for i in range(4)]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(5):
+            got[i] = flat(chain(*ins[i], stream=s))
+        s.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, r in zip(ins, got):
+        assert all(torch.equal(x, y) for x, y in zip(r, flat(chain(*a))))
 
 
 def test_front_end_refuses_bad_tensors():
