@@ -738,7 +738,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
             float ks_cur = ks_next, vs_cur = vs_next;
             load_next(t + 2);
             const int n = rows_of(t);
-            float ag[kGroups], bg[kGroups], ig[kGroups];
+            float ag[kGroups], bg[kGroups];
+            float iv = 1.0f;
             const bool partial = t >= ns && partial_at(t);
             if (t >= ns) {
                 if (partial) {
@@ -754,12 +755,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const uint32_t mine = (lane & 2) ? vis[kWords - 1] : vis[0];
                     if (((lane & 1) ? mine >> 16 : mine & 0xffffu) == 0u) ks_cur = vs_cur = 1.0f;
                 }
-                const float lv = ptx::lg2(vs_cur), iv = 1.0f / vs_cur;
+                const float lv = ptx::lg2(vs_cur);
+                iv = 1.0f / vs_cur;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     ag[g] = __shfl_sync(0xffffffffu, ks_cur, g) * sqs;
                     bg[g] = __shfl_sync(0xffffffffu, lv, g);
-                    ig[g] = __shfl_sync(0xffffffffu, iv, g);
                 }
             } else if (t > 0) {
                 // the second suffix tile follows the first in one buffer: its
@@ -887,7 +888,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     two_terms(w0, w1, w2, w3, hi[e >> 2], lo[e >> 2]);
                 }
                 const float2 lp = ptx::unpack_f32x2(l2);
-                l = fmaf(lp.x + lp.y, ig[g], l);
+                l = fmaf(lp.x + lp.y, __shfl_sync(0xffffffffu, iv, g), l);
             };
             if (t < ns) {
                 uint32_t pk[16];

@@ -551,7 +551,7 @@ def check_evict(g, B, H, P, bucket, block, keep, first=0, last=0, valid=None, ma
 @pytest.mark.parametrize("block", [0, 16, 64, 128])
 @pytest.mark.parametrize("P,bucket,keep,first,last,valid", [
     (1, 1, 1, 0, 0, None), (1, 3, 0, 0, 0, None), (40, 40, 40, 0, 0, [40, 0]), (200, 64, 50, 4, 10, [200, 30]),
-    (513, 200, 129, 0, 0, [513, 512]), (1000, 576, 512, 16, 64, [900, 700]), (777, 300, 17, 100, 0, [777, 5])])
+    (513, 200, 129, 0, 0, [513, 512]), (33, 100, 90, 40, 40, [33, 7]), (1000, 576, 512, 16, 64, [900, 700]), (777, 300, 17, 100, 0, [777, 5])])
 def test_evict(block, P, bucket, keep, first, last, valid):
     check_evict(gen(P + keep + block), 1 if valid is None else 2, 2, P, bucket, block, keep, first, last, valid)
 
