@@ -499,7 +499,8 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     const long long grid = static_cast<long long>(units) * pl.row_blocks * pl.splits;
     if (grid > 0x7fffffffLL) return DM05_ERR_SHAPE;
     CUtensorMap tq, tkp, tvp, tks, tvs, to;
-    if (encode_rows16(&tq, q, GS, units, pl.qrows, pl.copies == 1 ? 4 : 1) != DM05_OK || encode_rows16(&to, out, GS, units, pl.qrows) != DM05_OK ||
+    if (encode_rows16(&tq, q, GS, units, pl.qrows, pl.copies == 1 ? 4 : 1) != DM05_OK ||
+        encode_rows16(&to, out, GS, units, pl.qrows) != DM05_OK ||
         encode_rows16(&tks, k_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK ||
         encode_rows16(&tvs, v_suffix, S, units, dm05::kv8::kSufTile) != DM05_OK)
         return DM05_ERR_CUDA;
@@ -543,7 +544,8 @@ int dm05_suffix_attn_kv8(const void *q, const void *k8, const void *v8, const fl
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = pl.cluster ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kv8_kernel(pl.copies, pl.cluster), tq, tkp, tvp, tks, tvs, to, ap) != cudaSuccess) return DM05_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kv8_kernel(pl.copies, pl.cluster), tq, tkp, tvp, tks, tvs, to, ap) != cudaSuccess)
+        return DM05_ERR_CUDA;
     if (pl.splits == 1 || pl.cluster) return DM05_OK;
     dm05::kv8::MergeParams mp = {};
     mp.part = ap.part;

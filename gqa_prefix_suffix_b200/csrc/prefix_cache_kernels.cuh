@@ -123,7 +123,8 @@ struct QuantParams {
 
 // One CTA per (block of rows, unit, K or V): every value is read once, held
 // in registers for the block's maximum and then encoded.  Bound by HBM
-// (2 bytes read and 1 written per value).
+// (2 bytes read and 1 written per value): B = 32, 4 heads, P = 1024 in 24.9 us,
+// 6.3 TB/s; small caches by launch and one round trip (2.7 us).
 template <int BLOCK>
 __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p)
 {
@@ -389,7 +390,8 @@ __device__ __forceinline__ int select_positions(const SelectParams &p, int unit,
             if (KPT > 0) {
 #pragma unroll
                 for (int i = 0; i < kKeys; ++i)
-                    if (keys[i] != 0u && (keys[i] & known) == prefix) atomicAdd(&hist[pass][(keys[i] >> shift) & 255u], 1);
+                    if (keys[i] != 0u && (keys[i] & known) == prefix)
+                        atomicAdd(&hist[pass][(keys[i] >> shift) & 255u], 1);
             } else {
                 for (int i = 0; i < rounds; ++i) {
                     const uint32_t k = key_of(i);

@@ -24,6 +24,12 @@
 // cores' running sum loses a little with every step (2e-6 of the weight of
 // a key of large logit in one chain, 0.8e-6 in two).  Two buffers of two halves
 // of 128 columns fill the tensor memory.
+//
+// B = 32, P = 1024, 100 rows a unit: 14.1 us from codes (a tile takes 1.65k cycles
+// of which the MMAs are 1.1k; the rest waits for a buffer to be read), 13.8 us
+// from bf16 (HBM and start-up); B = 1, P = 2048 4.7 us.  The CTA's 18 warps leave a
+// thread 96 registers: holding a tile's logits to free its buffer earlier
+// spills, and with this much shared memory a spill of 20 bytes costs 1 us.
 #pragma once
 
 #include "kv8_attn_kernel.cuh"
