@@ -3,7 +3,7 @@
 // give, and calls the C ABI on the current stream.
 //
 // The operators' smallest calls take 3 to 13 us on the GPU; the same checks
-// and the call through ctypes took 9 to 19 us on the host, this takes 4 to 9.
+// and the call through ctypes took 9 to 19 us on the host, this takes 4 to 8.
 // The library's entry points are handed in by address (bind), so that
 // there is one loaded library whatever opened it.
 #include <Python.h>
