@@ -19,18 +19,22 @@
 //
 // Warp roles: warp 16 loads, warp 17 issues the MMAs, warps 0-15 are two
 // groups that take the tiles in turn (two warps per 32 keys), so that one
-// group's waits run beside the other's exponentials.  The 256 products
-// of a logit are summed in two halves, joined in fp32 registers: the tensor
-// cores' running sum loses a little with every step (2e-6 of the weight of
-// a key of large logit in one chain, 0.8e-6 in two).  Two buffers of two halves
-// of 128 columns fill the tensor memory.
+// group's waits run beside the other's exponentials.  The 256 products of a
+// logit are summed in two chains, of a bf16 cache in four where they fit,
+// joined in fp32 registers: the tensor cores' running sum loses a little with
+// every step (bf16, one query against 7281 keys, whose sum is mostly one key of
+// large logit: 2e-6 relative in one chain, 1.2e-6 in two, 0.7e-6 in four;
+// 8-bit: 0.4e-6 in two and in four).  Two buffers of two chains of 128 columns, or
+// of four of 64, fill the tensor memory.
 //
 // B = 32, P = 1024, 100 rows a unit: 14.1 us from codes (a tile takes 1.65k cycles
 // of which the MMAs are 1.1k; the rest waits for a buffer to be read), 13.8 us
-// from bf16 (HBM and start-up); B = 1, P = 2048 4.7 us.  The CTA's 18 warps leave a
+// from bf16 (HBM and start-up); B = 1, P = 2048 4.9 us (4.7 in two chains).  The CTA's 18 warps leave a
 // thread 96 registers: holding a tile's logits to free its buffer earlier
 // spills, and with this much shared memory a spill of 20 bytes costs 1 us.
 #pragma once
+
+#include <type_traits>
 
 #include "kv8_attn_kernel.cuh"
 
@@ -42,7 +46,7 @@ constexpr int kSoftWarps = 16;
 constexpr int kLoadWarp = 16;
 constexpr int kIssueWarp = 17;
 constexpr int kThreadsM = 576;
-constexpr int kBufs = 2;       // logit buffers of two halves of 128 columns
+constexpr int kBufs = 2;       // logit buffers of 256 columns
 
 template <bool KV8>
 struct Smem {
@@ -148,6 +152,10 @@ __global__ void __launch_bounds__(kThreadsM, 1)
     // mass is only carried over)
     const int t0 = static_cast<int>(static_cast<long long>(t_in) * blockIdx.x / gridDim.x);
     const int T = static_cast<int>(static_cast<long long>(t_in) * (blockIdx.x + 1) / gridDim.x) - t0;
+    // The 256 products of a bf16 logit are summed in four chains where tensor memory
+    // holds them: 64 columns or fewer each, or one tile that needs no second buffer.
+    const bool four = !KV8 && (p.N <= 64 || T <= 1);
+    const int chain_cols = p.N <= 64 ? 64 : 128;
     bool failed = false;
 
     if (warp == kLoadWarp) {
@@ -186,20 +194,28 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 ptx::tc_fence_after_sync();
                 const uint64_t kd = kdesc + static_cast<uint64_t>((s * L::kSlotBytes) >> 4);
                 const uint32_t d = tmem + sb * 256;
+                auto issue = [&](auto chain, int cols) {
+                    constexpr int kLen = decltype(chain)::value;  // MMAs of a chain
 #pragma unroll
-                for (int kk = 0; kk < 16; ++kk) {
-                    if (KV8) {
-                        // 32 columns j against both terms of the queries
-                        const int j = kk >> 1;
-                        const uint32_t qo = ((j >> 1) * qpitch + (j & 1) * 64 + (kk & 1) * 32) >> 4;
-                        const uint32_t ko = ((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4;
-                        ptx::mma_f8_ss(d + (kk >> 3) * 128, kd + ko, qdesc + qo, idesc, (kk & 7) > 0 ? 1u : 0u);
-                    } else {
-                        const uint32_t qo = ((kk >> 2) * qpitch + (kk & 3) * 32) >> 4;
-                        const uint32_t ko = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-                        ptx::mma_bf16_ss(d + (kk >> 3) * 128, kd + ko, qdesc + qo, idesc, (kk & 7) > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 16; ++kk) {
+                        const uint32_t dk = d + kk / kLen * cols, add = kk % kLen > 0 ? 1u : 0u;
+                        if (KV8) {
+                            // 32 columns j against both terms of the queries
+                            const int j = kk >> 1;
+                            const uint32_t qo = ((j >> 1) * qpitch + (j & 1) * 64 + (kk & 1) * 32) >> 4;
+                            const uint32_t ko = ((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4;
+                            ptx::mma_f8_ss(dk, kd + ko, qdesc + qo, idesc, add);
+                        } else {
+                            const uint32_t qo = ((kk >> 2) * qpitch + (kk & 3) * 32) >> 4;
+                            const uint32_t ko = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+                            ptx::mma_bf16_ss(dk, kd + ko, qdesc + qo, idesc, add);
+                        }
                     }
-                }
+                };
+                if (four)
+                    issue(std::integral_constant<int, 4>(), chain_cols);
+                else
+                    issue(std::integral_constant<int, 8>(), 128);
                 ptx::mma_commit(&bars[L::kBarEmpty + s]);
                 ptx::mma_commit(&bars[L::kBarSFull + sb]);
             }
@@ -272,10 +288,20 @@ __global__ void __launch_bounds__(kThreadsM, 1)
             for (int h = 0; h < 4; ++h) {
                 const int g = hf + 2 * h;
                 if (g >= groups) break;
-                uint32_t raw[2][16];  // the two halves of the 256 products
+                uint32_t raw[2][16];  // the chains' sums: all but the last, the last
                 ptx::tmem_ld16(col + g * 16, raw[0]);
-                ptx::tmem_ld16(col + 128 + g * 16, raw[1]);
+                ptx::tmem_ld16(col + (four ? chain_cols : 128) + g * 16, raw[1]);
                 ptx::tmem_ld_wait();
+                if (four) {
+#pragma unroll
+                    for (int c = 2; c < 4; ++c) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            raw[0][i] = __float_as_uint(__uint_as_float(raw[0][i]) + __uint_as_float(raw[1][i]));
+                        ptx::tmem_ld16(col + c * chain_cols + g * 16, raw[1]);
+                        ptx::tmem_ld_wait();
+                    }
+                }
                 if (g == last) {
                     ptx::tc_fence_before_sync();
                     ptx::mbar_arrive(&bars[L::kBarSFree + sb]);
