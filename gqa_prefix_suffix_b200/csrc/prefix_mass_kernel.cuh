@@ -23,7 +23,7 @@
 // logit are summed in two chains, of a bf16 cache in four where they fit,
 // joined in fp32 registers: the tensor cores' running sum loses a little with
 // every step (bf16, one query against 7281 keys, whose sum is mostly one key of
-// large logit: 2e-6 relative in one chain, 1.2e-6 in two, 0.7e-6 in four;
+// large logit: 1.2e-6 relative in two chains, 0.7e-6 in four;
 // 8-bit: 0.4e-6 in two and in four).  Two buffers of two chains of 128 columns, or
 // of four of 64, fill the tensor memory.
 //
