@@ -12,25 +12,36 @@
 //     as two e4m3 terms, hi = e4m3(q'), lo = e4m3(q' - hi): a bf16 value has 8
 //     significant bits, two e4m3 terms hold 4 each, so every element within
 //     2^-10 of the row's largest is exact and smaller ones are off by at
-//     most 2^-10 in units of that scale.  A weight is carried the same way
-//     (from its fp16 rounding): its error is at most 2^-8 of it and on
-//     average under half of what one bf16 rounding leaves.
+//     most 2^-10 in units of that scale.
+//   * Weights have no such common unit: where one key is far above the others
+//     all of those still count, and V's scales have sizes of their own.
+//     kind::mxf8f6f4 gives every row of A a power-of-two scale for each 32
+//     keys: a weight times its vs is carried in units in which its step's
+//     largest lies in (2^7.8, 2^8.8], as e4m3 and, of what that leaves, e5m2
+//     (kTermBits further down).  It is off by at most 2^-7 of itself (rms
+//     1.4e-3; one bf16 rounding: 2^-8 and 1.66e-3) down to 2^-14 of the step's
+//     largest, by at most a sixth down to 2^-28 of it.  (As two e4m3 terms in
+//     one unit for the whole row, weights under 2^-14 of the row's largest
+//     were lost: outputs off by 20 to 90 % behind a key 10 nats above the
+//     rest, at 8.1, 11.6, 28.7 and 37 us below.  A third term costs 3 to 14 %;
+//     V widened to bf16 in shared memory, with two bf16 terms, 4 to 27 %.)
+//   * What a step's largest weight is off by goes into the sum that divides
+//     the output, so that in a row of one such weight it cancels.
+//   * Two blocks of 16 share a step.  One without a value (the quantiser gives
+//     it scale 1) must not set its unit: where the two scales are far apart,
+//     the V tile is looked at first.
 //   * The same MMAs over a bf16 copy of the codes would need the codes
-//     widened in shared memory (three times the shared-memory traffic and
-//     half the tile); two 8-bit terms run at twice the 16-bit rate, so they
-//     cost the tensor pipe the same.
+//     widened in shared memory (three times the shared-memory traffic); two
+//     8-bit terms run at twice the 16-bit rate, so they cost the tensor pipe the same.
 //   * Measured on one SM: 70 cycles for a 128 x 128 x 32 MMA with both
 //     operands in shared memory (66 at N = 64, so tiles are 128 keys), 131
-//     for 128 x 256 x 32 with A in tensor memory; 2.1k cycles per 128 keys.
-//   * The running maximum is taken over z + log2(vs) (log2 units), that is
-//     over the weights the PV product sees, with the same lazy update as the
-//     bf16 kernel: a new maximum sits at 2^4 and weights may grow to 2^8.75
-//     before O is rescaled, so the smallest step of the second term (2^-9) is
-//     at most 2^-13 of the largest weight.  (Any of 32 rows asks for a
-//     rescale: with 2^6 and 2^8 most tiles of a batch with peaked keys had one.)
+//     for 128 x 256 x 32 with A in tensor memory, block scales or not; 2.1k cycles per
+//     128 keys.
+//   * The running maximum is taken over the logits alone, lazily: O is rescaled
+//     once it has grown by 2^16.
 //
 // One CTA walks a contiguous run of a unit's key tiles: the suffix tiles (64
-// rows of bf16, kind::f16), then prefix tiles of 128 codes, each 32 KB of K
+// rows of bf16, kind::f16, weights as two bf16 terms), then prefix tiles of 128 codes, each 32 KB of K
 // and of V in two rings of shared memory filled by TMA.  Warps 16 and 18 load
 // (Q and K; V), warp 17 issues the MMAs, and warps 0-15 are two softmax groups
 // that take the tiles in turn (two warps per 32 query rows, half of a tile's
@@ -53,10 +64,10 @@
 // would limit a unit to 16 CTAs and the grid to what clusters leave resident:
 // 68 instead of 42 us at B = 2, P = 30016.)
 //
-// Times a call (device, Hq = 8 over Hkv = 4): one token, P = 576: 8.1 us; S = 50,
-// P = 1024: 11.6 us; B = 32, masked: 28.7 us, bound by a tile's chain of logits,
-// maximum, weights and product (3.9k cycles, two tiles at a time); B = 2, P =
-// 30016, S = 10: 37 us, its loop at 5.2 TB/s.
+// Times a call (device, Hq = 8 over Hkv = 4): one token, P = 576: 8.7 us; S = 50,
+// P = 1024: 12.5 us; B = 32, masked: 30.6 us, bound by a tile's chain of logits,
+// maximum, weights and product (4.2k cycles, two tiles at a time); B = 2, P =
+// 30016, S = 10: 40 us.
 #pragma once
 
 #include "prefix_cache_kernels.cuh"
@@ -77,16 +88,38 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// The same with A in tensor memory: 32 codes of a row in 8 columns.
-__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate)
+// D[tmem] (+)= (A[tmem] * scales of A) * (B[smem] * scales of B)^T, 8-bit inputs (32 codes of
+// a row of A in 8 columns), K = 32, one scale for each row of A and of B.
+__device__ __forceinline__ void mma_mxf8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t a_scales, uint32_t b_scales, uint32_t accumulate)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], [%1], %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
         : "memory");
+}
+
+// Instruction descriptor of a kind::mxf8f6f4 MMA: A e4m3 or e5m2, B e4m3 and
+// MN-major, ue8m0 scales, those of byte `byte` of the scale columns, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_mxf8_f32(int M, int N, bool a_e5m2, int byte)
+{
+    return (static_cast<uint32_t>(byte) << 4) | ((a_e5m2 ? 1u : 0u) << 7) | (1u << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) |
+           (static_cast<uint32_t>(byte) << 29);
+}
+
+// Copies 32 rows of 16 bytes (512 bytes of shared memory) to 4 columns of each quarter of
+// tensor memory's lanes: the scales of 128 rows, row r's word at (r % 32) * 4 + r / 32.  Ordered
+// before the tcgen05.mma operations the same thread issues later.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr)
+{
+    // eight rows of 16 bytes lie together, 128 bytes apart; no swizzle
+    const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(16 >> 4) << 16 |
+                          static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Instruction descriptor of a kind::f8f6f4 MMA: e4m3 A and B (type 0), fp32
@@ -154,14 +187,17 @@ constexpr int kClearWarp = 19;       // clears hidden V rows
 constexpr int kThreads8 = 640;
 constexpr uint32_t kTmemO8 = 0;      // O: columns [0, 256)
 constexpr uint32_t kTmemS8 = 256;    // two S / P buffers of 128 columns
-constexpr float kTopBits = 4.0f;     // a new maximum's weight is 2^4 ...
-constexpr float kMaxBits = 8.75f;    // ... and may grow to 2^8.75 before O is rescaled (e4m3 ends at 448 = 2^8.8)
-// Codes reach up to 448 where suffix values have their own size, so a suffix
-// weight (bf16, any size will do) counts 2^-7 of itself in the maximum: the
-// prefix weights of ordinary data then use the upper part of e4m3's range
-// (error of a 900-key row 2.3e-3 -> 1.7e-3 relative, 1.65e-3 being the
-// output's own rounding).
-constexpr float kSuffixBits = 7.0f;
+constexpr int kTerms = 2;            // 8-bit terms of a prefix weight
+constexpr int kTermBits = 11;        // the second one's unit is 2^-11 of the first one's
+// The weights of a 32-key step take the first 16 of the 32 columns of an S / P
+// buffer where its logits were, eight for each term.  Behind those of the first and of the
+// second step lie the scales of all steps: of the weights (four columns a term), of V.
+constexpr uint32_t kStepCols = 32;
+constexpr uint32_t kScaleColsA = 16, kScaleColsB = kStepCols + 16;
+// O is rescaled once a row's largest logit has grown by 2^16: weights, and sums
+// of 2^24 of them times values of 2^73, stay far inside fp32's range, and their
+// terms, scaled step by step, are as exact at any size.
+constexpr float kGrowBits = 16.0f;
 
 constexpr int kPartRow = kHeadDim * 4 + 16;  // a partial row: D fp32 of O, then {m, l, 0, 0}
 constexpr int kMaxSplits8 = 64;
@@ -193,7 +229,14 @@ struct Smem {
     // tile maxima [2 groups][2 halves][128], reference maxima [2][128], sums
     // [4][128], visibility limits [16 warps][64]
     static constexpr int kXchgOff = (kTmemSlotOff + 16 + 15) / 16 * 16;
-    static constexpr int kEnd = kXchgOff + (4 + 2 + 4) * kMRows * 4 + kSoftWarps * 64 * 4;
+    // a step's largest weight [2 groups][2 halves][128] (R = 4)
+    static constexpr int kStepMaxOff = kXchgOff + (4 + 2 + 4) * kMRows * 4 + kSoftWarps * 64 * 4;
+    // scales of the weights [2 buffers][terms][128 rows][4 steps], and of V
+    static constexpr int kCarriedOff = kStepMaxOff + 4 * kMRows * 4;  // sums as carried less the sums [4][128]
+    static constexpr int kScaleOff = (kCarriedOff + 4 * kMRows * 4 + 127) / 128 * 128;
+    static constexpr int kScaleBOff = kScaleOff + 2 * kTerms * 512;
+    static constexpr int kZeroOff = kScaleBOff + 1024;  // per V slot: its 16-row groups without a value
+    static constexpr int kEnd = kZeroOff + kSlots * 4;
     static constexpr int kAllocBytes = kEnd + 1024;
     static_assert(kDataEnd >= kMRows * kPartRow, "the rows staged on their way out");
     static_assert(kAllocBytes <= 232448, "shared memory of a CTA");
@@ -247,6 +290,72 @@ __device__ __forceinline__ void two_terms(float v0, float v1, float v2, float v3
         "mov.b32 %1, {l0, l1};\n\t}"
         : "=r"(hi), "=r"(lo)
         : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
+}
+
+// Whether the scales of two groups that share a step differ by more than 2^6 (a
+// NaN does).  A group without a value and with a closer scale costs the other's
+// weights at most six of the 14 binades that are carried to 2^-7; to look at
+// every V tile before its weights costs 3 us at B = 2, P = 30016.
+__device__ __forceinline__ bool scales_apart(float a, float b) { return !(a <= 64.0f * b && b <= 64.0f * a); }
+
+// Two fp32 weights as two bf16 terms each (suffix rows): hi = bf16(w), lo =
+// bf16(w - hi), off by at most 2^-16 of w, whatever its size.
+__device__ __forceinline__ void bf16_terms(uint64_t w, uint32_t &hi, uint32_t &lo)
+{
+    const float2 f = ptx::unpack_f32x2(w);
+    hi = pack_bf16x2(f.x, f.y);
+    const float2 r = ptx::unpack_f32x2(ptx::fma_f32x2(
+        ptx::f32x2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), ptx::f32x2(-1.0f, -1.0f), w));
+    lo = pack_bf16x2(r.x, r.y);
+}
+
+// Four prefix weights, scaled to at most 448, as two 8-bit terms (four codes a
+// word): x = fp16(v), e4m3(x), and the remainder x - e4m3(x), which is exact, times 2^11 in
+// e5m2 (16 * 2^11 at most, and e5m2 goes 2^28 below that).
+__device__ __forceinline__ void weight_terms(float v0, float v1, float v2, float v3, uint32_t &hi, uint32_t &lo)
+{
+    asm("{\n\t.reg .b16 h0, h1, l0, l1;\n\t.reg .b32 x0, x1, b0, b1, s;\n\t"
+        "cvt.rn.f16x2.f32 x0, %3, %2;\n\t"
+        "cvt.rn.f16x2.f32 x1, %5, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h0, x0;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h1, x1;\n\t"
+        "mov.b32 %0, {h0, h1};\n\t"
+        "cvt.rn.f16x2.e4m3x2 b0, h0;\n\t"
+        "cvt.rn.f16x2.e4m3x2 b1, h1;\n\t"
+        "sub.rn.f16x2 x0, x0, b0;\n\t"
+        "sub.rn.f16x2 x1, x1, b1;\n\t"
+        "mov.b32 s, 0x68006800;\n\t"
+        "mul.rn.f16x2 x0, x0, s;\n\t"
+        "mul.rn.f16x2 x1, x1, s;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 l0, x0;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 l1, x1;\n\t"
+        "mov.b32 %1, {l0, l1};\n\t}"
+        : "=r"(hi), "=r"(lo)
+        : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
+}
+
+// What the terms of two such weights are off by.
+__device__ __forceinline__ float2 terms_error(float v0, float v1)
+{
+    float hi0, hi1, lo0, lo1;
+    asm("{\n\t.reg .b16 c, a, b;\n\t.reg .b32 x, y, s;\n\t"
+        "cvt.rn.f16x2.f32 x, %5, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 c, x;\n\t"
+        "cvt.rn.f16x2.e4m3x2 y, c;\n\t"
+        "mov.b32 {a, b}, y;\n\t"
+        "cvt.f32.f16 %0, a;\n\t"
+        "cvt.f32.f16 %1, b;\n\t"
+        "sub.rn.f16x2 x, x, y;\n\t"
+        "mov.b32 s, 0x68006800;\n\t"
+        "mul.rn.f16x2 x, x, s;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 c, x;\n\t"
+        "cvt.rn.f16x2.e5m2x2 y, c;\n\t"
+        "mov.b32 {a, b}, y;\n\t"
+        "cvt.f32.f16 %2, a;\n\t"
+        "cvt.f32.f16 %3, b;\n\t}"
+        : "=f"(hi0), "=f"(hi1), "=f"(lo0), "=f"(lo1)
+        : "f"(v0), "f"(v1));
+    return make_float2(fmaf(lo0, 0x1p-11f, hi0 - v0), fmaf(lo1, 0x1p-11f, hi1 - v1));
 }
 
 // Rewrites n query rows (four chunks of 64 bf16 a row, qpitch bytes apart,
@@ -334,9 +443,9 @@ __device__ __forceinline__ void split_query_rows(uint8_t *q, int qpitch, int n, 
 
 // Joins the `splits` partials of one row, two warps a row (thread col4 of 64
 // owns four columns): with M = max_c m_c and w_c = 2^(m_c - M), out = sum_c w_c
-// O_c / sum_c w_c l_c and lse = (M + log2 sum_c w_c l_c) ln 2.  A partial without
+// O_c / sum_c w_c l'_c and lse = (M + log2 sum_c w_c l_c) ln 2.  A partial without
 // keys (l = 0) has no weight, whatever its O holds.  part(c): the four
-// columns of partial c; state(c): its {m, l}.  Latency is all there is: the
+// columns of partial c; state(c): its {m, l, l'}.  Latency is all there is: the
 // first AHEAD partials are requested before their weights are known.
 template <int AHEAD, class Part, class State>
 __device__ __forceinline__ void join_partials(int splits, Part &&part, State &&state, __nv_bfloat16 *out, float *lse,
@@ -347,26 +456,31 @@ __device__ __forceinline__ void join_partials(int splits, Part &&part, State &&s
 #pragma unroll
     for (int c = 0; c < AHEAD; ++c)
         if (c < splits) o[c] = part(c);
-    float m[2], l[2], M = -INFINITY;
+    float m[2], l[2], lc[2], M = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int c = lane + 32 * h;
-        float2 st = make_float2(-INFINITY, 0.0f);
+        float4 st = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
         if (c < splits) st = state(c);
         m[h] = st.x;
         l[h] = st.y;
+        lc[h] = st.z;
         if (l[h] != 0.0f) M = fmaxf(M, m[h]);
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-    float w[2], total = 0.0f;
+    float w[2], total = 0.0f, carried = 0.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         w[h] = l[h] != 0.0f ? ptx::ex2(m[h] - M) : 0.0f;
         total = fmaf(w[h], l[h], total);
+        carried = fmaf(w[h], lc[h], carried);
     }
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
+    for (int s = 16; s > 0; s >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, s);
+        carried += __shfl_xor_sync(0xffffffffu, carried, s);
+    }
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto add = [&](int c, const float4 &v) {
         const float wc = __shfl_sync(0xffffffffu, c < 32 ? w[0] : w[1], c & 31);
@@ -381,7 +495,7 @@ __device__ __forceinline__ void join_partials(int splits, Part &&part, State &&s
         if (c < splits) add(c, o[c]);
 #pragma unroll 4
     for (int c = AHEAD; c < splits; ++c) add(c, part(c));
-    const float inv = 1.0f / total;
+    const float inv = 1.0f / carried;
     *reinterpret_cast<uint2 *>(out + r * kHeadDim + col4 * 4) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (col4 == 0 && lse != nullptr) lse[r] = (M + ptx::lg2(total)) * 0.69314718055994531f;
@@ -435,6 +549,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         ptx::fence_mbar_init();
     }
+    // scales of 1: V's, and those of the rows' steps that are another copy's
+    for (int i = threadIdx.x; i < (2 * kTerms * 512 + 1024) / 4; i += kThreads8)
+        reinterpret_cast<uint32_t *>(smem + L::kScaleOff)[i] = 0x7f7f7f7fu;
+    ptx::fence_proxy_async_smem();
     if (warp == kLoadWarp && lane == 0) {
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_kp);
@@ -505,7 +623,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
         // weights, this took 1k cycles a tile).  Every tile is passed on, so
         // that no phase of its barrier goes by unseen here.
         uint32_t see_next[4];
+        float vs_next = 1.0f;  // blocks of 16: the scale of group `lane`
+        const float *vsc = p.v_scale + static_cast<size_t>(unit) * p.nblk;
         auto load_next = [&](int t) {
+            vs_next = 1.0f;
+            if (p.shift == 4 && t >= ns && t < T && lane < kTile / 16 && lane * 16 < rows_of(t))
+                vs_next = ptx::load(vsc + row0_of(t) / 16 + lane);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const int c = w * 32 + lane;
@@ -522,6 +645,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 hidden[w] = __ballot_sync(0xffffffffu, see_next[w] == 0u);
                 if (w >= n32 || t < ns) hidden[w] = 0u;
             }
+            const bool apart = __any_sync(0xffffffffu, scales_apart(vs_next, __shfl_xor_sync(0xffffffffu, vs_next, 1)));
             load_next(t + 1);
             if (!warp_wait(&bars[L::kBarVFull + t % kSlots], (t / kSlots) & 1)) {
                 failed = true;
@@ -538,6 +662,23 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     h &= h - 1u;
                     *reinterpret_cast<uint4 *>(vt + (w * 32 + (lane < 16 ? r0 : r1)) * 128) = make_uint4(0u, 0u, 0u, 0u);
                 }
+            }
+            if (apart) {
+                // Groups of 16 keys whose values are all zero: where a step's two
+                // scales are far apart, theirs must not set the step's.
+                __syncwarp();
+                uint32_t zero = 0u;
+                const uint8_t *vg = v_slot(t) + ((lane & 15) >> 3) * (kTile * 128) + (lane & 7) * 16 + (lane >> 4) * 128;
+#pragma unroll 1
+                for (int g = 0; g < 2 * n32; ++g) {
+                    bool any = false;
+                    for (int r = 0; r < 16 && !any; r += 2) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(vg + (g * 16 + r) * 128);
+                        any = __any_sync(0xffffffffu, ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0u);
+                    }
+                    if (!any) zero |= 1u << g;
+                }
+                if (lane == 0) *reinterpret_cast<volatile uint32_t *>(smem + L::kZeroOff + t % kSlots * 4) = zero;
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -573,7 +714,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
         // ================================================== MMA issuer
         if (lane == 0 && T > 0) {
             constexpr uint32_t id_qk = ptx::idesc_e4m3_f32(kMRows, kTile, false);
-            constexpr uint32_t id_pv = ptx::idesc_e4m3_f32(kMRows, kHeadDim, true);
             constexpr uint32_t id_qk16 = ptx::idesc_bf16_f32(kMRows, kSufTile, false);
             constexpr uint32_t id_pv16 = ptx::idesc_bf16_f32(kMRows, kHeadDim, true);
             const uint64_t qdesc = ptx::sw128_desc(ptx::smem_addr(smem), 16, 1024);
@@ -596,20 +736,28 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                     for (int kk = 0; kk < kSufTile / 16; ++kk) {
                         if (kk >= nk) break;
-                        ptx::mma_bf16_ts(tmem + kTmemO8, a + (kk >> 1) * 32 + (kk & 1) * 8,
-                                         vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv16,
-                                         (u > 0 || kk > 0) ? 1u : 0u);
+                        // the weights' first terms, then their second ones
+                        const uint64_t vk = vd + static_cast<uint64_t>((kk * 16 * 128) >> 4);
+                        ptx::mma_bf16_ts(tmem + kTmemO8, a + kk * 16, vk, id_pv16, (u > 0 || kk > 0) ? 1u : 0u);
+                        ptx::mma_bf16_ts(tmem + kTmemO8, a + kk * 16 + 8, vk, id_pv16, 1u);
                     }
                 } else {
                     const uint64_t vd = vdesc0 + slot_off(u);
                     const int nk = (n + 31) / 32;  // 32-row steps that hold rows in range
+                    const uint32_t scales = ptx::smem_addr(smem + L::kScaleOff) + pb * (kTerms * 512);
+#pragma unroll
+                    for (int j = 0; j < kTerms; ++j) ptx::tmem_cp_scales(a + kScaleColsA + j * 4, scales + j * 512);
+                    ptx::tmem_cp_scales(a + kScaleColsB, ptx::smem_addr(smem + L::kScaleBOff));
+                    ptx::tmem_cp_scales(a + kScaleColsB + 4, ptx::smem_addr(smem + L::kScaleBOff) + 512);
 #pragma unroll
                     for (int kk = 0; kk < kTile / 32; ++kk) {
                         if (kk >= nk) break;
                         const uint64_t vk = vd + static_cast<uint64_t>((kk * 32 * 128) >> 4);
-                        const uint32_t ak = a + (kk >> 1) * 64 + (kk & 1) * 16;
-                        ptx::mma_f8_ts(tmem + kTmemO8, ak, vk, id_pv, (u > 0 || kk > 0) ? 1u : 0u);
-                        ptx::mma_f8_ts(tmem + kTmemO8, ak + 8, vk, id_pv, 1u);
+#pragma unroll
+                        for (int j = 0; j < kTerms; ++j)
+                            ptx::mma_mxf8_ts(tmem + kTmemO8, a + kk * kStepCols + j * 8, vk,
+                                             ptx::idesc_mxf8_f32(kMRows, kHeadDim, j > 0, kk), a + kScaleColsA + j * 4,
+                                             a + kScaleColsB, (u > 0 || kk > 0 || j > 0) ? 1u : 0u);
                     }
                 }
                 ptx::mma_commit(&bars[L::kBarVEmpty + s]);
@@ -688,6 +836,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         const float *ksc = p.k_scale + static_cast<size_t>(unit) * p.nblk;
         const float *vsc = p.v_scale + static_cast<size_t>(unit) * p.nblk;
         float *xmax = reinterpret_cast<float *>(smem + L::kXchgOff) + grp * 2 * kMRows;  // [2 halves][128] of this group
+        float *xstep = reinterpret_cast<float *>(smem + L::kStepMaxOff) + grp * 2 * kMRows;
         float *mref = reinterpret_cast<float *>(smem + L::kXchgOff) + 4 * kMRows;        // [2 tile parity][128]
         float *xl = mref + 2 * kMRows;                                                   // [4][128]
         float *lim = xl + 4 * kMRows + warp * 64;  // this warp's columns: +inf visible, -inf hidden
@@ -712,11 +861,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         float m_l = -INFINITY;  // what this thread's sum refers to
         float l = 0.0f;         // its sum of p, in units of 2^m_l
+        // What the steps' largest weights are off by, as carried, in these units: the output
+        // is divided by the sum with them, so that one weight above all others cancels (its error would be
+        // the whole row's, up to 2^-7); the others' differ in sign.
+        float lc = 0.0f;
         // What tile t needs from global memory, one of the group's tiles ahead:
         // the mask bytes of this lane's columns, and (the first lanes) the scales
         // of the thread's 16-column groups (a block never ends inside one).
         uint32_t mask_next[kWords];
         float ks_next, vs_next;
+        constexpr int kScales = R == 4 ? 2 : kGroups;
         auto load_next = [&](int t) {
 #pragma unroll
             for (int w = 0; w < kWords; ++w) mask_next[w] = 1u;
@@ -730,8 +884,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     if (w * 32 + lane < kCols && c < n) mask_next[w] = ptx::load(mask_row + r0 + c);
                 }
             }
-            const int c = col0 + lane * 16;
-            if (lane < kGroups && c < n) {
+            // (R = 4: both groups of the step, of which this thread's is number hf)
+            const int c = (R == 4 ? col0 & ~31 : col0) + lane * 16;
+            if (lane < kScales && c < n) {
                 ks_next = ptx::load(ksc + ((r0 + c) >> p.shift));
                 vs_next = ptx::load(vsc + ((r0 + c) >> p.shift));
             }
@@ -745,10 +900,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
             float ks_cur = ks_next, vs_cur = vs_next;
             load_next(t + 2);
             const int n = rows_of(t);
-            float ag[kGroups], bg[kGroups];
-            float iv = 1.0f;
+            // per 16 keys: what takes a product to log2 units; V's scale, and its logarithm
+            float ag[kGroups], vg[kGroups], bg[kGroups];
             const bool partial = t >= ns && partial_at(t);
             if (t >= ns) {
+                const bool apart = p.shift == 4 && __any_sync(0xffffffffu, scales_apart(vs_cur, __shfl_xor_sync(0xffffffffu, vs_cur, 1)));
                 if (partial) {
                     uint32_t vis[kWords];
 #pragma unroll
@@ -760,14 +916,25 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     __syncwarp();
                     // a group without a visible key may have any scale: it gets 1
                     const uint32_t mine = (lane & 2) ? vis[kWords - 1] : vis[0];
-                    if (((lane & 1) ? mine >> 16 : mine & 0xffffu) == 0u) ks_cur = vs_cur = 1.0f;
+                    if (((R != 4 && (lane & 1)) ? mine >> 16 : mine & 0xffffu) == 0u) ks_cur = vs_cur = 1.0f;
+                }
+                if (apart) {
+                    // a group without a value does not count in its step's scale
+                    if (!warp_wait(&bars[L::kBarClear + t % kSlots], (t / kSlots) & 1)) {
+                        failed = true;
+                        break;
+                    }
+                    const uint32_t zero = *reinterpret_cast<volatile uint32_t *>(smem + L::kZeroOff + t % kSlots * 4);
+                    if (lane < kScales && (zero >> ((R == 4 ? col0 & ~31 : col0) / 16 + lane) & 1u) != 0u)
+                        vs_cur = 0.0f;
                 }
                 const float lv = ptx::lg2(vs_cur);
-                iv = 1.0f / vs_cur;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    ag[g] = __shfl_sync(0xffffffffu, ks_cur, g) * sqs;
-                    bg[g] = __shfl_sync(0xffffffffu, lv, g);
+                    const int from = R == 4 ? hf : g;
+                    ag[g] = __shfl_sync(0xffffffffu, ks_cur, from) * sqs;
+                    vg[g] = __shfl_sync(0xffffffffu, vs_cur, from);
+                    bg[g] = __shfl_sync(0xffffffffu, lv, from);
                 }
             } else if (t > 0) {
                 // the second suffix tile follows the first in one buffer: its
@@ -786,7 +953,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const uint32_t scol = sbuf + (t < ns ? hf * 32 : col0);
             uint32_t raw[2][16];
             float hmax = -INFINITY;
-            // the group's largest exponent (rounding is monotone)
+            float gmax[kGroups];  // per 16 keys: the largest product of q and k
             auto group_max = [&](const uint32_t (&x)[16], int g) {
                 float a = __uint_as_float(x[0]), c = __uint_as_float(x[1]);
 #pragma unroll
@@ -795,7 +962,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     c = ptx::max3(c, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
                 }
                 a = ptx::max3(a, __uint_as_float(x[14]), __uint_as_float(x[15]));
-                return fmaf(fmaxf(a, c), ag[g], bg[g]);
+                gmax[g] = fmaxf(a, c);
+                hmax = fmaxf(hmax, gmax[g] * ag[g]);
             };
             // min(x, -inf) is -inf for any x, NaN included
             auto hide = [&](uint32_t (&x)[16], int c0) {
@@ -820,7 +988,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         if (hf * 32 + c >= n) x = 0xff800000u;
                         hmax = fmaxf(hmax, __uint_as_float(x));
                     }
-                    hmax = fmaf(hmax, p.scale_log2, -kSuffixBits);
+                    hmax *= p.scale_log2;
                 }
             } else if (R == 1) {
                 // 64 columns, 32 at a time: read again below (registers); hidden
@@ -836,7 +1004,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         ptx::tmem_st16(scol + w * 32, raw[0]);
                         ptx::tmem_st16(scol + w * 32 + 16, raw[1]);
                     }
-                    hmax = fmaxf(hmax, fmaxf(group_max(raw[0], (w * 2) % kGroups), group_max(raw[1], (w * 2 + 1) % kGroups)));
+                    group_max(raw[0], (w * 2) % kGroups);
+                    group_max(raw[1], (w * 2 + 1) % kGroups);
                 }
                 if (partial) ptx::tmem_st_wait();
             } else {
@@ -846,11 +1015,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     if (partial) hide(raw[g % 2], g * 16);
-                    hmax = fmaxf(hmax, group_max(raw[g % 2], g));
+                    group_max(raw[g % 2], g);
                 }
             }
             if (!row_valid) hmax = -INFINITY;  // not a query row: never a reason to rescale
             xmax[hf * kMRows + row] = hmax;
+            if (R == 4 && t >= ns) xstep[hf * kMRows + row] = fmaf(gmax[0], ag[0], bg[0]);  // its two halves are a step
             if (!pair_sync()) {
                 failed = true;
                 break;
@@ -867,94 +1037,141 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 }
                 m_old = mref[((t - 1) & 1) * kMRows + row];
             }
-            // weights of this tile are 2^(z + log2 vs - m_used)
-            const bool grow = t == 0 || tmax > m_old + kMaxBits;
-            const float m_used = grow ? tmax - kTopBits : m_old;
+            // weights of this tile are 2^(z - m_used), times vs in the product
+            const bool grow = t == 0 || tmax > m_old + kGrowBits;
+            const float m_used = grow ? tmax : m_old;
             const bool rescale = grow && m_old != -INFINITY;  // (before any weight O is zero)
             if (hf == 0) mref[(t & 1) * kMRows + row] = m_used;
             ptx::mbar_arrive(max_bar);
             if (m_l != m_used) {
-                if (l != 0.0f) l *= ptx::ex2(m_l - m_used);
+                if (l != 0.0f) {
+                    const float f = ptx::ex2(m_l - m_used);
+                    l *= f;
+                    lc *= f;
+                }
                 m_l = m_used;
             }
             const float msub = m_used == -INFINITY ? 0.0f : m_used;
-            // a group's weights: their sum without the scale, and two terms each
-            auto weigh = [&](const uint32_t (&x)[16], int g, uint32_t *hi, uint32_t *lo) {
-                const float cg = bg[g] - msub;
-                const uint64_t a2 = ptx::f32x2(ag[g], ag[g]), c2 = ptx::f32x2(cg, cg);
-                uint64_t l2 = ptx::f32x2(0.0f, 0.0f);
+            // four weights and their sum
+            auto weigh4 = [&](const uint32_t (&x)[16], int e, uint64_t a2, uint64_t c2, uint64_t &l2, uint64_t &w01, uint64_t &w23) {
+                const float2 u = ptx::unpack_f32x2(
+                    ptx::fma_f32x2(ptx::f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), a2, c2));
+                const float2 v = ptx::unpack_f32x2(
+                    ptx::fma_f32x2(ptx::f32x2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), a2, c2));
+                w01 = ptx::f32x2(ptx::ex2(u.x), ptx::ex2(u.y));
+                w23 = ptx::f32x2(ptx::ex2(v.x), ptx::ex2(v.y));
+                l2 = ptx::add_f32x2(ptx::add_f32x2(l2, w01), w23);
+            };
+            const uint64_t c2 = ptx::f32x2(-msub, -msub);
+            // 16 weights of a step, whose products with fv are at most 448
+            auto weigh = [&](const uint32_t (&x)[16], float a, float fv, uint32_t (&w)[kTerms][8], int at) {
+                const uint64_t a2 = ptx::f32x2(a, a), f2 = ptx::f32x2(fv, fv);
+                uint64_t l2 = ptx::f32x2(0.0f, 0.0f), w01, w23;
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float2 u = ptx::unpack_f32x2(ptx::fma_f32x2(
-                        ptx::f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), a2, c2));
-                    const float2 v = ptx::unpack_f32x2(ptx::fma_f32x2(
-                        ptx::f32x2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), a2, c2));
-                    const float w0 = ptx::ex2(u.x), w1 = ptx::ex2(u.y), w2 = ptx::ex2(v.x), w3 = ptx::ex2(v.y);
-                    l2 = ptx::add_f32x2(l2, ptx::f32x2(w0, w1));
-                    l2 = ptx::add_f32x2(l2, ptx::f32x2(w2, w3));
-                    two_terms(w0, w1, w2, w3, hi[e >> 2], lo[e >> 2]);
+                for (int e = 0; e < 4; ++e) {
+                    weigh4(x, 4 * e, a2, c2, l2, w01, w23);
+                    const float2 u = ptx::unpack_f32x2(ptx::mul_f32x2(w01, f2)), v = ptx::unpack_f32x2(ptx::mul_f32x2(w23, f2));
+                    weight_terms(u.x, u.y, v.x, v.y, w[0][at + e], w[1][at + e]);
                 }
                 const float2 lp = ptx::unpack_f32x2(l2);
-                l = fmaf(lp.x + lp.y, __shfl_sync(0xffffffffu, iv, g), l);
+                l += lp.x + lp.y;
             };
+            // A step's scale 2^k, its largest weight times V's scale in (2^-0.2, 2^0.8] of it
+            // (any scale for a row without weight there, or of NaN).
+            auto step_bits = [&](float top) {
+                return __float_as_int(fminf(fmaxf(top - msub, -100.0f), 110.0f) - 0.3f + 12582912.0f) - 0x4b400000;
+            };
+            auto store_scales = [&](int code, int step, auto type) {
+                auto *sc = smem + L::kScaleOff + sb * (kTerms * 512) + ((row & 31) * 4 + (row >> 5)) * 4 + step;
+                using T = decltype(type);
+                constexpr int kOnes = sizeof(T) == 2 ? 0x101 : 1;
+#pragma unroll
+                for (int j = 0; j < kTerms; ++j)
+                    *reinterpret_cast<T *>(sc + j * 512) = static_cast<T>(code - j * kTermBits * kOnes);
+            };
+            // V's scale times 2^(8 - k)  (finite: 0 * inf where the weights are that far below the reference)
+            auto factor_of = [&](int g, int k) { return fminf(vg[g] * __int_as_float((127 + 8 - k) << 23), 3e38f); };
+            // log2 of a group's largest weight times V's scale, but for the reference
+            auto group_top = [&](int g) { return fmaf(gmax[g], ag[g], bg[g]); };
+            // that weight of a step's two groups (the one that sets the step's scale) as carried, and its factor
+            auto largest = [&](int g, int h, bool second, float fg, float fh, float &f) {
+                f = second ? fh : fg;
+                return ptx::ex2(fmaf(second ? gmax[h] : gmax[g], second ? ag[h] : ag[g], -msub)) * f;
+            };
+            // (a group without a value is carried as zero times zero)
+            auto per_factor = [](float e, float f) { return f > 0.0f ? __fdividef(e, f) : 0.0f; };
+            // the thread's steps' largest weights as carried, and their factors
+            float top0 = 0.0f, top1 = 0.0f, f0 = 0.0f, f1 = 0.0f;
             if (t < ns) {
-                uint32_t pk[16];
-                if (R == 1 || copy == 0) {
-                    const uint64_t a2 = ptx::f32x2(p.scale_log2, p.scale_log2), c2 = ptx::f32x2(-msub, -msub);
-                    uint64_t l2 = ptx::f32x2(0.0f, 0.0f);
+                // 16 keys: eight columns of first bf16 terms, eight of second ones
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float2 x = ptx::unpack_f32x2(ptx::fma_f32x2(
-                            ptx::f32x2(__uint_as_float(raw[c >> 4][c & 15]), __uint_as_float(raw[c >> 4][(c & 15) + 1])), a2, c2));
-                        const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
-                        pk[c >> 1] = pack_bf16x2(p0, p1);
-                        l2 = ptx::add_f32x2(l2, ptx::f32x2(p0, p1));
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t pk[16];
+                    if (R == 1 || copy == 0) {
+                        const uint64_t a2 = ptx::f32x2(p.scale_log2, p.scale_log2);
+                        uint64_t l2 = ptx::f32x2(0.0f, 0.0f), w01, w23;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            weigh4(raw[g], 4 * e, a2, c2, l2, w01, w23);
+                            bf16_terms(w01, pk[2 * e], pk[8 + 2 * e]);
+                            bf16_terms(w23, pk[2 * e + 1], pk[8 + 2 * e + 1]);
+                        }
+                        const float2 lp = ptx::unpack_f32x2(l2);
+                        l += lp.x + lp.y;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) pk[c] = 0u;
                     }
-                    const float2 lp = ptx::unpack_f32x2(l2);
-                    l += lp.x + lp.y;
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) pk[c] = 0u;
+                    ptx::tmem_st16(scol + g * 16, pk);
                 }
-                ptx::tmem_st16(scol, pk);
             } else if (R == 1) {
+                constexpr int g1 = 1 % kGroups, g2 = 2 % kGroups, g3 = 3 % kGroups;
+                const float t0 = group_top(0), t1 = group_top(g1), t2 = group_top(g2), t3 = group_top(g3);
+                const int k0 = step_bits(fmaxf(t0, t1)), k1 = step_bits(fmaxf(t2, t3));
+                store_scales((119 + k0) | (119 + k1) << 8, hf * 2, uint16_t());
+                const float fv[4] = {factor_of(0, k0), factor_of(g1, k0), factor_of(g2, k1), factor_of(g3, k1)};
+                top0 = largest(0, g1, t1 > t0, fv[0], fv[1], f0);
+                top1 = largest(g2, g3, t3 > t2, fv[2], fv[3], f1);
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     ptx::tmem_ld16(scol + w * 32, raw[0]);
                     ptx::tmem_ld16(scol + w * 32 + 16, raw[1]);
                     ptx::tmem_ld_wait();
-                    uint32_t hi[8], lo[8];
-                    weigh(raw[0], (w * 2) % kGroups, hi, lo);
-                    weigh(raw[1], (w * 2 + 1) % kGroups, hi + 4, lo + 4);
-                    // in the first 16 columns of the half for its first 32 keys, then
-                    // the next 16: where only this warp's own logits were
-                    ptx::tmem_st8(scol + w * 16, hi);
-                    ptx::tmem_st8(scol + w * 16 + 8, lo);
+                    uint32_t o[kTerms][8];
+                    weigh(raw[0], ag[w == 0 ? 0 : g2], fv[2 * w], o, 0);
+                    weigh(raw[1], ag[w == 0 ? g1 : g3], fv[2 * w + 1], o, 4);
+#pragma unroll
+                    for (int j = 0; j < kTerms; ++j) ptx::tmem_st8(scol + w * kStepCols + j * 8, o[j]);
                 }
             } else {
-                // Both halves hold their logits in registers by now.  A 32-key step
-                // kk has its weights in 16 columns of its own; the other copies'
-                // steps are zero in these rows.
-                const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                auto step = [&](int kk) { return sbuf + (kk >> 1) * 64 + (kk & 1) * 16; };
-                const int kk = col0 >> 5;
-                uint32_t hi[8], lo[8];
-                weigh(raw[0], 0, hi, lo);
+                // Both halves hold their logits in registers by now.  The other
+                // copies' steps weigh zero in these rows.
+                const int own = col0 >> 5;
+                constexpr int g1 = kGroups - 1;
+                uint32_t o[kTerms][8];
+                const float t0 = R == 2 ? group_top(0) : xstep[hf * kMRows + row];
+                const float t1 = R == 2 ? group_top(g1) : xstep[(hf ^ 1) * kMRows + row];
+                const int k0 = step_bits(fmaxf(t0, t1));
+                if (R == 2 || hf == 0) store_scales(119 + k0, own, uint8_t());
+                const float fv0 = factor_of(0, k0), fv1 = factor_of(g1, k0);
+                // (R = 4: the half that holds it counts it)
+                if (R == 2 || t0 > t1 || (t0 == t1 && hf == 0)) top0 = largest(0, g1, R == 2 && t1 > t0, fv0, fv1, f0);
+                weigh(raw[0], ag[0], fv0, o, 0);
                 if (R == 2) {
-                    weigh(raw[1], kGroups - 1, hi + 4, lo + 4);
-                    ptx::tmem_st8(step(kk), hi);
-                    ptx::tmem_st8(step(kk) + 8, lo);
-                    ptx::tmem_st8(step(kk ^ 2), zero);
-                    ptx::tmem_st8(step(kk ^ 2) + 8, zero);
+                    weigh(raw[1], ag[g1], fv1, o, 4);
+#pragma unroll
+                    for (int j = 0; j < kTerms; ++j) ptx::tmem_st8(sbuf + own * kStepCols + j * 8, o[j]);
                 } else {
-                    ptx::tmem_st4(step(kk) + hf * 4, hi);
-                    ptx::tmem_st4(step(kk) + 8 + hf * 4, lo);
-                    const int k1 = (kk + 1 + hf) & 3;
-                    ptx::tmem_st8(step(k1), zero);
-                    ptx::tmem_st8(step(k1) + 8, zero);
-                    ptx::tmem_st8(step((kk + 3) & 3) + hf * 8, zero);
+#pragma unroll
+                    for (int j = 0; j < kTerms; ++j) ptx::tmem_st4(sbuf + own * kStepCols + j * 8 + hf * 4, o[j]);
                 }
+                const uint32_t zero[8] = {};
+#pragma unroll
+                for (int i = 0; i < 4 * kTerms; ++i)
+                    if (i / kTerms / (4 / R) != copy && (i & 1) == hf)
+                        ptx::tmem_st8(sbuf + i / kTerms * kStepCols + i % kTerms * 8, zero);
             }
+            ptx::fence_proxy_async_smem();  // the scales
             if (__any_sync(0xffffffffu, rescale)) {
                 // O holds the sum through PV(t-1) once that PV has completed; PV(t)
                 // waits for this warp's arrival below, so the parity is exact
@@ -965,22 +1182,26 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 ptx::tc_fence_after_sync();
                 const float factor = rescale ? ptx::ex2(m_old - m_used) : 1.0f;  // 0 when m_old is -inf
 #pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t o[4][16];
-                    const uint32_t oc = tmem + lane_base + kTmemO8 + hf * (kHeadDim / 2) + j * 64;
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t o[2][16];
+                    const uint32_t oc = tmem + lane_base + kTmemO8 + hf * (kHeadDim / 2) + j * 32;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) ptx::tmem_ld16(oc + e * 16, o[e]);
+                    for (int e = 0; e < 2; ++e) ptx::tmem_ld16(oc + e * 16, o[e]);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
+                    for (int e = 0; e < 32; ++e)
                         o[e >> 4][e & 15] = __float_as_uint(__uint_as_float(o[e >> 4][e & 15]) * factor);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) ptx::tmem_st16(oc + e * 16, o[e]);
+                    for (int e = 0; e < 2; ++e) ptx::tmem_st16(oc + e * 16, o[e]);
                 }
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before_sync();
             ptx::mbar_arrive(&bars[L::kBarPReady + sb]);
+            if (t >= ns) {
+                const float2 e = terms_error(top0, top1);
+                lc += per_factor(e.x, f0) + per_factor(e.y, f1);
+            }
         }
 
         // The last reference, then the last PV (its barrier's earlier phase is
@@ -992,7 +1213,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
                      !warp_wait(&bars[L::kBarPFree + buffer_of(T - 1, ns)], uses_before(T - 1, ns) & 1);
             ptx::tc_fence_after_sync();
             m_end = mref[((T - 1) & 1) * kMRows + row];
-            if (l != 0.0f && m_l != m_end) l *= ptx::ex2(m_l - m_end);
+            if (l != 0.0f && m_l != m_end) {
+                const float f = ptx::ex2(m_l - m_end);
+                l *= f;
+                lc *= f;
+            }
         }
         if (T == 0) {
             // Q and an early tile still land in the shared memory used below
@@ -1001,13 +1226,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         const bool have_o = T > 0 && !failed;
         // a row's four sums meet; only rows that leave normalised need the total before they are staged
+        float *xc = reinterpret_cast<float *>(smem + L::kCarriedOff);  // [4][128]
         xl[c4 * kMRows + row] = l;
+        xc[c4 * kMRows + row] = lc;
         const bool direct = R == 1 && C == 1;
-        float l_row = 0.0f, inv_l = 0.0f;
+        float l_row = 0.0f, carried = 0.0f, inv_l = 0.0f;
         auto total = [&]() {
             if (!failed && !warp_wait(row_bar, row_phase++ & 1)) failed = true;
             l_row = (xl[row] + xl[kMRows + row]) + (xl[2 * kMRows + row] + xl[3 * kMRows + row]);
-            inv_l = 1.0f / l_row;
+            carried = l_row + ((xc[row] + xc[kMRows + row]) + (xc[2 * kMRows + row] + xc[3 * kMRows + row]));
+            inv_l = 1.0f / carried;
         };
         ptx::mbar_arrive(row_bar);
         if (direct) total();
@@ -1054,7 +1282,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         if (c4 == 0 && row_valid) {
             if (!direct)
                 *reinterpret_cast<float4 *>(smem + srow * kPartRow + kHeadDim * 4) =
-                    make_float4(m_end, have_o && !failed ? l_row : 0.0f, 0.0f, 0.0f);
+                    make_float4(m_end, have_o && !failed ? l_row : 0.0f, carried, 0.0f);
             else if (p.lse != nullptr && !failed)
                 p.lse[static_cast<size_t>(unit) * p.GS + q0 + row] = (m_end + ptx::lg2(l_row)) * 0.69314718055994531f;
         }
@@ -1068,14 +1296,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
             if (!failed) {
                 const int col4 = threadIdx.x & 63;
                 for (int r = threadIdx.x >> 6; r < nr; r += kSoftWarps / 2) {
-                    float2 st[R];
+                    float4 st[R];
                     float M = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < R; ++c) {
-                        st[c] = *reinterpret_cast<const float2 *>(smem + (c * nr + r) * kPartRow + kHeadDim * 4);
+                        st[c] = *reinterpret_cast<const float4 *>(smem + (c * nr + r) * kPartRow + kHeadDim * 4);
                         if (st[c].y != 0.0f) M = fmaxf(M, st[c].x);
                     }
-                    float total = 0.0f;
+                    float total = 0.0f, carried = 0.0f;
                     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int c = 0; c < R; ++c) {
@@ -1083,6 +1311,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         const float4 v = *reinterpret_cast<const float4 *>(smem + (c * nr + r) * kPartRow + col4 * 16);
                         const bool use = w != 0.0f;
                         total = fmaf(w, st[c].y, total);
+                        carried = fmaf(w, st[c].z, carried);
                         acc.x = fmaf(w, use ? v.x : 0.0f, acc.x);
                         acc.y = fmaf(w, use ? v.y : 0.0f, acc.y);
                         acc.z = fmaf(w, use ? v.z : 0.0f, acc.z);
@@ -1090,14 +1319,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                     if (C == 1) {
                         const size_t o = static_cast<size_t>(unit) * p.GS + q0 + r;
-                        const float inv = 1.0f / total;
+                        const float inv = 1.0f / carried;
                         *reinterpret_cast<uint2 *>(p.out + o * kHeadDim + col4 * 4) =
                             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
                         if (col4 == 0 && p.lse != nullptr) p.lse[o] = (M + ptx::lg2(total)) * 0.69314718055994531f;
                     } else {
                         uint8_t *dst = p.part + ((static_cast<size_t>(unit) * C + rank) * p.GS + q0 + r) * kPartRow;
                         *reinterpret_cast<float4 *>(dst + col4 * 16) = acc;
-                        if (col4 == 0) *reinterpret_cast<float4 *>(dst + kHeadDim * 4) = make_float4(M, total, 0.0f, 0.0f);
+                        if (col4 == 0) *reinterpret_cast<float4 *>(dst + kHeadDim * 4) = make_float4(M, total, carried, 0.0f);
                     }
                 }
             }
@@ -1128,8 +1357,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             join_partials<8>(
                 C, [&](int c) { return ptx::ld_dsmem_f32x4(ptx::mapa(at + static_cast<uint32_t>(col4) * 16u, c)); },
                 [&](int c) {
-                    const float4 v = ptx::ld_dsmem_f32x4(ptx::mapa(at + static_cast<uint32_t>(kHeadDim) * 4u, c));
-                    return make_float2(v.x, v.y);
+                    return ptx::ld_dsmem_f32x4(ptx::mapa(at + static_cast<uint32_t>(kHeadDim) * 4u, c));
                 },
                 p.out, p.lse, static_cast<size_t>(unit) * p.GS + q0 + r, col4);
         }
@@ -1164,7 +1392,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeParams p)
     ptx::griddep_wait();
     join_partials<AHEAD>(
         p.splits, [&](int c) { return *reinterpret_cast<const float4 *>(base + c * step + col4 * 16); },
-        [&](int c) { return *reinterpret_cast<const float2 *>(base + c * step + kHeadDim * 4); }, p.out, p.lse,
+        [&](int c) { return *reinterpret_cast<const float4 *>(base + c * step + kHeadDim * 4); }, p.out, p.lse,
         static_cast<size_t>(r), col4);
 }
 

@@ -1,0 +1,179 @@
+"""The suffix attention over an 8-bit cache where its weights and its values
+differ much in size (bounds: kv8_weights_ref)."""
+import pytest
+import torch
+
+import kv8_weights_ref as wr
+import prefix_cache_ref as ref
+from gqa_prefix_suffix_b200 import binding as bd
+
+pytestmark = pytest.mark.gpu
+
+BF, F8, F64 = torch.bfloat16, torch.float8_e4m3fn, torch.float64
+
+
+@pytest.fixture(autouse=True)
+def needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    bd.dm05_set_split_override(0)
+    assert bd.dm05_get_error_word(None) == (0, 0)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def check(q, cache, ks, vs, what, valid=None, mask=None, rms=True):
+    B, P = q.shape[0], cache[0].shape[2]
+    on = bd.Kv8Cache(*[t.cuda() for t in cache[:4]], cache[4])
+    vl = None if valid is None else torch.tensor(valid, dtype=torch.int32).cuda()
+    out, lse = bd.suffix_attn_kv8(q.cuda(), on, ks.cuda(), vs.cuda(), vl, None if mask is None else mask.cuda())
+    vis = ref.visible(valid, mask, B, P)
+    o, l, far, far_l = wr.attention(q, cache, ks, vs, vis)
+    worst, off = wr.off(out.cpu(), o, far)
+    worst_l = ((lse.cpu().to(F64) - l).abs() / far_l).max().item()
+    print(f"[{what}] of the bound {worst:.3f}, rms {off:.2e}, lse {worst_l:.3f}")
+    assert worst <= 1 and worst_l <= 1, (what, worst, worst_l)
+    if rms:
+        assert off <= wr.RMS, (what, off)
+    else:  # values alike: their rounding is not spread evenly
+        plain = wr.off(wr.with_weights(q, cache, ks, vs, vis, wr.bf16_weights), o, far)[1]
+        assert off <= 2 * plain, (what, off, plain)
+    return out, lse
+
+
+@pytest.mark.parametrize("splits", [1, 2, 0])
+@pytest.mark.parametrize("gap", [0.0, 8.0, 10.0, 11.0, 12.0, 14.0, 20.0])
+def test_one_key_far_above_the_others(gap, splits):
+    """9 to 14 nats are a gap that a sink key reaches; every other key's weight counts all the same."""
+    assert bd.dm05_set_split_override(splits) == 0
+    for block, S, at in ((64, 50, 3), (16, 64, 500), (16, 9, 3), (128, 30, 899)):
+        for value in (0.0, 0.02, 1.0):
+            a = wr.sink_inputs(gen(int(gap) * 8 + S), 900, S, gap, value, at, block)
+            check(*a, what=(gap, splits, block, S, value), rms=False)
+
+
+def test_one_key_far_above_a_long_prefix():
+    assert bd.dm05_set_split_override(1) == 0
+    for S in (10, 50):
+        a = wr.sink_inputs(gen(S), 30016, S, 11.0, 0.02, 3, 16)
+        check(*a, what=("long", S), rms=False)
+
+
+def cache_of(g, B, H, P, block, size=1.0, zero=()):
+    """The quantiser's cache of a bf16 prefix whose V has this size; `zero`: rows of V that are all zero."""
+    k, v = torch.randn(B, H, P, 256, generator=g).to(BF), (size * torch.randn(B, H, P, 256, generator=g)).to(BF)
+    for a, b in zero:
+        v[:, :, a:b] = 0
+    c = bd.kv8_quantize(k.cuda(), v.cuda(), block)
+    return tuple(t.cpu() for t in c[:4]) + (block,)
+
+
+def queries(g, B, Hq, H, S, size=1.0):
+    r = lambda h: torch.randn(B, h, S, 256, generator=g)  # noqa: E731
+    return r(Hq).to(BF), r(H).to(BF), (size * r(H)).to(BF)
+
+
+@pytest.mark.parametrize("splits", [1, 0])
+@pytest.mark.parametrize("exp", [0, -3, -6, -8, -10, -12, -40, 30])
+def test_values_of_any_size(exp, splits):
+    """The operator is linear in V: its relative error is the same at every size."""
+    assert bd.dm05_set_split_override(splits) == 0
+    for B, P, S, block in ((1, 900, 50, 64), (1, 512, 1, 64), (3, 300, 7, 16)):
+        g = gen(P + S)
+        c = cache_of(g, B, 4, P, block, 2.0 ** exp)
+        q, ks, vs = queries(g, B, 8, 4, S, 2.0 ** exp)
+        check(q, c, ks, vs, (exp, B, P, S, block))
+
+
+@pytest.mark.parametrize("splits", [1, 0])
+@pytest.mark.parametrize("exp", [0, -3, -8, -12, -40])
+def test_visible_blocks_without_a_value(exp, splits):
+    """Blocks of zeros have scale 1 whatever the size of the others, and take weight without adding to the output."""
+    assert bd.dm05_set_split_override(splits) == 0
+    for P, S, block, zero in ((900, 50, 64, [(128, 192)]), (512, 1, 64, [(0, 64)]), (900, 10, 16, [(16, 32), (400, 496)])):
+        g = gen(P + S)
+        c = cache_of(g, 1, 4, P, block, 2.0 ** exp, zero)
+        assert (c[3][:, :, zero[0][0] // block] == 1).all()
+        q, ks, vs = queries(g, 1, 8, 4, S, 2.0 ** exp)
+        check(q, c, ks, vs, (exp, P, S, block))
+
+
+def test_suffix_and_prefix_values_of_different_size():
+    for e8, e16 in ((-20, 0), (0, -20), (20, 0)):
+        g = gen(e8 + 50)
+        c = cache_of(g, 1, 4, 700, 32, 2.0 ** e8)
+        q, ks, vs = queries(g, 1, 8, 4, 50, 2.0 ** e16)
+        check(q, c, ks, vs, (e8, e16))
+
+
+def test_scales_at_both_ends_of_their_range():
+    """A value's scale does not enter the normaliser: weights of blocks with scale 2^-64 count beside 2^64."""
+    for block, splits in ((16, 1), (64, 1), (16, 0)):
+        assert bd.dm05_set_split_override(splits) == 0
+        g = gen(block)
+        c = cache_of(g, 1, 4, 600, block)
+        c[3][:, :, ::2] = 2.0 ** -64
+        c[3][:, :, 1::2] = 2.0 ** 64
+        q, ks, vs = queries(g, 1, 8, 4, 30)
+        check(q, c, ks, vs, (block, splits))
+
+
+def test_batch_of_masked_samples_with_a_sink():
+    g = gen(9)
+    one = [wr.sink_inputs(g, 1024, 50, 11.0, 0.02, 5, 64, H=4) for _ in range(3)]
+    q, ks, vs = (torch.cat([a[i] for a in one]) for i in (0, 2, 3))
+    c = tuple(torch.cat([a[1][i] for a in one]) for i in range(4)) + (64,)
+    mask = (torch.rand(3, 1024, generator=g) >= 0.1).to(torch.uint8)
+    mask[:, 5] = 1
+    for splits in (1, 0):
+        assert bd.dm05_set_split_override(splits) == 0
+        check(q, c, ks, vs, splits, [1024, 700, 901], mask, rms=False)
+
+
+def test_every_code_reaches_the_output():
+    """With all weight on one prefix row the output is its values: every code but NaN, exactly, and NaN where the code is."""
+    codes = torch.arange(256, dtype=torch.uint8).view(1, 1, 1, 256).expand(1, 1, 40, 256).contiguous()
+    want = codes.view(F8).to(F64)[0, 0, 0]
+    q = torch.zeros(1, 2, 5, 256, dtype=BF)
+    q[..., 0] = 16.0
+    ks = torch.zeros(1, 1, 5, 256, dtype=BF)
+    ks[..., 0] = -1000.0
+    for at in (0, 17, 39):
+        for scale in (1.0, 2.0 ** -64, 1.5, 2.0 ** 40):
+            c = bd.Kv8Cache(torch.zeros(1, 1, 40, 256).to(F8).cuda(), codes.view(F8).cuda(), torch.ones(1, 1, 3).cuda(),
+                            torch.full((1, 1, 3), scale).cuda(), 16)
+            mask = torch.zeros(1, 40, dtype=torch.uint8)
+            mask[0, at] = 1
+            out, lse = bd.suffix_attn_kv8(q.cuda(), c, ks.cuda(), ks.cuda(), None, mask.cuda())
+            got = out.cpu().to(F64)
+            nan = torch.isnan(want)
+            assert torch.equal(torch.isnan(got[0, 1, 4]), nan) and nan.sum() == 2
+            assert (got[..., ~nan] == (want * scale)[~nan]).all()
+            assert (lse == 0).all()
+
+
+def test_a_hidden_rows_codes_are_never_seen_and_a_visible_nan_is():
+    """NaN codes of K and V in hidden rows of every 16-row step, at lengths that end inside one."""
+    for P, valid in ((900, 893), (130, 129), (70, 65), (64, 17)):
+        g = gen(P)
+        c = cache_of(g, 1, 4, P, 16)
+        mask = (torch.rand(1, P, generator=g) >= 0.3).to(torch.uint8)
+        mask[0, 0] = 1
+        vis = ref.visible([valid], mask, 1, P)
+        q, ks, vs = queries(g, 1, 8, 4, 20)
+        good = check(q, c, ks, vs, (P, valid), [valid], mask)
+        bad = tuple(t.clone() for t in c[:4]) + (16,)
+        for x in bad[:2]:
+            x.view(torch.uint8).masked_fill_(~vis[:, None, :, None], 0xFF)
+        got = check(q, bad, ks, vs, (P, valid, "nan"), [valid], mask)
+        assert all(torch.equal(x, y) for x, y in zip(good, got))
+        bad[1].view(torch.uint8)[0, 2, 0, 77] = 0x7F
+        on = bd.Kv8Cache(*[t.cuda() for t in bad[:4]], 16)
+        out, lse = bd.suffix_attn_kv8(q.cuda(), on, ks.cuda(), vs.cuda(), torch.tensor([valid], dtype=torch.int32).cuda(),
+                                      mask.cuda())
+        nan = torch.isnan(out.cpu())
+        assert nan[0, 4:6, :, 77].all() and nan.sum() == 2 * 20
+        assert torch.equal(lse, good[1])
