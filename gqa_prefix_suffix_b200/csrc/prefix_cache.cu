@@ -288,12 +288,6 @@ int mass_call(bool kv8, const void *q, const void *k, const float *k_scale, int 
     return e == cudaSuccess ? DM05_OK : DM05_ERR_CUDA;
 }
 
-bool overlap(const void *a, size_t na, const void *b, size_t nb)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
 int evict_checks(const void *k, const void *v, const float *mass, const int32_t *valid_len, const void *k_out,
                  const void *v_out, const float *mass_out, const int32_t *positions, const int32_t *valid_out, int B,
                  int Hkv, int P, int P_out, int D, int n_keep, int n_first, int n_last)
@@ -309,16 +303,68 @@ int evict_checks(const void *k, const void *v, const float *mass, const int32_t 
     return DM05_OK;
 }
 
-// An eviction in place would write rows that other CTAs have yet to read.
-bool evict_overlaps(int row_bytes, const void *k, const void *v, const float *mass, const void *k_out,
-                    const void *v_out, const float *mass_out, int units, int P, int P_out)
-{
-    const size_t rows = static_cast<size_t>(units) * P, rows_out = static_cast<size_t>(units) * P_out;
-    const size_t in = rows * row_bytes, out = rows_out * row_bytes;
-    return overlap(k, in, k_out, out) || overlap(k, in, v_out, out) || overlap(v, in, k_out, out) ||
-           overlap(v, in, v_out, out) || overlap(k_out, out, v_out, out) ||
-           overlap(mass, rows * 4, mass_out, rows_out * 4);
-}
+struct Range {
+    const void *p;
+    size_t n;
+    bool meets(const Range &o) const
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return p != nullptr && o.p != nullptr && n != 0 && o.n != 0 && a < b + o.n && b < a + n;
+    }
+};
+
+// The arrays of an eviction.  CTAs of a unit, and of a sample's heads, read all
+// of the inputs while others already write: no output may lie on an input, nor
+// on another output.
+struct EvictArrays {
+    Range k, v, k_scale, v_scale, mass, valid_len, mask;
+    Range k_out, v_out, k_scale_out, v_scale_out, mass_out, positions, valid_out;
+
+    // rows of row_bytes; nblk > 0: an 8-bit cache with so many scales a unit
+    EvictArrays(const dm05::cache::EvictParams &ep, int row_bytes, int B, int nblk, int nblk_out)
+    {
+        const size_t units = static_cast<size_t>(B) * ep.s.Hkv, rows = units * ep.s.P, rows_out = units * ep.s.Pout;
+        k = {ep.g.k, rows * row_bytes};
+        v = {ep.g.v, rows * row_bytes};
+        k_scale = {ep.g.k_scale, units * nblk * 4};
+        v_scale = {ep.g.v_scale, units * nblk * 4};
+        mass = {ep.s.mass, rows * 4};
+        valid_len = {ep.s.valid_len, static_cast<size_t>(B) * 4};
+        mask = {ep.s.mask, static_cast<size_t>(B) * ep.s.P};
+        k_out = {ep.g.k_out, rows_out * row_bytes};
+        v_out = {ep.g.v_out, rows_out * row_bytes};
+        k_scale_out = {ep.g.k_scale_out, units * nblk_out * 4};
+        v_scale_out = {ep.g.v_scale_out, units * nblk_out * 4};
+        mass_out = {ep.s.mass_out, rows_out * 4};
+        positions = {ep.s.pos, rows_out * 4};
+        valid_out = {ep.s.valid_out, static_cast<size_t>(B) * 4};
+    }
+
+    // The new cache, its weights and its lengths: known without a device.
+    bool overlap() const
+    {
+        for (const Range &o : {k_out, v_out, mass_out})
+            for (const Range &i : {k, v, k_scale, v_scale, mass, valid_len, mask, positions, valid_out})
+                if (o.meets(i)) return true;
+        for (const Range &o : {positions, valid_out})
+            for (const Range &i : {mass, valid_len, mask})
+                if (o.meets(i)) return true;
+        return k_out.meets(v_out) || k_out.meets(mass_out) || v_out.meets(mass_out);
+    }
+
+    // Every other pair, before the launch.
+    bool overlap_rest() const
+    {
+        const Range outs[] = {k_scale_out, v_scale_out, positions, valid_out, k_out, v_out, mass_out};
+        for (int a = 0; a < 4; ++a) {
+            for (const Range &i : {k, v, k_scale, v_scale, mass, valid_len, mask})
+                if (outs[a].meets(i)) return true;
+            for (int b = a + 1; b < 7; ++b)
+                if (outs[a].meets(outs[b])) return true;
+        }
+        return false;
+    }
+};
 
 // CTAs per unit of the one-kernel eviction: what one wave holds, at most one
 // for each block (8-bit) or eight rows (bf16); 0 where the selection and a
@@ -396,8 +442,8 @@ int run_evict(const dm05::cache::EvictParams &ep, int units, int n_keep, int blo
 }
 
 dm05::cache::SelectParams select_params(const float *mass, const int32_t *valid_len, const uint8_t *mask,
-                                        float *mass_out, int32_t *positions, int32_t *valid_out, uint32_t *err,
-                                        int Hkv, int P, int P_out, int n_keep, int n_first, int n_last)
+                                        float *mass_out, int32_t *positions, int32_t *valid_out, int Hkv, int P,
+                                        int P_out, int n_keep, int n_first, int n_last)
 {
     dm05::cache::SelectParams sp = {};
     sp.mass = mass;
@@ -406,7 +452,6 @@ dm05::cache::SelectParams select_params(const float *mass, const int32_t *valid_
     sp.mass_out = mass_out;
     sp.pos = positions;
     sp.valid_out = valid_out;
-    sp.err = err;
     sp.Hkv = Hkv;
     sp.P = P;
     sp.Pout = P_out;
@@ -583,13 +628,9 @@ int dm05_prefix_evict(const void *k, const void *v, const float *mass, const int
     int rc = evict_checks(k, v, mass, valid_len, k_out, v_out, mass_out, positions, valid_out, B, Hkv, P, P_out, D,
                           n_keep, n_first, n_last);
     if (rc != DM05_OK) return rc;
-    if (evict_overlaps(512, k, v, mass, k_out, v_out, mass_out, B * Hkv, P, P_out)) return DM05_ERR_UNSUPPORTED;
-    Device dev;
-    rc = dm05::internal::device(stream, true, &dev);
-    if (rc != DM05_OK) return rc;
     dm05::cache::EvictParams ep = {};
-    ep.s = select_params(mass, valid_len, mask, mass_out, positions, valid_out, dev.err, Hkv, P, P_out, n_keep,
-                         n_first, n_last);
+    ep.s = select_params(mass, valid_len, mask, mass_out, positions, valid_out, Hkv, P, P_out, n_keep, n_first,
+                         n_last);
     dm05::cache::GatherParams &gp = ep.g;
     gp.k = static_cast<const uint8_t *>(k);
     gp.v = static_cast<const uint8_t *>(v);
@@ -600,6 +641,13 @@ int dm05_prefix_evict(const void *k, const void *v, const float *mass, const int
     gp.P = P;
     gp.Pout = P_out;
     gp.n_keep = n_keep;
+    const EvictArrays arrays(ep, 512, B, 0, 0);
+    if (arrays.overlap()) return DM05_ERR_UNSUPPORTED;
+    Device dev;
+    rc = dm05::internal::device(stream, true, &dev);
+    if (rc != DM05_OK) return rc;
+    if (arrays.overlap_rest()) return DM05_ERR_UNSUPPORTED;
+    ep.s.err = dev.err;
     return run_evict(ep, B * Hkv, n_keep, 0, dev.num_sms, stream);
 }
 
@@ -617,13 +665,9 @@ int dm05_prefix_evict_kv8(const void *k8, const void *v8, const float *k_scale, 
     if (shift < 0) return DM05_ERR_UNSUPPORTED;
     if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(k_scale_out, 4) || !aligned(v_scale_out, 4))
         return DM05_ERR_ALIGN;
-    if (evict_overlaps(256, k8, v8, mass, k8_out, v8_out, mass_out, B * Hkv, P, P_out)) return DM05_ERR_UNSUPPORTED;
-    Device dev;
-    rc = dm05::internal::device(stream, true, &dev);
-    if (rc != DM05_OK) return rc;
     dm05::cache::EvictParams ep = {};
-    ep.s = select_params(mass, valid_len, mask, mass_out, positions, valid_out, dev.err, Hkv, P, P_out, n_keep,
-                         n_first, n_last);
+    ep.s = select_params(mass, valid_len, mask, mass_out, positions, valid_out, Hkv, P, P_out, n_keep, n_first,
+                         n_last);
     dm05::cache::GatherParams &gp = ep.g;
     gp.k = static_cast<const uint8_t *>(k8);
     gp.v = static_cast<const uint8_t *>(v8);
@@ -641,6 +685,13 @@ int dm05_prefix_evict_kv8(const void *k8, const void *v8, const float *k_scale, 
     gp.nblk = blocks_of(P, shift);
     gp.nblk_out = blocks_of(P_out, shift);
     gp.shift = shift;
+    const EvictArrays arrays(ep, 256, B, gp.nblk, gp.nblk_out);
+    if (arrays.overlap()) return DM05_ERR_UNSUPPORTED;
+    Device dev;
+    rc = dm05::internal::device(stream, true, &dev);
+    if (rc != DM05_OK) return rc;
+    if (arrays.overlap_rest()) return DM05_ERR_UNSUPPORTED;
+    ep.s.err = dev.err;
     return run_evict(ep, B * Hkv, n_keep, block, dev.num_sms, stream);
 }
 

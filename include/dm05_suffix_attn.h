@@ -436,8 +436,9 @@ int dm05_prefix_attn_mass_kv8(const void *q, const void *k8, const float *k_scal
  *   positions  int32 [B, Hkv, P_out]: where each row came from, then -1
  *   valid_out  int32 [B]: n, the valid length of the new cache
  * Every position of the new cache below valid_out is visible, so no mask
- * goes with it.  n_keep may be 0.  A new cache (or its mass) that overlaps
- * the old one is refused with DM05_ERR_UNSUPPORTED.
+ * goes with it.  n_keep may be 0.  An output that overlaps an input or
+ * another output is refused with DM05_ERR_UNSUPPORTED: in place there is
+ * neither an eviction nor an update of the valid lengths.
  * dm05_prefix_evict_kv8 does the same on an 8-bit cache: the kept rows form
  * new blocks, whose scales follow dm05_kv8_quantize's rule over the values
  * scale * code, and are rounded to them (scales of blocks without a kept row
