@@ -1,10 +1,13 @@
-"""Builds the C-ABI shared library libdm05_suffix_attn.so in-tree (sm_100a), and
-the Python module _torch_front.so, the torch front end of the prefix-cache
-operators (host code)."""
+"""Builds the C-ABI shared library libdm05_suffix_attn.so in-tree (sm_100a), which
+needs nvcc alone, and where torch and Python's headers are installed the Python
+module _torch_front.so, the torch front end of the prefix-cache operators (host
+code)."""
 from __future__ import annotations
 
 import os
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -37,32 +40,43 @@ def nvcc() -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile when the library is missing or older than a source file (the
-    front end with it)."""
-    build_front(force)
-    if not force and os.path.exists(LIB):
-        t = os.path.getmtime(LIB)
-        if all(os.path.getmtime(d) <= t for d in deps()):
-            return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *SOURCES]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    """Compile what is missing or older than a source file; the path of the library."""
+    if force or not _fresh(LIB, deps()):
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *SOURCES]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+            print(" ".join(cmd))
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
+    why = front_unavailable()
+    if why is None:
+        build_front(force)
+    else:
+        print(f"the torch front end is not built: {why}", file=sys.stderr)
     return LIB
+
+
+def _fresh(path: str, sources: list) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in sources)
+
+
+def front_unavailable():
+    """Why the torch front end cannot be built on this machine, or None."""
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h is not installed"
+    return None
 
 
 def build_front(force: bool = False) -> str:
     """Compile the torch front end when it is missing or older than its sources."""
     sources = [FRONT_SOURCE, os.path.join(ROOT, "include", "dm05_suffix_attn.h")]
-    if not force and os.path.exists(FRONT):
-        t = os.path.getmtime(FRONT)
-        if all(os.path.getmtime(d) <= t for d in sources):
-            return FRONT
-    import sysconfig
-
+    if not force and _fresh(FRONT, sources):
+        return FRONT
     import torch
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
@@ -78,5 +92,4 @@ def build_front(force: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     build(force="--force" in sys.argv, verbose=True)
