@@ -18,7 +18,6 @@ from typing import NamedTuple, Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdm05_suffix_attn.so")
-FRONT_PATH = os.path.join(_HERE, "_torch_front.so")
 
 DM05_OK = 0
 DM05_ERR_NULL = -1
@@ -558,13 +557,14 @@ def _load_front():
     """The compiled torch front end (csrc/torch_front.cpp), bound to the
     loaded library; raises if it has not been built."""
     global _front
+    from .build import front_path
     L = lib()
-    import torch  # noqa: F401  (the module's symbols come from it)
+    path = front_path()  # imports torch, which the module's symbols come from
     with _lock:
         if _front is None:
-            if not os.path.exists(FRONT_PATH):
-                raise RuntimeError(f"{FRONT_PATH} is missing: build it with `python -m gqa_prefix_suffix_b200.build`")
-            loader = importlib.machinery.ExtensionFileLoader("_torch_front", FRONT_PATH)
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: build it with `python -m gqa_prefix_suffix_b200.build`")
+            loader = importlib.machinery.ExtensionFileLoader("_torch_front", path)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_torch_front", loader))
             loader.exec_module(m)
             m.bind(Dm05Error, *[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (

@@ -1,6 +1,6 @@
 """Builds the C-ABI shared library libdm05_suffix_attn.so in-tree (sm_100a), which
 needs nvcc alone, and where torch and Python's headers are installed the Python
-module _torch_front.so, the torch front end of the prefix-cache operators (host
+module _torch_front, the torch front end of the prefix-cache operators (host
 code)."""
 from __future__ import annotations
 
@@ -30,13 +30,20 @@ NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", 
               "-Xcompiler", "-fPIC", "-shared"]
 
 
-FRONT = os.path.join(HERE, "_torch_front.so")
 FRONT_SOURCE = os.path.join(HERE, "csrc", "torch_front.cpp")
 
 
 def nvcc() -> str:
     cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
+
+
+def front_path() -> str:
+    """Where the torch front end is built and loaded: it is C++ against this
+    interpreter's and this torch's binary interface, whose versions its name
+    carries, so that one built against others is never loaded."""
+    import torch
+    return os.path.join(HERE, f"_torch_front.{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}.so")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -73,22 +80,24 @@ def front_unavailable():
 
 
 def build_front(force: bool = False) -> str:
-    """Compile the torch front end when it is missing or older than its sources."""
+    """Compile the torch front end when it is missing or older than its sources;
+    the path of this interpreter's and this torch's."""
+    front = front_path()
     sources = [FRONT_SOURCE, os.path.join(ROOT, "include", "dm05_suffix_attn.h")]
-    if not force and _fresh(FRONT, sources):
-        return FRONT
+    if not force and _fresh(front, sources):
+        return front
     import torch
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
-    tmp = FRONT + f".tmp{os.getpid()}"
+    tmp = front + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[f"-I{d}" for d in include], FRONT_SOURCE, "-o", tmp, "-L" + os.path.join(home, "lib"), "-lc10",
            "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     subprocess.run(cmd, check=True)
-    os.replace(tmp, FRONT)
-    return FRONT
+    os.replace(tmp, front)
+    return front
 
 
 if __name__ == "__main__":

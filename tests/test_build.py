@@ -19,7 +19,8 @@ def compiled(monkeypatch, tmp_path):
         out.append(os.path.basename(path).split(".tmp")[0])
     monkeypatch.setattr(b.subprocess, "run", run)
     monkeypatch.setattr(b, "LIB", str(tmp_path / os.path.basename(b.LIB)))
-    monkeypatch.setattr(b, "FRONT", str(tmp_path / os.path.basename(b.FRONT)))
+    front = b.front_path
+    monkeypatch.setattr(b, "front_path", lambda: str(tmp_path / os.path.basename(front())))
     return out
 
 
@@ -47,3 +48,25 @@ def test_both_are_built_where_both_can_be(compiled):
     assert len(compiled) == 2
     b.build(force=True)
     assert len(compiled) == 4
+
+
+def test_a_front_end_of_another_torch_is_not_loaded(compiled, monkeypatch):
+    torch = pytest.importorskip("torch")
+    from gqa_prefix_suffix_b200 import binding as bd
+    b.build()
+    here = b.front_path()
+    assert os.path.exists(here)
+    monkeypatch.setattr(bd, "_front", None)
+    monkeypatch.setattr(bd, "lib", lambda: None)
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    assert b.front_path() != here
+    with pytest.raises(RuntimeError, match="9.9.9.*missing"):
+        bd._load_front()
+    assert not b._fresh(b.front_path(), [])
+
+
+def test_a_front_end_of_another_interpreter_is_not_loaded(monkeypatch):
+    pytest.importorskip("torch")
+    here = b.front_path()
+    monkeypatch.setattr(b.sysconfig, "get_config_var", lambda name: "cpython-399")
+    assert b.front_path() != here
