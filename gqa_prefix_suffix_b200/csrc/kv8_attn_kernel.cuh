@@ -53,21 +53,22 @@
 // the 128 rows of the MMA, and copy r of a row weighs only the r-th part of
 // every tile's keys (its other weights are zeros): the exponentials, which
 // every one of 128 rows would otherwise do for every key, are dealt to all
-// warps, at the price of joining R partial rows at the end.  (P = 30016, S =
-// 10: 37 instead of 42 us; with runs under four tiles the joining costs more.)
+// warps, at the price of joining R partial rows at the end.  (B = 2, P = 30016, S
+// = 10: 37.6 instead of 43.3 us; with runs under four tiles the joining costs more.)
 //
 // A unit's tiles may be split over any number of CTAs (and its query rows
 // over blocks, so that a CTA writes fewer partial rows).  Each has its
-// unnormalised O with {m, l} per row.  Few splits form a cluster whose CTAs
+// unnormalised O with {m, l, l'} per row, l' being
+// the sum that divides the output.  Few splits form a cluster whose CTAs
 // read one another's partial rows from shared memory (CL); else the rows go to
 // the workspace and merge_kernel, launched behind, joins them.  (Clusters alone
 // would limit a unit to 16 CTAs and the grid to what clusters leave resident:
-// 68 instead of 42 us at B = 2, P = 30016.)
+// 68 instead of 42 us at B = 2, P = 30016, before rows were copied.)
 //
 // Times a call (device, Hq = 8 over Hkv = 4): one token, P = 576: 8.7 us; S = 50,
 // P = 1024: 12.5 us; B = 32, masked: 30.6 us, bound by a tile's chain of logits,
 // maximum, weights and product (4.2k cycles, two tiles at a time); B = 2, P =
-// 30016, S = 10: 40 us.
+// 30016, S = 10: 37.6 us in blocks of 64, 39.7 in blocks of 16.
 #pragma once
 
 #include "prefix_cache_kernels.cuh"

@@ -145,16 +145,18 @@ struct Kv8Plan {
 // short as one wave allows; unsplit while that is as short.  A split unit's
 // query rows are cut into blocks while SMs are left (at least 32 rows each):
 // every CTA then prepares, stages and writes fewer rows, for K and V tiles read
-// from L2 once more (B = 1, P = 1024, S = 50: 12.7 instead of 13.3 us).  Few
-// rows are copied over the MMA's when a CTA walks at least four tiles.
+// from L2 once more (B = 1, P = 1024, S = 64: 12.6 instead of 14.4 us; B = 2, S = 50:
+// 13.5 instead of 14.9).  Few rows are copied over the MMA's when a CTA walks at least
+// four tiles (B = 2, P = 30016: S = 10 37.6 instead of 43.3 us, S = 30 44.0 instead of
+// 45.4; always: B = 1, P = 1024, S = 64 13.4 instead of 12.6).
 //
 // Splits that fit a cluster join their rows inside it as long as all clusters
-// run at once (B = 1, P = 576, S = 1: 8.7 instead of 9.5 us with a second
-// kernel, P = 1024, S = 50: 12.0 instead of 12.5; B = 2, P = 1024, S = 32 in
-// clusters that do not: 21.0 instead of 12.3), for which the rows may be cut into
-// fewer blocks, and the partial rows of a cluster are few (B = 2, P = 576, S =
-// 50, 6 x 56 rows: 12.2 instead of 13.2; P = 1024, 9 x 104 rows: 16.3 instead of
-// 13.1).  Call after set_attributes(dev, false).
+// run at once (for which the rows may be cut into fewer blocks) and the partial
+// rows of a cluster are few.  In a cluster / with a second kernel (us, splits x
+// rows): B = 1, P = 576, S = 1, 6 x 8: 8.7 / 9.7; B = 1, P = 1024: S = 10, 9 x 24: 10.0 / 10.3;
+// S = 50, 9 x 40: 12.4 / 13.1; S = 25, 9 x 56: 12.1 / 11.4; S = 64, 9 x 48: 12.9 / 12.6; B = 2, P = 576,
+// S = 50, 6 x 56: 12.8 / 13.6; B = 2, P = 1024: S = 16, 9 x 32: 11.4 / 11.8; S = 32, 9 x 64:
+// 13.6 / 12.6; S = 50, 9 x 104: 17.0 / 13.5.  Call after set_attributes(dev, false).
 Kv8Plan kv8_plan(int B, int Hq, int Hkv, int P, int S, const Device &dev)
 {
     const long long units = static_cast<long long>(B) * Hkv;
