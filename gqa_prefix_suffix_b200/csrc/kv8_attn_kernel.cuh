@@ -66,8 +66,8 @@
 // 68 instead of 42 us at B = 2, P = 30016, before rows were copied.)
 //
 // Times a call (device, Hq = 8 over Hkv = 4): one token, P = 576: 8.7 us; S = 50,
-// P = 1024: 12.5 us; B = 32, masked: 30.6 us, bound by a tile's chain of logits,
-// maximum, weights and product (4.2k cycles, two tiles at a time); B = 2, P =
+// P = 1024: 12.5 us; B = 32, masked: 29.2 us, bound by a tile's chain of logits,
+// maximum, weights and product (4.1k cycles, two tiles at a time); B = 2, P =
 // 30016, S = 10: 37.6 us in blocks of 64, 39.7 in blocks of 16.
 #pragma once
 
@@ -1133,14 +1133,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const float fv[4] = {factor_of(0, k0), factor_of(g1, k0), factor_of(g2, k1), factor_of(g3, k1)};
                 top0 = largest(0, g1, t1 > t0, fv[0], fv[1], f0);
                 top1 = largest(g2, g3, t3 > t2, fv[2], fv[3], f1);
-#pragma unroll
+                // not unrolled: less code to fetch (stalls on it 2.3 -> 2.0 warps an issue)
+                // and no spills; B = 32 30.4 -> 29.2 us
+#pragma unroll 1
                 for (int w = 0; w < 2; ++w) {
                     ptx::tmem_ld16(scol + w * 32, raw[0]);
                     ptx::tmem_ld16(scol + w * 32 + 16, raw[1]);
                     ptx::tmem_ld_wait();
                     uint32_t o[kTerms][8];
-                    weigh(raw[0], ag[w == 0 ? 0 : g2], fv[2 * w], o, 0);
-                    weigh(raw[1], ag[w == 0 ? g1 : g3], fv[2 * w + 1], o, 4);
+                    weigh(raw[0], w == 0 ? ag[0] : ag[g2], w == 0 ? fv[0] : fv[2], o, 0);
+                    weigh(raw[1], w == 0 ? ag[g1] : ag[g3], w == 0 ? fv[1] : fv[3], o, 4);
 #pragma unroll
                     for (int j = 0; j < kTerms; ++j) ptx::tmem_st8(scol + w * kStepCols + j * 8, o[j]);
                 }
