@@ -310,7 +310,9 @@ __device__ __forceinline__ int warp_scan_table(int *table, int n)
 //
 // KPT > 0: P <= KPT * 1024 and every thread keeps its keys in registers (the
 // weights are read once).  KPT == 0: any P; the keys are formed again in
-// every pass, and the positions are found 1024 at a time.
+// every pass, and the positions are found 1024 at a time.  Weights (or a
+// length) that someone changes meanwhile make its passes disagree: what is kept is
+// then anything, but positions stay inside the prefix and their number inside the new cache.
 constexpr int kSelectThreads = 1024;
 
 template <int KPT>
@@ -318,7 +320,7 @@ struct SelectShared {
     static constexpr int kKeys = KPT > 0 ? KPT : 1;
     int hist[4][256];
     int table[kKeys * 32 + 1];
-    int seen, pick[4][3];
+    int seen, pick[4][3], len;
 };
 
 template <int KPT, class Emit>
@@ -349,7 +351,12 @@ __device__ __forceinline__ int select_positions(const SelectParams &p, int unit,
             shown[i] = j < p.P && (mask == nullptr || mask[j] != 0);
         }
     }
-    const int vl = clamped_len(p.valid_len, b, p.P, p.err, threadIdx.x == 0 && blockIdx.x == 0 && unit % p.Hkv == 0);
+    int vl = clamped_len(p.valid_len, b, p.P, p.err, threadIdx.x == 0 && blockIdx.x == 0 && unit % p.Hkv == 0);
+    if (KPT == 0) {  // one length for all, whatever happens to it
+        if (threadIdx.x == 0) sh.len = vl;
+        __syncthreads();
+        vl = sh.len;
+    }
     const int rounds = KPT > 0 ? KPT : (vl + kSelectThreads - 1) / kSelectThreads;
     uint32_t keys[kKeys];
     auto key_of = [&](int i) -> uint32_t {
@@ -472,10 +479,11 @@ __device__ __forceinline__ int select_positions(const SelectParams &p, int unit,
                 if (m >> lane & 1u) {
                     const int at = base + table[warp] + __popc(m & ((1u << lane) - 1u));
                     const int j = i * kSelectThreads + threadIdx.x;
-                    emit(keep, at, j, mass[j]);
+                    if (at < keep) emit(keep, at, j, mass[j]);
                 }
                 base += table[32];
             }
+            return min(keep, base);
         }
     }
     return keep;
