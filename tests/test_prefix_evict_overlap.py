@@ -81,18 +81,18 @@ def test_calls_in_place_are_refused_and_change_nothing():
     before = [t.clone() for t in (m, n, c.k_scale, c.v_scale)]
     pos = torch.empty(3, 4, 128, dtype=torch.int32, device="cuda")
     codes = c.k.view(torch.uint8).view(-1)
-    for kw in (dict(valid_len=n), dict(positions=m.view(torch.int32).view(-1)[:1536].view(3, 4, 128)),
+    for kw in (dict(valid_len=n), dict(positions=m.view(torch.int32).view(-1)[:pos.numel()].view(3, 4, 128)),
                dict(mass_out=pos.view(torch.float32), positions=pos),
                dict(out=out._replace(k_scale=c.k_scale.view(-1)[:24].view(3, 4, 2))),
                dict(out=out._replace(v_scale=c.v_scale.view(-1)[8:32].view(3, 4, 2))),
                dict(out=out._replace(v_scale=c.k_scale.view(-1)[:24].view(3, 4, 2))),
                dict(out=out._replace(v_scale=out.k_scale)),
-               dict(positions=codes[:6144].view(torch.int32).view(3, 4, 128)),
+               dict(positions=codes[:4 * pos.numel()].view(torch.int32).view(3, 4, 128)),
                dict(valid_len=codes[:12].view(torch.int32)),
                dict(positions=pos, valid_len=pos.view(-1)[:3])):
         with pytest.raises(bd.Dm05Error):
             bd.prefix_evict_kv8(c, m, 100, prefix_valid_len=n, **dict(dict(out=out), **kw))
-    for kw in (dict(valid_len=n), dict(positions=k.view(-1)[:3072].view(torch.int32).view(3, 4, 128)),
+    for kw in (dict(valid_len=n), dict(positions=k.view(-1)[:2 * pos.numel()].view(torch.int32).view(3, 4, 128)),
                dict(positions=pos, valid_len=pos.view(-1)[5:8])):
         with pytest.raises(bd.Dm05Error):
             bd.prefix_evict(k, v, m, 100, prefix_valid_len=n, bucket=128, **kw)
