@@ -904,8 +904,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
             // per 16 keys: what takes a product to log2 units; V's scale, and its logarithm
             float ag[kGroups], vg[kGroups], bg[kGroups];
             const bool partial = t >= ns && partial_at(t);
+            bool apart = false;
             if (t >= ns) {
-                const bool apart = p.shift == 4 && __any_sync(0xffffffffu, scales_apart(vs_cur, __shfl_xor_sync(0xffffffffu, vs_cur, 1)));
+                apart = p.shift == 4 &&
+                        __any_sync(0xffffffffu, scales_apart(vs_cur, __shfl_xor_sync(0xffffffffu, vs_cur, 1)));
                 if (partial) {
                     uint32_t vis[kWords];
 #pragma unroll
@@ -918,16 +920,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     // a group without a visible key may have any scale: it gets 1
                     const uint32_t mine = (lane & 2) ? vis[kWords - 1] : vis[0];
                     if (((R != 4 && (lane & 1)) ? mine >> 16 : mine & 0xffffu) == 0u) ks_cur = vs_cur = 1.0f;
-                }
-                if (apart) {
-                    // a group without a value does not count in its step's scale
-                    if (!warp_wait(&bars[L::kBarClear + t % kSlots], (t / kSlots) & 1)) {
-                        failed = true;
-                        break;
-                    }
-                    const uint32_t zero = *reinterpret_cast<volatile uint32_t *>(smem + L::kZeroOff + t % kSlots * 4);
-                    if (lane < kScales && (zero >> ((R == 4 ? col0 & ~31 : col0) / 16 + lane) & 1u) != 0u)
-                        vs_cur = 0.0f;
                 }
                 const float lv = ptx::lg2(vs_cur);
 #pragma unroll
@@ -948,6 +940,23 @@ __global__ void __launch_bounds__(kThreads8, 1)
             if (!warp_wait(&bars[L::kBarSFull + sb], before & 1)) {
                 failed = true;
                 break;
+            }
+            if (apart) {
+                // A group without a value does not count in its step's scale.  (S(t)
+                // exists, so PV(t - 2) has run, and the phase of the tile before in this
+                // slot is past.)
+                if (!warp_wait(&bars[L::kBarClear + t % kSlots], (t / kSlots) & 1)) {
+                    failed = true;
+                    break;
+                }
+                const uint32_t zero = *reinterpret_cast<volatile uint32_t *>(smem + L::kZeroOff + t % kSlots * 4);
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    if (zero >> (col0 / 16 + g) & 1u) {
+                        vg[g] = 0.0f;
+                        bg[g] = -INFINITY;
+                    }
+                }
             }
             ptx::tc_fence_after_sync();
             const uint32_t sbuf = tmem + lane_base + kTmemS8 + sb * kTile;

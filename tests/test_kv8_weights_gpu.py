@@ -195,3 +195,48 @@ def test_as_far_from_the_bf16_call_as_the_two_are_from_the_sum(splits):
     print(f"rms {off:.2e}")
     assert off <= 3.6e-3
     assert (la - lb).abs().max() <= 1e-3
+
+
+@pytest.mark.parametrize("S", [3, 10, 25, 50])
+@pytest.mark.parametrize("splits", [1, 2, 0])
+def test_blocks_of_sixteen_beside_blocks_without_a_value(S, splits):
+    """Rows laid once, twice and four times over the MMA's; blocks whose only values are hidden, hidden
+    blocks with any scale, and rows of zeros that draw the weight."""
+    assert bd.dm05_set_split_override(splits) == 0
+    g = gen(S)
+    P, valid = 900, 889
+    c = cache_of(g, 1, 4, P, 16, 2.0 ** -30)
+    k8, v8, sk, sv = (t.clone() for t in c[:4])
+    q, ks, vs = queries(g, 1, 8, 4, S, 2.0 ** -30)
+    mask = (torch.rand(1, P, generator=g) >= 0.2).to(torch.uint8)
+    mask[0, ::16] = 1
+    for b in (0, 3, 8, 9, 30, 41, 55):                     # both places of a step, a whole step, the last block
+        v8.view(torch.uint8)[:, :, b * 16:(b + 1) * 16] = 0x80 if b & 1 else 0
+        sv[:, :, b] = 1.0
+    k8.view(torch.uint8)[:, :, 130:140] = 0x50            # large keys in rows of zeros
+    v8.view(torch.uint8)[:, :, 48:52] = 0x40              # values that are hidden
+    mask[0, 48:52] = 0
+    mask[0, 52:64] = 1
+    mask[0, 320:336] = mask[0, 560:576] = 0                # hidden blocks beside visible ones
+    for s in (sk, sv):
+        s[:, :, 20] = float("nan")
+        s[:, :, 35] = 2.0 ** 60
+    for x in (k8, v8):
+        x.view(torch.uint8)[:, :, 320:336] = 0x7F
+    check(q, (k8, v8, sk.nan_to_num(1.0), sv.nan_to_num(1.0), 16), ks, vs, (S, splits, "numbers"), [valid], mask)
+    on = bd.Kv8Cache(k8.cuda(), v8.cuda(), sk.cuda(), sv.cuda(), 16)
+    n = torch.tensor([valid], dtype=torch.int32).cuda()
+    a = bd.suffix_attn_kv8(q.cuda(), on, ks.cuda(), vs.cuda(), n, mask.cuda())
+    b = bd.suffix_attn_kv8(q.cuda(), on._replace(k_scale=sk.nan_to_num(1.0).cuda(), v_scale=sv.nan_to_num(1.0).cuda()),
+                           ks.cuda(), vs.cuda(), n, mask.cuda())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and not torch.isnan(a[0]).any()
+
+
+def test_a_block_of_zeros_with_a_close_scale():
+    """Its scale is within 2^6 of the other's in its step: six binades of the fourteen that are carried to 2^-7."""
+    for S, splits in ((10, 1), (30, 1), (50, 1), (50, 0)):
+        assert bd.dm05_set_split_override(splits) == 0
+        g = gen(S)
+        c = cache_of(g, 1, 4, 900, 16, 0.3, [(32, 48), (400, 416)])
+        q, ks, vs = queries(g, 1, 8, 4, S, 0.3)
+        check(q, c, ks, vs, (S, splits))
