@@ -66,9 +66,9 @@
 // 68 instead of 42 us at B = 2, P = 30016, before rows were copied.)
 //
 // Times a call (device, Hq = 8 over Hkv = 4): one token, P = 576: 8.8 us; S = 50,
-// P = 1024: 12.5 us; B = 32, masked: 29.2 us, bound by a tile's chain of logits,
+// P = 1024: 12.6 us; B = 32, masked: 29.7 us, bound by a tile's chain of logits,
 // maximum, weights and product (4.1k cycles, two tiles at a time); B = 2, P =
-// 30016, S = 10: 37.6 us in blocks of 64, 39.7 in blocks of 16.
+// 30016, S = 10: 37.6 us in blocks of 64, 40.0 in blocks of 16.
 #pragma once
 
 #include "prefix_cache_kernels.cuh"
